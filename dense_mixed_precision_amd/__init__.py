@@ -33,6 +33,20 @@ beside the product by ``load_timeline()``: mpgemm_f16f32 plus
 mpgemm_timeline_entries(), mpgemm_timeline_read(out, entries) and
 mpgemm_timeline_clear() -- per-workgroup stamps of the pipelined kernel.
 
+Operators beside the GEMM (libmpgemm_ops.so, include/mpgemm_ops.h): raw entry
+points mpgemm_quantize_rows, mpgemm_i8_gemm, mpgemm_route_workspace,
+mpgemm_route, mpgemm_gather_rows, mpgemm_combine_rows,
+mpgemm_combine_rows_backward, mpgemm_grouped and mpgemm_grouped_wgrad, and
+for torch tensors
+    quantize_rows(X, Q, scale, order, top_k)      rows to 8-bit codes
+    gemm_i8(A, B, C, scale_a, scale_b, bias, offsets)   their product
+    route(experts, num_experts) -> order, position, offsets
+    gather_rows(X, order, Y, top_k)               tokens into expert order
+    gemm_grouped(A, B, C, offsets, alpha, beta)   each expert's rows times its matrix
+    gemm_grouped_wgrad(A, B, C, offsets, alpha, beta)   gradient by the matrices
+    combine_rows(Y, position, out, weights)       back to tokens, weighted
+    combine_rows_backward(dout, Y, position, weights, dY, dweights)
+
 Tensor convenience: ``gemm(A, B, C, alpha, beta)`` for torch tensors on the
 GPU (A, B both float16 or both bfloat16, each row- or column-major, e.g. a
 transposed view; C float32 row-major), launched on torch's current stream.
@@ -95,4 +109,32 @@ from ._binding import (  # noqa: F401
     mpgemm_strerror,
     mpgemm_version,
     query_for,
+)
+from ._ops import (  # noqa: F401
+    MPGEMM_I8_MAX_K,
+    MPGEMM_ID_I32,
+    MPGEMM_ID_I64,
+    MPGEMM_MAX_GROUPS,
+    MPGEMM_T_BF16,
+    MPGEMM_T_F16,
+    MPGEMM_T_F32,
+    OPS_PATH,
+    combine_rows,
+    combine_rows_backward,
+    gather_rows,
+    gemm_grouped,
+    gemm_grouped_wgrad,
+    gemm_i8,
+    load_ops,
+    mpgemm_combine_rows,
+    mpgemm_combine_rows_backward,
+    mpgemm_gather_rows,
+    mpgemm_grouped,
+    mpgemm_grouped_wgrad,
+    mpgemm_i8_gemm,
+    mpgemm_quantize_rows,
+    mpgemm_route,
+    mpgemm_route_workspace,
+    quantize_rows,
+    route,
 )

@@ -1,0 +1,430 @@
+"""ctypes binding for libmpgemm_ops.so (include/mpgemm_ops.h): products of
+8-bit codes and products of tokens with experts.  Argument marshalling only,
+as in ``_binding``: every step runs in the HIP library, there is no fallback."""
+from __future__ import annotations
+
+import ctypes
+import os
+
+from ._binding import MPGEMM_COL_MAJOR, MPGEMM_OK, MPGEMM_ROW_MAJOR, MpgemmError, _check_tensor
+
+OPS_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmpgemm_ops.so")
+
+MPGEMM_T_F16 = 0
+MPGEMM_T_BF16 = 1
+MPGEMM_T_F32 = 2
+MPGEMM_ID_I32 = 0
+MPGEMM_ID_I64 = 1
+#: groups (experts) of one grouped call
+MPGEMM_MAX_GROUPS = 1024
+#: largest K of mpgemm_i8_gemm
+MPGEMM_I8_MAX_K = 131071
+
+_lib = None
+
+
+def load_ops():
+    """Load the in-tree libmpgemm_ops.so.  Raises if it has not been built."""
+    global _lib
+    if _lib is not None:
+        return _lib
+    if not os.path.exists(OPS_PATH):
+        raise RuntimeError(f"{OPS_PATH} is not built; run `python -c 'import __graft_entry__ as g; g.build()'` "
+                           "(no fallback path exists)")
+    lib = ctypes.CDLL(OPS_PATH)
+    i64, f32, vp, i32 = ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_int
+    for name, args, res in (
+            ("mpgemm_quantize_rows", [i32, i64, i64, vp, i64, vp, i64, i64, vp, i64, vp, vp], i32),
+            ("mpgemm_i8_gemm", [i32, i64, i64, i64, i64, vp, i64, vp, i64, i64, vp, i64, vp, vp, vp, vp, vp], i32),
+            ("mpgemm_route_workspace", [i64, i64], i64),
+            ("mpgemm_route", [i32, i64, i64, vp, vp, vp, vp, vp, i64, vp], i32),
+            ("mpgemm_gather_rows", [i32, i64, i64, vp, i64, vp, i64, i64, vp, i64, vp], i32),
+            ("mpgemm_combine_rows", [i32, i32, i64, i64, i64, i64, vp, i64, vp, vp, vp, i64, vp], i32),
+            ("mpgemm_combine_rows_backward",
+             [i32, i32, i32, i64, i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, vp], i32),
+            ("mpgemm_grouped", [i32, i32, i64, i64, i64, i64, vp, i64, vp, i64, i64, vp, i64, f32, f32, vp, vp], i32),
+            ("mpgemm_grouped_wgrad", [i32, i64, i64, i64, i64, vp, i64, vp, i64, vp, i64, i64, f32, f32, vp, vp], i32)):
+        fn = getattr(lib, name)
+        fn.argtypes = args
+        fn.restype = res
+    _lib = lib
+    return lib
+
+
+# ---- raw entry points (same names and argument order as the C ABI) ----------
+
+def mpgemm_quantize_rows(x_type, T, H, X, ldx, order, R, top_k, Q, ldq, scale, stream=0) -> int:
+    return load_ops().mpgemm_quantize_rows(x_type, T, H, X, ldx, order, R, top_k, Q, ldq, scale, stream)
+
+
+def mpgemm_i8_gemm(out_type, groups, M, N, K, A, lda, W, ldw, stride_w, C, ldc, scale_a, scale_w, bias=0,
+                   offsets=0, stream=0) -> int:
+    return load_ops().mpgemm_i8_gemm(out_type, groups, M, N, K, A, lda, W, ldw, stride_w, C, ldc, scale_a, scale_w,
+                                     bias, offsets, stream)
+
+
+def mpgemm_route_workspace(pairs, experts) -> int:
+    """Bytes of workspace that mpgemm_route needs, or a negative code."""
+    return load_ops().mpgemm_route_workspace(pairs, experts)
+
+
+def mpgemm_route(id_type, pairs, experts, ids, order, position, offsets, workspace=0, workspace_bytes=0,
+                 stream=0) -> int:
+    return load_ops().mpgemm_route(id_type, pairs, experts, ids, order, position, offsets, workspace,
+                                   workspace_bytes, stream)
+
+
+def mpgemm_gather_rows(type_, T, H, X, ldx, order, R, top_k, Y, ldy, stream=0) -> int:
+    return load_ops().mpgemm_gather_rows(type_, T, H, X, ldx, order, R, top_k, Y, ldy, stream)
+
+
+def mpgemm_combine_rows(y_type, o_type, T, top_k, H, R, Y, ldy, position, weights, O, ldo, stream=0) -> int:
+    return load_ops().mpgemm_combine_rows(y_type, o_type, T, top_k, H, R, Y, ldy, position, weights, O, ldo, stream)
+
+
+def mpgemm_combine_rows_backward(d_type, y_type, dy_type, T, top_k, H, R, dO, ldo, Y, ldy, position, weights, dY,
+                                 lddy, dweights, stream=0) -> int:
+    return load_ops().mpgemm_combine_rows_backward(d_type, y_type, dy_type, T, top_k, H, R, dO, ldo, Y, ldy,
+                                                   position, weights, dY, lddy, dweights, stream)
+
+
+def mpgemm_grouped(in_type, layout_b, groups, R, N, K, A, lda, B, ldb, stride_b, C, ldc, alpha, beta, offsets,
+                   stream=0) -> int:
+    return load_ops().mpgemm_grouped(in_type, layout_b, groups, R, N, K, A, lda, B, ldb, stride_b, C, ldc, alpha,
+                                     beta, offsets, stream)
+
+
+def mpgemm_grouped_wgrad(in_type, groups, R, M, N, A, lda, B, ldb, C, ldc, stride_c, alpha, beta, offsets,
+                         stream=0) -> int:
+    return load_ops().mpgemm_grouped_wgrad(in_type, groups, R, M, N, A, lda, B, ldb, C, ldc, stride_c, alpha, beta,
+                                           offsets, stream)
+
+
+# ---- torch tensors ----------------------------------------------------------
+
+_TYPES = None
+
+
+def _type(t, name, types=(MPGEMM_T_F16, MPGEMM_T_BF16, MPGEMM_T_F32)):
+    """MPGEMM_T_* of a tensor's dtype, one of `types`."""
+    global _TYPES
+    import torch
+    if _TYPES is None:
+        _TYPES = {torch.float16: MPGEMM_T_F16, torch.bfloat16: MPGEMM_T_BF16, torch.float32: MPGEMM_T_F32}
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    code = _TYPES.get(t.dtype)
+    if code not in types:
+        names = [str(d).replace("torch.", "") for d, c in _TYPES.items() if c in types]
+        raise TypeError(f"{name} must be {' or '.join(names)}, got {t.dtype}")
+    return code
+
+
+def _rows(t, name, dtype):
+    """Leading dimension of a row-major 2-D GPU tensor."""
+    return _check_tensor(t, name, dtype)[1]
+
+
+def _flat(t, name, dtype, shape):
+    """Pointer of a contiguous GPU tensor of one dtype and shape."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {str(dtype).replace('torch.', '')} tensor")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    return t.data_ptr()
+
+
+def _matrices(t, name, dtype):
+    """(groups, rows, cols, layout, leading dimension, group stride) of a 3-D
+    GPU tensor of matrices, each row- or column-major."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {str(dtype).replace('torch.', '')} tensor")
+    if t.dim() != 3 or t.shape[0] < 1:
+        raise ValueError(f"{name} must be groups x rows x columns, at least one group")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    groups, rows, cols = t.shape
+    sg, sr, sc = t.stride()
+    if cols <= 1 or sc == 1:
+        layout, ld, least = MPGEMM_ROW_MAJOR, (sr if rows > 1 else max(cols, 1)), cols
+    elif rows <= 1 or sr == 1:
+        layout, ld, least = MPGEMM_COL_MAJOR, sc, rows
+    else:
+        raise ValueError(f"{name}: its matrices must have unit stride along one dimension")
+    if ld < max(least, 1):
+        raise ValueError(f"{name}: the rows or columns of its matrices overlap (stride {ld} < {least})")
+    return groups, rows, cols, layout, ld, (sg if groups > 1 else 0)
+
+
+class _On:
+    """The device and stream of a call: every tensor on one GPU, the launch on
+    that GPU's current stream or the one given, with that GPU current."""
+
+    def __init__(self, stream, *tensors):
+        import torch
+        self.device = tensors[0].device
+        for t in tensors[1:]:
+            if t is not None and t.device != self.device:
+                raise ValueError(f"tensors are on {self.device} and {t.device}: one GPU is needed")
+        if stream is None:
+            self.handle = torch.cuda.current_stream(self.device).cuda_stream
+        elif hasattr(stream, "cuda_stream"):
+            if stream.device != self.device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
+            self.handle = stream.cuda_stream
+        else:
+            self.handle = int(stream)
+
+    def call(self, fn, *args):
+        import torch
+        if torch.cuda.current_device() == self.device.index:
+            rc = fn(*args, self.handle)
+        else:
+            with torch.cuda.device(self.device):
+                rc = fn(*args, self.handle)
+        if rc != MPGEMM_OK:
+            raise MpgemmError(rc, fn.__name__)
+
+
+def quantize_rows(X, Q, scale, order=None, top_k: int = 1, stream=None):
+    """Rows of X to 8-bit codes: scale = max|row| / 127 and the codes nearest
+    to 127 * row / max|row| (ties to even).  Returns (Q, scale).
+
+    X (T x H): float16, bfloat16 or float32, row-major.  Q (R x H): int8,
+    row-major.  scale: float32, R values.  Without ``order`` R == T; with it
+    (int32, R values from :func:`route`) row p of Q is row order[p] // top_k
+    of X, and rows whose order is -1 keep what they hold.  A row with an
+    infinity or a NaN has a NaN scale and codes 0."""
+    import torch
+    xt = _type(X, "X")
+    ldx = _rows(X, "X", X.dtype)
+    ldq = _rows(Q, "Q", torch.int8)
+    T, H = X.shape
+    R = Q.shape[0]
+    if Q.shape[1] != H or (order is None and R != T):
+        raise ValueError(f"shape mismatch: X {tuple(X.shape)}, Q {tuple(Q.shape)}")
+    sp = _flat(scale, "scale", torch.float32, (R,))
+    op = 0 if order is None else _flat(order, "order", torch.int32, (R,))
+    _On(stream, X, Q, scale, order).call(mpgemm_quantize_rows, xt, T, H, X.data_ptr(), ldx, op, R, int(top_k),
+                                         Q.data_ptr(), ldq, sp)
+    return Q, scale
+
+
+def gemm_i8(A, B, C, scale_a, scale_b, bias=None, offsets=None, stream=None):
+    """C <- (A @ B) * scale_a[:, None] * scale_b (+ bias), A and B 8-bit codes,
+    the sum exact.  Returns C.
+
+    A (M x K): int8, row-major.  B (K x N): int8, column-major (the transpose
+    view of N x K weights).  C (M x N): float16, bfloat16 or float32,
+    row-major.  scale_a: float32, M values; scale_b and bias: float32, N
+    values.  With ``offsets`` (int32, groups + 1 values from :func:`route`) B
+    is groups x K x N and scale_b and bias are groups x N: rows offsets[g] ..
+    offsets[g+1]-1 of A and C use group g's, other rows of C keep what they
+    hold."""
+    import torch
+    ot = _type(C, "C")
+    lda = _rows(A, "A", torch.int8)
+    ldc = _rows(C, "C", C.dtype)
+    M, K = A.shape
+    if offsets is None:
+        if not isinstance(B, torch.Tensor) or B.dim() != 2:
+            raise ValueError("B must be 2-D (3-D with offsets)")
+        B = B.unsqueeze(0)
+    G, K2, N, layout, ldw, stride = _matrices(B, "B", torch.int8)
+    if layout != MPGEMM_COL_MAJOR:
+        # one value along a dimension: the bytes lie the same in both orders
+        if K2 > 1 and N > 1:
+            raise ValueError("B must be column-major (unit stride along K)")
+        if K2 <= 1:
+            ldw = B.stride(2) if N > 1 else 1
+        else:  # N <= 1
+            if B.stride(1) != 1 and N == 1:
+                raise ValueError("B must be column-major (unit stride along K)")
+            ldw = K2
+    if K2 != K or tuple(C.shape) != (M, N):
+        raise ValueError(f"shape mismatch: A {tuple(A.shape)}, B {tuple(B.shape)}, C {tuple(C.shape)}")
+    wide = (N,) if offsets is None else (G, N)
+    sa = _flat(scale_a, "scale_a", torch.float32, (M,))
+    sb = _flat(scale_b, "scale_b", torch.float32, wide)
+    bp = 0 if bias is None else _flat(bias, "bias", torch.float32, wide)
+    op = 0 if offsets is None else _flat(offsets, "offsets", torch.int32, (G + 1,))
+    _On(stream, C, A, B, scale_a, scale_b, bias, offsets).call(
+        mpgemm_i8_gemm, ot, G, M, N, K, A.data_ptr(), lda, B.data_ptr(), ldw, stride, C.data_ptr(), ldc, sa, sb, bp,
+        op)
+    return C
+
+
+def route(experts, num_experts: int, out=None, workspace=None, stream=None):
+    """The order of (token, slot) pairs by expert.  Returns (order, position,
+    offsets), int32.
+
+    experts: int32 or int64, contiguous, usually T x top_k; ids outside 0 ..
+    num_experts-1 are pairs without an expert.  order: the pair at each
+    position of the stable sort, -1 behind the last expert's; position (of
+    experts' shape): each pair's position, -1 without an expert; offsets
+    (num_experts + 1): each expert's first position.
+    ``out``: the three tensors to write (allocated when None).
+    ``workspace``: a contiguous int32 tensor of at least
+    mpgemm_route_workspace bytes; allocated when None and needed."""
+    import torch
+    if not isinstance(experts, torch.Tensor) or experts.dtype not in (torch.int32, torch.int64):
+        raise TypeError("experts must be an int32 or int64 tensor")
+    if not experts.is_cuda or not experts.is_contiguous():
+        raise ValueError("experts must be contiguous, on the GPU")
+    pairs, E = experts.numel(), int(num_experts)
+    need = mpgemm_route_workspace(pairs, E)
+    if need < 0:
+        raise MpgemmError(need, "mpgemm_route")
+    given = () if out is None else tuple(out)
+    if out is not None and len(given) != 3:
+        raise ValueError("out must be (order, position, offsets)")
+    if workspace is not None and (not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.int32
+                                  or not workspace.is_contiguous() or not workspace.is_cuda):
+        raise TypeError("workspace must be a contiguous int32 tensor on the GPU")
+    on = _On(stream, experts, *given, workspace)
+
+    def allocate():
+        new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=on.device)  # noqa: E731
+        return (given or (new(pairs), new(*experts.shape), new(E + 1)),
+                new(need // 4) if workspace is None and need else workspace)
+
+    if stream is None:
+        given, workspace = allocate()
+    else:
+        # memory from the launch's own stream: what the current stream freed
+        # may still be in use there
+        with torch.cuda.stream(torch.cuda.ExternalStream(on.handle, device=on.device)):
+            given, workspace = allocate()
+    order, position, offsets = given
+    op = _flat(order, "order", torch.int32, (pairs,))
+    pp = _flat(position, "position", torch.int32, experts.shape)
+    fp = _flat(offsets, "offsets", torch.int32, (E + 1,))
+    on.call(mpgemm_route, MPGEMM_ID_I64 if experts.dtype == torch.int64 else MPGEMM_ID_I32, pairs, E,
+            experts.data_ptr(), op, pp, fp, 0 if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else 4 * workspace.numel())
+    return order, position, offsets
+
+
+def gather_rows(X, order, Y, top_k: int = 1, stream=None):
+    """Y[p] = X[order[p] // top_k]: tokens' rows into expert order.  Returns Y.
+
+    X (T x H) and Y (R x H): float16, bfloat16 or float32, the same, row-major.
+    order: int32, R values from :func:`route`; rows whose order is -1 keep
+    what they hold.  The gradient by X is ``combine_rows(dY, position, dX)``."""
+    import torch
+    ty = _type(X, "X")
+    ldx, ldy = _rows(X, "X", X.dtype), _rows(Y, "Y", X.dtype)
+    if X.shape[1] != Y.shape[1]:
+        raise ValueError(f"shape mismatch: X {tuple(X.shape)}, Y {tuple(Y.shape)}")
+    op = _flat(order, "order", torch.int32, (Y.shape[0],))
+    _On(stream, Y, X, order).call(mpgemm_gather_rows, ty, X.shape[0], X.shape[1], X.data_ptr(), ldx, op, Y.shape[0],
+                                  int(top_k), Y.data_ptr(), ldy)
+    return Y
+
+
+def _slots(position, T):
+    if position.dim() != 2 or position.shape[0] != T:
+        raise ValueError(f"position must be {T} x top_k, got {tuple(position.shape)}")
+    return position.shape[1]
+
+
+def combine_rows(Y, position, out, weights=None, stream=None):
+    """out[t] = sum_s weights[t, s] * Y[position[t, s]] in FP32, slots
+    ascending.  Returns out.
+
+    Y (R x H) and out (T x H): float16, bfloat16 or float32 each, row-major.
+    position: int32, T x top_k from :func:`route`; pairs at -1 add nothing.
+    weights: float32, T x top_k, or None for ones."""
+    import torch
+    yt, ot = _type(Y, "Y"), _type(out, "out")
+    ldy, ldo = _rows(Y, "Y", Y.dtype), _rows(out, "out", out.dtype)
+    T, H = out.shape
+    if Y.shape[1] != H:
+        raise ValueError(f"shape mismatch: Y {tuple(Y.shape)}, out {tuple(out.shape)}")
+    pp = _flat(position, "position", torch.int32, position.shape)
+    k = _slots(position, T)
+    wp = 0 if weights is None else _flat(weights, "weights", torch.float32, (T, k))
+    _On(stream, out, Y, position, weights).call(mpgemm_combine_rows, yt, ot, T, k, H, Y.shape[0], Y.data_ptr(), ldy,
+                                                pp, wp, out.data_ptr(), ldo)
+    return out
+
+
+def combine_rows_backward(dout, Y, position, weights, dY, dweights=None, stream=None):
+    """The gradients of :func:`combine_rows`: dY[position[t, s]] = weights[t, s]
+    * dout[t] and dweights[t, s] = <dout[t], Y[position[t, s]]>.  Returns
+    (dY, dweights).
+
+    dout (T x H), Y and dY (R x H): float16, bfloat16 or float32 each,
+    row-major.  weights: float32, T x top_k, or None for ones.  dweights:
+    float32, T x top_k, 0 for pairs at -1; None: not computed (Y may be None).
+    Rows of dY that no pair has keep what they hold."""
+    import torch
+    dt, gt = _type(dout, "dout"), _type(dY, "dY")
+    ldo, ldg = _rows(dout, "dout", dout.dtype), _rows(dY, "dY", dY.dtype)
+    T, H = dout.shape
+    yt, ldy, yp = dt, ldo, 0
+    if Y is not None:
+        yt, ldy, yp = _type(Y, "Y"), _rows(Y, "Y", Y.dtype), Y.data_ptr()
+        if Y.shape != dY.shape:
+            raise ValueError(f"shape mismatch: Y {tuple(Y.shape)}, dY {tuple(dY.shape)}")
+    elif dweights is not None:
+        raise ValueError("dweights needs Y")
+    if dY.shape[1] != H:
+        raise ValueError(f"shape mismatch: dout {tuple(dout.shape)}, dY {tuple(dY.shape)}")
+    pp = _flat(position, "position", torch.int32, position.shape)
+    k = _slots(position, T)
+    wp = 0 if weights is None else _flat(weights, "weights", torch.float32, (T, k))
+    gp = 0 if dweights is None else _flat(dweights, "dweights", torch.float32, (T, k))
+    _On(stream, dY, dout, Y, position, weights, dweights).call(
+        mpgemm_combine_rows_backward, dt, yt, gt, T, k, H, dY.shape[0], dout.data_ptr(), ldo, yp, ldy, pp, wp,
+        dY.data_ptr(), ldg, gp)
+    return dY, dweights
+
+
+def gemm_grouped(A, B, C, offsets, alpha: float = 1.0, beta: float = 0.0, stream=None):
+    """C[rows of g] <- alpha * A[rows of g] @ B[g] + beta * C[rows of g] for
+    every group g, its rows being offsets[g] .. offsets[g+1]-1.  Returns C.
+
+    A (R x K, row-major) and B (groups x K x N, each row- or column-major):
+    both float16 or both bfloat16.  C (R x N): float32, row-major; rows of no
+    group keep what they hold.  offsets: int32, groups + 1 values.  The
+    gradient by A is ``gemm_grouped(dC, B.mT, dA, offsets)``."""
+    import torch
+    it = _type(A, "A", (MPGEMM_T_F16, MPGEMM_T_BF16))
+    lda, ldc = _rows(A, "A", A.dtype), _rows(C, "C", torch.float32)
+    G, K2, N, layout, ldb, stride = _matrices(B, "B", A.dtype)
+    R, K = A.shape
+    if K2 != K or tuple(C.shape) != (R, N):
+        raise ValueError(f"shape mismatch: A {tuple(A.shape)}, B {tuple(B.shape)}, C {tuple(C.shape)}")
+    op = _flat(offsets, "offsets", torch.int32, (G + 1,))
+    _On(stream, C, A, B, offsets).call(mpgemm_grouped, it, layout, G, R, N, K, A.data_ptr(), lda, B.data_ptr(), ldb,
+                                       stride, C.data_ptr(), ldc, float(alpha), float(beta), op)
+    return C
+
+
+def gemm_grouped_wgrad(A, B, C, offsets, alpha: float = 1.0, beta: float = 0.0, stream=None):
+    """C[g] <- alpha * A[:, rows of g] @ B[rows of g] + beta * C[g] for every
+    group g: the gradient of :func:`gemm_grouped` by its weights.  Returns C.
+
+    A (M x R, column-major: the transpose view of R x M rows) and B (R x N,
+    row-major): both float16 or both bfloat16.  C (groups x M x N): float32,
+    each row-major; a group without rows has beta * C[g]."""
+    import torch
+    it = _type(A, "A", (MPGEMM_T_F16, MPGEMM_T_BF16))
+    if A.dim() != 2:
+        raise ValueError("A must be 2-D")
+    lda, ldb = _rows(A.t(), "A (transposed)", A.dtype), _rows(B, "B", A.dtype)
+    G, M, N, layout, ldc, stride = _matrices(C, "C", torch.float32)
+    if layout != MPGEMM_ROW_MAJOR:
+        raise ValueError("C must be row-major")
+    R = B.shape[0]
+    if tuple(A.shape) != (M, R) or B.shape[1] != N:
+        raise ValueError(f"shape mismatch: A {tuple(A.shape)}, B {tuple(B.shape)}, C {tuple(C.shape)}")
+    op = _flat(offsets, "offsets", torch.int32, (G + 1,))
+    _On(stream, C, A, B, offsets).call(mpgemm_grouped_wgrad, it, G, R, M, N, A.data_ptr(), lda, B.data_ptr(), ldb,
+                                       C.data_ptr(), ldc, stride, float(alpha), float(beta), op)
+    return C

@@ -5,6 +5,9 @@
 * ``libmpgemm.so`` -- the product library (``csrc/mpgemm.hip``, C ABI in
   ``include/mpgemm.h``): the config entries the factory chooses from and the
   fallbacks;
+* ``libmpgemm_ops.so`` -- the operators beside the GEMM (``csrc/ops.hip``,
+  C ABI in ``include/mpgemm_ops.h``): products of 8-bit codes, products of
+  tokens with experts;
 * ``libmpgemm_probes.so`` -- the diagnostics (``csrc/probes.hip``, C ABI in
   ``include/mpgemm_probes.h``);
 * ``libmpgemm_timeline.so`` -- the product library built with
@@ -33,7 +36,11 @@ CSRC = os.path.join(HERE, "csrc")
 SRC = os.path.join(CSRC, "mpgemm.hip")
 PROBES_SRC = os.path.join(CSRC, "probes.hip")
 DEPS = [SRC, os.path.join(CSRC, "kernels.hpp"), os.path.join(ROOT, "include", "mpgemm.h")]
+OPS_SRC = os.path.join(CSRC, "ops.hip")
+OPS_DEPS = [OPS_SRC, os.path.join(ROOT, "include", "mpgemm_ops.h"), *DEPS[1:],
+            *(os.path.join(CSRC, f) for f in ("groups.hpp", "i8_kernels.hpp", "token_kernels.hpp"))]
 LIB = os.path.join(HERE, "libmpgemm.so")
+OPS_LIB = os.path.join(HERE, "libmpgemm_ops.so")
 PROBES_LIB = os.path.join(HERE, "libmpgemm_probes.so")
 CANDIDATES_LIB = os.path.join(HERE, "libmpgemm_candidates.so")
 TIMELINE_LIB = os.path.join(HERE, "libmpgemm_timeline.so")
@@ -74,9 +81,10 @@ def _finish(job):
 def build(extra=(), out: str = LIB, verbose: bool = False, probes: bool = True,
           candidates: bool = False) -> str:
     """Compile the product library to ``out`` (default: in-tree
-    ``libmpgemm.so``), the diagnostics libraries (probes, timeline), and
-    optionally the candidates library, in parallel.  Returns ``out``."""
-    jobs = [_start(SRC, out, extra, verbose)]
+    ``libmpgemm.so``), the operator library, the diagnostics libraries
+    (probes, timeline), and optionally the candidates library, in parallel.
+    Returns ``out``."""
+    jobs = [_start(SRC, out, extra, verbose), _start(OPS_SRC, OPS_LIB, extra, verbose)]
     if probes:
         jobs.append(_start(PROBES_SRC, PROBES_LIB, extra, verbose))
         jobs.append(_start(SRC, TIMELINE_LIB, (*extra, "-DMPGEMM_TIMELINE"), verbose))
@@ -116,10 +124,10 @@ def build_c_check(verbose: bool = False) -> str:
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(d) > t for d in DEPS)
+    for lib, deps in ((LIB, DEPS), (OPS_LIB, OPS_DEPS)):
+        if not os.path.exists(lib) or any(os.path.getmtime(d) > os.path.getmtime(lib) for d in deps):
+            return True
+    return False
 
 
 if __name__ == "__main__":

@@ -1,0 +1,399 @@
+// i8_kernels.hpp -- products of 8-bit codes with scales per token and channel
+// (gfx950).  Included by ops.hip after kernels.hpp, in its namespace.
+//
+//     C[i][j] = (float)(sum_k A[i][k] * W[j][k]) * scale_a[i] * scale_w[j] (+ bias[j])
+//
+// A: tokens x K codes, W: channels x K codes (both K-contiguous), the sum
+// exact in 32-bit integers, rounded once to FP32 before the scales and once
+// more to the output type.  With groups, token rows [offsets[g],
+// offsets[g+1]) use W[g], scale_w[g], bias[g].
+//
+// i8_tile<Cfg>: the schedule of the 16-bit pipelined kernel (an LDS ring of K
+// tiles filled by direct-to-LDS copies, operands one k-step ahead of their
+// matrix instructions) on v_mfma_i32_16x16x64_i8: a lane supplies 16
+// K-consecutive codes, the same 16 bytes as 8 16-bit values, so tiles,
+// swizzles and copies are those of a 16-bit product half as deep.  What
+// differs:
+//  * the weights are the instruction's first operand and the tokens its
+//    second, so a lane's accumulators are neighbouring channels of one token:
+//    one scale_a per lane and operand, and wide stores;
+//  * pairs of weight operands take interleaved groups of 4 channels (operand
+//    2p + h, row r holds channel 32p + 8*(r/4) + 4h + r%4), which gives a
+//    lane 8 consecutive channels: 16-byte stores of 16-bit outputs;
+//  * K % 16 needs no extra step: the vector that straddles K is filled
+//    through registers with zeros behind K.
+// Matrix-core layout (v_mfma_i32_16x16x64_i8): lane l supplies
+// A[l%16][16*(l/16) + 0..15] and B[16*(l/16) + 0..15][l%16]; accumulator v
+// of lane l holds D[4*(l/16) + v][l%16].
+
+struct I8Args {
+    const int8_t *A;
+    const int8_t *W;
+    void *C;
+    const float *scale_a;
+    const float *scale_w;
+    const float *bias;       // or nullptr
+    int64_t lda, ldw, ldc;   // elements
+    int32_t N, K;
+    int32_t tiles_n;
+    int32_t group_m;
+    GroupArgs groups;
+};
+
+// Element types of tensors, as MPGEMM_T_* in the header.
+constexpr int kTF16 = 0;
+constexpr int kTBF16 = 1;
+constexpr int kTF32 = 2;
+
+template <int T>
+struct ElemOf;
+template <>
+struct ElemOf<kTF16> {
+    typedef _Float16 type;
+};
+template <>
+struct ElemOf<kTBF16> {
+    typedef __bf16 type;
+};
+template <>
+struct ElemOf<kTF32> {
+    typedef float type;
+};
+
+// N elements at any element-aligned address (the vector memory of gfx9
+// devices runs in unaligned mode under ROCm).
+template <class E, int N>
+struct __attribute__((packed, aligned(sizeof(E)))) Pack {
+    E v[N];
+};
+
+// One K-contiguous operand tile of BX rows of BKB bytes in LDS; see OpTile.
+// PAIR: read by paired operands (rows 0..3, 8..11, 16..19, 24..27 of 32, or
+// those plus 4, in one 16-lane group); otherwise 16 consecutive rows.
+template <int BX, int BKB, int NW, bool PAIR>
+struct I8Tile {
+    static constexpr int CH = BKB / 16;      // 16-byte chunks per row
+    static constexpr int RPI = 64 / CH;      // rows per copy instruction
+    static constexpr int PW = BX / RPI / NW; // copies per wave per tile
+    static constexpr int BYTES = BX * BKB;
+    static_assert(CH == 8 || CH == 16, "rows of 128 or 256 bytes");
+    static_assert((BX / RPI) % NW == 0 && PW >= 1, "copies must split evenly over waves");
+    // The 16 rows that one 16-lane group of a ds_read_b128 touches at one
+    // chunk must fall on 256 distinct bytes of the 64 banks.  256-byte rows:
+    // 16 different chunks; 128-byte rows: the row's lowest bit picks the half
+    // of the banks, the other three bits that vary pick one of 8 chunks.
+    __device__ static __forceinline__ int swz(int r)
+    {
+        if constexpr (PAIR) {
+            const int hi = (r >> 3) & 3;     // bits 3, 4
+            return CH == 16 ? (r & 3) | (hi << 2) : ((r >> 1) & 1) | (hi << 1);
+        } else {
+            return CH == 16 ? (r & 15) : ((r >> 1) & 7);
+        }
+    }
+};
+
+template <int BM_, int BN_, int BKB_, int WAVES_M_, int WAVES_N_, int STAGES_>
+struct I8Cfg {
+    static constexpr int BM = BM_, BN = BN_, BKB = BKB_;
+    static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, STAGES = STAGES_;
+    static constexpr int NW = WAVES_M * WAVES_N, NT = 64 * NW;
+    static constexpr int WTM = BM / WAVES_M, WTN = BN / WAVES_N;
+    static constexpr int FM = WTM / 16, FN = WTN / 16;
+    static constexpr int KS = BKB / 64;               // k-steps per tile
+    static constexpr bool PAIR = FN % 2 == 0;
+    using TA = I8Tile<BM, BKB, NW, false>;
+    using TW = I8Tile<BN, BKB, NW, PAIR>;
+    static constexpr int STAGE_BYTES = TA::BYTES + TW::BYTES;
+    static constexpr int LDS_BYTES = STAGES * STAGE_BYTES;
+    static constexpr int NCOPY = TA::PW + TW::PW;
+    static constexpr int COPY_WINDOW = STAGES == 2 ? (NCOPY < KS * FM ? NCOPY : KS * FM) : KS * FM;
+    static_assert(WTM % 16 == 0 && WTN % 16 == 0, "wave tiles are multiples of the instruction's");
+    static_assert(KS >= 2, "a K tile holds two k-steps at least");
+    static_assert(STAGES >= 2 && STAGES <= 4, "2..4 LDS stages");
+    static_assert(NCOPY * (STAGES - 1) < 64, "vmcnt is 6 bits");
+    static_assert(LDS_BYTES <= 160 * 1024, "gfx950 has 160 KiB of LDS per workgroup");
+};
+
+typedef int32_t i32x4v __attribute__((ext_vector_type(4)));
+
+// One value of the product: the exact sum, rounded to FP32, then the scales
+// and the bias in FP32.
+__device__ __forceinline__ float i8_value(int32_t sum, float sa, float sw, float bias, bool has_bias)
+{
+    const float v = (float)sum * sa * sw;
+    return has_bias ? v + bias : v;
+}
+
+// COUNT consecutive channels of one token, from column `col` (left = columns
+// from it to the edge).
+template <int OUT, int COUNT>
+__device__ __forceinline__ void i8_store(typename ElemOf<OUT>::type *row, int col, int left, const float *v)
+{
+    typedef typename ElemOf<OUT>::type E;
+    if (left >= COUNT) {
+        Pack<E, COUNT> p;
+#pragma unroll
+        for (int e = 0; e < COUNT; ++e)
+            p.v[e] = (E)v[e];
+        *(Pack<E, COUNT> *)(row + col) = p;
+    } else {
+#pragma unroll
+        for (int e = 0; e < COUNT; ++e)
+            if (e < left)
+                row[col + e] = (E)v[e];
+    }
+}
+
+template <class Cfg, int OUT>
+__global__ void __launch_bounds__(Cfg::NT)
+i8_tile(I8Args args)
+{
+    constexpr int BM = Cfg::BM, BN = Cfg::BN, BKB = Cfg::BKB, S = Cfg::STAGES;
+    constexpr int FM = Cfg::FM, FN = Cfg::FN, KS = Cfg::KS, NCOPY = Cfg::NCOPY;
+    using TA = typename Cfg::TA;
+    using TW = typename Cfg::TW;
+    typedef typename ElemOf<OUT>::type E;
+
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[Cfg::LDS_BYTES];
+    lds_u8 *const lds = (lds_u8 *)smem;
+    const uint32_t lds_base = (uint32_t)(uintptr_t)lds;
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / Cfg::WAVES_N;
+    const int wn = wave % Cfg::WAVES_N;
+
+    GroupTile gt;
+    if (!find_row_tile(args.groups, BM, args.tiles_n, args.group_m, gt))
+        return;
+    const int K = args.K;
+    const int row0 = gt.start + gt.tm * BM;          // first token row of the tile
+    const int rows_left = gt.rows - gt.tm * BM;      // > 0
+    const int n0 = gt.tn * BN;
+    const int cols_left = args.N - n0;               // > 0
+    const int8_t *const Ap = args.A + (int64_t)row0 * args.lda;
+    const int8_t *const Wp = args.W + (int64_t)gt.group * args.groups.stride + (int64_t)n0 * args.ldw;
+
+    // ---- copies: slot q of this wave fills LDS rows RPI*j .. of its operand
+    // (j = i*NW + wave) from a fixed place of the operand; the K tile moves
+    // the scalar offset.  Rows outside the product, and in the last tile
+    // chunks at or past K, read zeros.
+    const i32x4 rsA = make_rsrc4(Ap), rsW = make_rsrc4(Wp);
+    uint32_t voff[NCOPY];
+#pragma unroll
+    for (int q = 0; q < NCOPY; ++q) {
+        const bool is_a = q < TA::PW;
+        const int i = is_a ? q : q - TA::PW;
+        const int j = i * Cfg::NW + wave;
+        const int r = TA::RPI * j + lane / TA::CH;
+        const int c = (lane % TA::CH) ^ (is_a ? TA::swz(r) : TW::swz(r));
+        const bool ok = r < (is_a ? rows_left : cols_left);
+        voff[q] = ok ? (uint32_t)(r * (int)(is_a ? args.lda : args.ldw) + 16 * c) : kOOB;
+    }
+    const int num_k = (K + BKB - 1) / BKB;
+    const int klast = K - (num_k - 1) * BKB;         // bytes of the last tile
+    // this lane's 16-byte chunk of slot q's rows (looked at in the last tile)
+    auto chunk_of = [&](int q) __attribute__((always_inline)) {
+        const bool is_a = q < TA::PW;
+        const int i = is_a ? q : q - TA::PW;
+        const int r = TA::RPI * (i * Cfg::NW + wave) + lane / TA::CH;
+        return (lane % TA::CH) ^ (is_a ? TA::swz(r) : TW::swz(r));
+    };
+    uint32_t copy_region = 0, copy_soff = 0;
+    int copy_tile = 0;
+    auto begin_copies = [&](int t, int buf) __attribute__((always_inline)) {
+        copy_region = lds_base + buf * Cfg::STAGE_BYTES;
+        copy_soff = (uint32_t)t * BKB;
+        copy_tile = t;
+    };
+    auto copy_one = [&](int q) __attribute__((always_inline)) {
+        if (copy_tile >= num_k)
+            return;
+        const bool is_a = q < TA::PW;
+        const int j = (is_a ? q : q - TA::PW) * Cfg::NW + wave;
+        uint32_t off = voff[q];
+        if (copy_tile == num_k - 1 && klast < BKB && 16 * chunk_of(q) + 16 > klast)
+            off = kOOB;
+        dma16(is_a ? rsA : rsW, copy_region + (is_a ? 0 : TA::BYTES) + j * 1024, off, copy_soff);
+    };
+    // The vectors of the last tile that straddle K: byte loads, zeros at and
+    // past K, into the slots where the copies wrote zeros.
+    auto fill = [&](int buf) __attribute__((always_inline)) {
+        int ln = lane;
+        asm volatile("" : "+v"(ln));
+        const int c_at = klast / 16, nv = klast % 16;
+        const int ko = (num_k - 1) * BKB + 16 * c_at;
+#pragma unroll
+        for (int q = 0; q < NCOPY; ++q) {
+            const bool is_a = q < TA::PW;
+            const int j = (is_a ? q : q - TA::PW) * Cfg::NW + wave;
+            const int r = TA::RPI * j + ln / TA::CH;
+            const int c = (ln % TA::CH) ^ (is_a ? TA::swz(r) : TW::swz(r));
+            if (c == c_at && r < (is_a ? rows_left : cols_left)) {
+                const int8_t *p = is_a ? Ap + (int64_t)r * args.lda + ko : Wp + (int64_t)r * args.ldw + ko;
+                uint32_t w[4] = {0, 0, 0, 0};
+                for (int e = 0; e < nv; ++e) {
+                    const uint32_t b = (uint32_t)(uint8_t)p[e] << (8 * (e & 3));
+                    if (e < 4)
+                        w[0] |= b;
+                    else if (e < 8)
+                        w[1] |= b;
+                    else if (e < 12)
+                        w[2] |= b;
+                    else
+                        w[3] |= b;
+                }
+                *(lds_u32x4 *)(lds + buf * Cfg::STAGE_BYTES + (is_a ? 0 : TA::BYTES) + j * 1024 + ln * 16) =
+                    u32x4{w[0], w[1], w[2], w[3]};
+            }
+        }
+    };
+
+    // ---- operand reads
+    const int a_row = wm * Cfg::WTM + (lane & 15);
+    const int a_base = a_row * BKB, a_sw = TA::swz(a_row);
+    const int w_row = wn * Cfg::WTN + (Cfg::PAIR ? 8 * ((lane & 15) >> 2) + (lane & 3) : (lane & 15));
+    const int w_base = w_row * BKB, w_sw = TW::swz(w_row);
+    i32x4v ra[FM], rw[2][FN];
+    auto read_a = [&](int buf, int ks, int f) __attribute__((always_inline)) {
+        ra[f] = *(const __attribute__((address_space(3))) i32x4v *)(lds + buf * Cfg::STAGE_BYTES + a_base +
+                                                                    f * 16 * BKB + ((4 * ks + lane / 16) ^ a_sw) * 16);
+    };
+    auto read_w = [&](int buf, int ks, int set, int f) __attribute__((always_inline)) {
+        const int drow = Cfg::PAIR ? 32 * (f / 2) + 4 * (f % 2) : 16 * f;
+        rw[set][f] = *(const __attribute__((address_space(3))) i32x4v *)(lds + buf * Cfg::STAGE_BYTES + TA::BYTES +
+                                                                         w_base + drow * BKB +
+                                                                         ((4 * ks + lane / 16) ^ w_sw) * 16);
+    };
+
+    i32x4v acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            acc[i][j] = i32x4v{0};
+
+    // Make tile t (in buffer buf) visible: its copies have landed (`newer`
+    // whole tiles issued after it may still be in flight).
+    auto publish = [&](int t, int buf, int newer) __attribute__((always_inline)) {
+        if (t == num_k - 1 && (klast & 15) != 0) {
+            wait_vmcnt<0>();
+            fill(buf);
+        } else if (newer <= 0) {
+            wait_vmcnt<0>();
+        } else if (newer == 1) {
+            wait_vmcnt<NCOPY>();
+        } else if (newer == 2) {
+            wait_vmcnt<(S > 2 ? 2 : 1) * NCOPY>();
+        } else {
+            wait_vmcnt<(S > 3 ? 3 : 1) * NCOPY>();
+        }
+        __syncthreads();
+    };
+    auto copy_slice = [&](int p) __attribute__((always_inline)) {
+        constexpr int CW = Cfg::COPY_WINDOW;
+#pragma unroll
+        for (int c = 0; c < NCOPY; ++c)
+            if (c >= (p * NCOPY + CW - 1) / CW && c < ((p + 1) * NCOPY + CW - 1) / CW)
+                copy_one(c);
+    };
+
+    if (num_k > 0) {
+#pragma unroll
+        for (int t = 0; t < S; ++t) {
+            begin_copies(t, t);
+#pragma unroll
+            for (int c = 0; c < NCOPY; ++c)
+                copy_one(c);
+        }
+        publish(0, 0, num_k - 1 < S - 1 ? num_k - 1 : S - 1);
+#pragma unroll
+        for (int f = 0; f < FM; ++f)
+            read_a(0, 0, f);
+#pragma unroll
+        for (int f = 0; f < FN; ++f)
+            read_w(0, 0, 0, f);
+    }
+    int buf = 0;
+    for (int kt = 0; kt < num_k; ++kt) {
+        const int nbuf = (buf + 1 == S) ? 0 : buf + 1;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            const int set = ks & 1;
+            const bool last = ks + 1 == KS;
+            if (last && kt + 1 < num_k) {
+                const int newer = num_k - 2 - kt;
+                publish(kt + 1, nbuf, newer < S - 2 ? newer : S - 2);
+            }
+            if (last)
+                begin_copies(kt + S, buf);
+#pragma unroll
+            for (int f = 0; f < FN; ++f) {
+                if (!last)
+                    read_w(buf, ks + 1, set ^ 1, f);
+                else if (kt + 1 < num_k)
+                    read_w(nbuf, 0, set ^ 1, f);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(rw[set][j], ra[i], acc[i][j], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                if (!last)
+                    read_a(buf, ks + 1, i);
+                else if (kt + 1 < num_k)
+                    read_a(nbuf, 0, i);
+                // the last k-step opens the window of tile kt+S; the others
+                // continue that of tile kt+S-1, which the ring fill issued
+                // whole when kt == 0
+                if (last)
+                    copy_slice(i);
+                else if (kt > 0)
+                    copy_slice(FM + ks * FM + i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        buf = nbuf;
+    }
+
+    // ---- epilogue: lane l holds token l%16 of operand i and, per operand
+    // pair, channels 32p + 8*(l/16) + 0..7 (unpaired: 16j + 4*(l/16) + 0..3)
+    constexpr int COUNT = Cfg::PAIR ? 8 : 4;
+    constexpr int NP = Cfg::PAIR ? FN / 2 : FN;
+    const int lrow = wm * Cfg::WTM + (lane & 15);
+    const int lcol = wn * Cfg::WTN + COUNT * (lane >> 4);
+    const float *const sw_p = args.scale_w + (int64_t)gt.group * args.N + n0;
+    const float *const bias_p = args.bias ? args.bias + (int64_t)gt.group * args.N + n0 : nullptr;
+    float sa[FM];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+        sa[i] = lrow + 16 * i < rows_left ? args.scale_a[row0 + lrow + 16 * i] : 0.0f;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        const int c = lcol + 4 * COUNT * p;
+        const int left = cols_left - c;
+        if (left <= 0)
+            continue;
+        float sw[COUNT], bv[COUNT];
+#pragma unroll
+        for (int e = 0; e < COUNT; ++e) {
+            sw[e] = e < left ? sw_p[c + e] : 0.0f;
+            bv[e] = bias_p && e < left ? bias_p[c + e] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            if (lrow + 16 * i >= rows_left)
+                continue;
+            float v[COUNT];
+#pragma unroll
+            for (int e = 0; e < COUNT; ++e) {
+                const int32_t sum = acc[i][Cfg::PAIR ? 2 * p + e / 4 : p][e % 4];
+                v[e] = i8_value(sum, sa[i], sw[e], bv[e], bias_p != nullptr);
+            }
+            i8_store<OUT, COUNT>((E *)args.C + (int64_t)(row0 + lrow + 16 * i) * args.ldc + n0, c, left, v);
+        }
+    }
+}

@@ -164,6 +164,10 @@ __device__ __forceinline__ void tile_coords(int bid, int nb, int tiles_n, int ti
     tn = in_group / gsize;
 }
 
+#ifdef MPGEMM_GROUPED
+#include "groups.hpp"
+#endif
+
 // Bounds-checked epilogue for one 32x32 accumulator tile whose top-left
 // element is C[row0][col0]: C = alpha*acc + beta*C, C not read when beta == 0.
 __device__ __forceinline__ void store_tile32(const floatx16 &acc, float *C, int64_t ldc,
@@ -578,9 +582,16 @@ struct OpReader {
     }
 };
 
+// MPGEMM_GROUPED compiles the same kernel as one launch over several products
+// (the operator library; see groups.hpp): only which product and which tile of
+// it a workgroup takes differs.
 template <class Cfg, bool NT_STORES = true>
 __global__ void __launch_bounds__(Cfg::NT)
+#ifdef MPGEMM_GROUPED
+gemm_grouped_pipe(GemmArgs args_in, GroupArgs groups)
+#else
 gemm_pipe(GemmArgs args_in)
+#endif
 {
     constexpr int BM = Cfg::BM, BN = Cfg::BN, BK = Cfg::BK, S = Cfg::STAGES;
     constexpr int FM = Cfg::FM, FN = Cfg::FN, KS = Cfg::KS;
@@ -623,6 +634,13 @@ gemm_pipe(GemmArgs args_in)
     const int wn = wl % Cfg::WAVES_N;
     const int ks0 = kgroup * Cfg::KSL;               // this group's first k-step of a tile
 
+#ifdef MPGEMM_GROUPED
+    // This workgroup's product and its tile of it.
+    GemmArgs args = args_in;
+    int tm, tn;
+    if (!locate_group<BM, BN, !A_ROW>(args, groups, tm, tn))
+        return;
+#else
     // Split-K: this workgroup's K range and partial-sum destination; the rest
     // of the kernel sees an ordinary product over that range.
     GemmArgs args = args_in;
@@ -646,6 +664,7 @@ gemm_pipe(GemmArgs args_in)
 
     int tm, tn;
     tile_coords(bid, nb, args.tiles_n, args.tiles_m, args.group_m, tm, tn);
+#endif
     const int64_t m0 = (int64_t)tm * BM;
     const int64_t n0 = (int64_t)tn * BN;
     // K tail: the copy loop covers the largest multiple of 8 of K, so every

@@ -1,0 +1,539 @@
+// ops.hip -- host side of the operators beside the GEMM (include/mpgemm_ops.h):
+// argument validation, the choice of kernel, launches.
+#include "mpgemm_ops.h"
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+// The GEMM's device code, compiled here for grouped launches, in a namespace
+// of its own: a program may link both libraries.
+#define MPGEMM_GROUPED
+#define mpg mpg_ops
+#include "kernels.hpp"
+
+namespace mpg {
+#include "i8_kernels.hpp"
+#include "token_kernels.hpp"
+}  // namespace mpg
+
+namespace {
+
+using mpg::GemmArgs;
+using mpg::GroupArgs;
+using mpg::I8Args;
+using mpg::I8Cfg;
+using mpg::kColMajor;
+using mpg::kInBF16;
+using mpg::kInF16;
+using mpg::kRowMajor;
+using mpg::PipeCfg;
+
+constexpr int64_t kMax32 = 0x7FFFFFFF;
+constexpr int64_t kMaxSpan = 0x7FFFFFF0;  // bytes a 32-bit buffer offset may reach
+
+int64_t at_least_one(int64_t v) { return v > 1 ? v : 1; }
+int64_t cdiv(int64_t a, int64_t b) { return a / b + (a % b != 0); }
+
+// Saturating product and sum of sizes >= 0: a saturated value fails every
+// limit it is compared with.
+int64_t mul_sat(int64_t a, int64_t b)
+{
+    if (a == 0 || b == 0)
+        return 0;
+    return a > INT64_MAX / b ? INT64_MAX : a * b;
+}
+int64_t add_sat(int64_t a, int64_t b) { return a > INT64_MAX - b ? INT64_MAX : a + b; }
+
+bool aligned(const void *p, int64_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (uint64_t)(bytes - 1)) == 0; }
+
+bool is_type(int t) { return t == MPGEMM_T_F16 || t == MPGEMM_T_BF16 || t == MPGEMM_T_F32; }
+int64_t size_of(int t) { return t == MPGEMM_T_F32 ? 4 : 2; }
+
+hipStream_t stream_of(void *s) { return reinterpret_cast<hipStream_t>(s); }
+
+// An error left by an earlier, unrelated call must not be reported as ours.
+void forget_error() { (void)hipGetLastError(); }
+int launched() { return hipGetLastError() == hipSuccess ? MPGEMM_OK : MPGEMM_ELAUNCH; }
+
+// Do `rows` stored rows of `width` elements, `ld` apart, fit 32-bit buffer
+// offsets?
+bool span_fits(int64_t rows, int64_t ld, int64_t width, int64_t bytes)
+{
+    return mul_sat(add_sat(mul_sat(rows, ld), width), bytes) < kMaxSpan;
+}
+
+// M tiles of at most `bm` rows that any split of `rows` rows into `groups`
+// ranges can make.
+int64_t row_tiles(int64_t rows, int64_t groups, int64_t bm)
+{
+    if (groups <= 1)
+        return cdiv(rows, bm);
+    const int64_t most = (rows + groups * (bm - 1)) / bm;
+    return most < rows ? most : rows;
+}
+
+// ---------------------------------------------------------------------------
+// Products of 8-bit codes
+// ---------------------------------------------------------------------------
+using i8_launch = void (*)(const I8Args &, dim3, hipStream_t);
+
+template <class Cfg, int OUT>
+void launch_i8(const I8Args &a, dim3 grid, hipStream_t s)
+{
+    hipLaunchKernelGGL((mpg::i8_tile<Cfg, OUT>), grid, dim3(Cfg::NT), 0, s, a);
+}
+
+struct I8Entry {
+    int bm, bn, bkb;
+    i8_launch launch[3];  // by output type
+};
+
+template <class Cfg>
+constexpr I8Entry i8_entry()
+{
+    return I8Entry{Cfg::BM, Cfg::BN, Cfg::BKB,
+                   {&launch_i8<Cfg, mpg::kTF16>, &launch_i8<Cfg, mpg::kTBF16>, &launch_i8<Cfg, mpg::kTF32>}};
+}
+
+const I8Entry kI8Table[] = {
+    i8_entry<I8Cfg<64, 64, 128, 2, 2, 2>>(),
+};
+
+// ---------------------------------------------------------------------------
+// Grouped 16-bit products
+// ---------------------------------------------------------------------------
+using grouped_launch = void (*)(const GemmArgs &, const GroupArgs &, dim3, hipStream_t);
+
+struct GroupedEntry {
+    int bm, bn, bk;
+    grouped_launch launch;
+};
+
+template <class Cfg>
+void launch_grouped(const GemmArgs &a, const GroupArgs &g, dim3 grid, hipStream_t s)
+{
+    hipLaunchKernelGGL((mpg::gemm_grouped_pipe<Cfg>), grid, dim3(Cfg::NT), 0, s, a, g);
+}
+
+template <class Cfg>
+constexpr GroupedEntry grouped_entry()
+{
+    return GroupedEntry{Cfg::BM, Cfg::BN, Cfg::BK, &launch_grouped<Cfg>};
+}
+
+template <int LA, int LB, int IN>
+const GroupedEntry *grouped_table()
+{
+    static constexpr GroupedEntry table[] = {
+        grouped_entry<PipeCfg<64, 64, 64, 2, 2, 2, LA, LB, IN>>(),
+    };
+    return table;
+}
+
+const GroupedEntry *grouped_family(int la, int lb, int in)
+{
+    if (la == kColMajor)
+        return in == kInBF16 ? grouped_table<kColMajor, kRowMajor, kInBF16>()
+                             : grouped_table<kColMajor, kRowMajor, kInF16>();
+    if (lb == kColMajor)
+        return in == kInBF16 ? grouped_table<kRowMajor, kColMajor, kInBF16>()
+                             : grouped_table<kRowMajor, kColMajor, kInF16>();
+    return in == kInBF16 ? grouped_table<kRowMajor, kRowMajor, kInBF16>()
+                         : grouped_table<kRowMajor, kRowMajor, kInF16>();
+}
+
+bool grouped_fits(const GroupedEntry &e, int la, int lb, int64_t lda, int64_t ldb, int64_t ldc)
+{
+    return (la == kRowMajor ? span_fits(e.bm, lda, e.bk, 2) : span_fits(e.bk, lda, e.bm, 2)) &&
+           (lb == kRowMajor ? span_fits(e.bk, ldb, e.bn, 2) : span_fits(e.bn, ldb, e.bk, 2)) &&
+           span_fits(e.bm, ldc, e.bn, 4);
+}
+
+// ---------------------------------------------------------------------------
+// Launches of the row kernels by type
+// ---------------------------------------------------------------------------
+template <int XT>
+void launch_quantize(const mpg::QuantArgs &a, hipStream_t s)
+{
+    hipLaunchKernelGGL((mpg::quantize_rows<XT, 256>), dim3((unsigned)a.R), dim3(256), 0, s, a);
+}
+
+template <int YT>
+void launch_combine(int o_type, const mpg::CombineArgs &a, dim3 grid, hipStream_t s)
+{
+    if (o_type == MPGEMM_T_F16)
+        hipLaunchKernelGGL((mpg::combine_rows<YT, mpg::kTF16>), grid, dim3(256), 0, s, a);
+    else if (o_type == MPGEMM_T_BF16)
+        hipLaunchKernelGGL((mpg::combine_rows<YT, mpg::kTBF16>), grid, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((mpg::combine_rows<YT, mpg::kTF32>), grid, dim3(256), 0, s, a);
+}
+
+template <int DT, int YT>
+void launch_combine_backward(int g_type, const mpg::CombineBackArgs &a, dim3 grid, hipStream_t s)
+{
+    if (g_type == MPGEMM_T_F16)
+        hipLaunchKernelGGL((mpg::combine_rows_backward<DT, YT, mpg::kTF16>), grid, dim3(256), 0, s, a);
+    else if (g_type == MPGEMM_T_BF16)
+        hipLaunchKernelGGL((mpg::combine_rows_backward<DT, YT, mpg::kTBF16>), grid, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((mpg::combine_rows_backward<DT, YT, mpg::kTF32>), grid, dim3(256), 0, s, a);
+}
+
+template <int DT>
+void launch_combine_backward(int y_type, int g_type, const mpg::CombineBackArgs &a, dim3 grid, hipStream_t s)
+{
+    if (y_type == MPGEMM_T_F16)
+        launch_combine_backward<DT, mpg::kTF16>(g_type, a, grid, s);
+    else if (y_type == MPGEMM_T_BF16)
+        launch_combine_backward<DT, mpg::kTBF16>(g_type, a, grid, s);
+    else
+        launch_combine_backward<DT, mpg::kTF32>(g_type, a, grid, s);
+}
+
+// Pairs one workgroup sorts alone.
+constexpr int64_t kRouteOne = 4096;
+
+struct RoutePlan {
+    int64_t blocks, per_wave;
+};
+
+RoutePlan plan_route(int64_t pairs)
+{
+    if (pairs <= kRouteOne)
+        return RoutePlan{1, cdiv(cdiv(pairs, mpg::kRouteWaves), 64) * 64};
+    int64_t blocks = cdiv(pairs, 2048);
+    if (blocks > 256)
+        blocks = 256;
+    const int64_t per_wave = cdiv(cdiv(pairs, blocks * mpg::kRouteWaves), 64) * 64;
+    return RoutePlan{cdiv(pairs, per_wave * mpg::kRouteWaves), per_wave};
+}
+
+template <int WIDE>
+void launch_route(const mpg::RouteArgs &a, int64_t blocks, hipStream_t s)
+{
+    const size_t one = (size_t)(a.E + 1) * 4;
+    const size_t lds = one * (mpg::kRouteWaves + 1) + mpg::kRouteWaves * 4;
+    if (blocks == 1) {
+        hipLaunchKernelGGL(mpg::route_one<WIDE>, dim3(1), dim3(mpg::kRouteThreads), lds, s, a);
+        return;
+    }
+    hipLaunchKernelGGL(mpg::route_hist<WIDE>, dim3((unsigned)blocks), dim3(mpg::kRouteThreads), one, s, a);
+    hipLaunchKernelGGL(mpg::route_place_blocks<WIDE>, dim3((unsigned)blocks), dim3(mpg::kRouteThreads), lds, s, a);
+}
+
+}  // namespace
+
+extern "C" {
+
+int mpgemm_quantize_rows(int x_type, int64_t T, int64_t H, const void *X, int64_t ldx,
+                         const int32_t *order, int64_t R, int64_t top_k,
+                         int8_t *Q, int64_t ldq, float *scale, void *stream)
+{
+    if (!is_type(x_type))
+        return MPGEMM_ETYPE;
+    if (T < 0 || H < 0 || R < 0 || T > kMax32 || H > kMax32 || R > kMax32)
+        return MPGEMM_EDIM;
+    if (order ? (top_k < 1 || top_k > kMax32) : R != T)
+        return MPGEMM_EDIM;
+    if (ldx < at_least_one(H) || ldq < at_least_one(H))
+        return MPGEMM_ELD;
+    if (R == 0)
+        return MPGEMM_OK;
+    if (scale == nullptr || (H > 0 && (Q == nullptr || (T > 0 && X == nullptr))))
+        return MPGEMM_ENULL;
+    if (!aligned(X, size_of(x_type)) || !aligned(order, 4) || !aligned(scale, 4))
+        return MPGEMM_EALIGN;
+    const mpg::QuantArgs a{X, Q, scale, order, ldx, ldq, (int32_t)T, (int32_t)H, (int32_t)R, (int32_t)top_k};
+    forget_error();
+    if (x_type == MPGEMM_T_F16)
+        launch_quantize<mpg::kTF16>(a, stream_of(stream));
+    else if (x_type == MPGEMM_T_BF16)
+        launch_quantize<mpg::kTBF16>(a, stream_of(stream));
+    else
+        launch_quantize<mpg::kTF32>(a, stream_of(stream));
+    return launched();
+}
+
+int mpgemm_i8_gemm(int out_type, int64_t groups, int64_t M, int64_t N, int64_t K,
+                   const int8_t *A, int64_t lda, const int8_t *W, int64_t ldw, int64_t stride_w,
+                   void *C, int64_t ldc, const float *scale_a, const float *scale_w,
+                   const float *bias, const int32_t *offsets, void *stream)
+{
+    if (!is_type(out_type))
+        return MPGEMM_ETYPE;
+    if (groups < 1 || groups > MPGEMM_MAX_GROUPS || M < 0 || N < 0 || K < 0 || M > kMax32 || N > kMax32 ||
+        K > MPGEMM_I8_MAX_K)
+        return MPGEMM_EDIM;
+    if (lda < at_least_one(K) || ldw < at_least_one(K) || ldc < at_least_one(N) || stride_w < 0)
+        return MPGEMM_ELD;
+    if (M == 0 || N == 0)
+        return MPGEMM_OK;
+    if (C == nullptr || scale_a == nullptr || scale_w == nullptr || (K > 0 && (A == nullptr || W == nullptr)) ||
+        (groups > 1 && offsets == nullptr))
+        return MPGEMM_ENULL;
+    if (!aligned(C, size_of(out_type)) || !aligned(scale_a, 4) || !aligned(scale_w, 4) || !aligned(bias, 4) ||
+        !aligned(offsets, 4))
+        return MPGEMM_EALIGN;
+    const I8Entry &e = kI8Table[0];
+    if (!span_fits(e.bm, lda, K, 1) || !span_fits(e.bn, ldw, K, 1))
+        return MPGEMM_ELD;
+    const int64_t tiles_n = cdiv(N, e.bn);
+    const int64_t grid = mul_sat(offsets ? row_tiles(M, groups, e.bm) : cdiv(M, e.bm), tiles_n);
+    if (grid > kMax32 / 64)
+        return MPGEMM_EDIM;
+    I8Args a{};
+    a.A = A;
+    a.W = W;
+    a.C = C;
+    a.scale_a = scale_a;
+    a.scale_w = scale_w;
+    a.bias = bias;
+    a.lda = lda;
+    a.ldw = ldw;
+    a.ldc = ldc;
+    a.N = (int32_t)N;
+    a.K = (int32_t)K;
+    a.tiles_n = (int32_t)tiles_n;
+    a.group_m = 8;
+    a.groups = GroupArgs{offsets, (int32_t)groups, (int32_t)M, stride_w};
+    forget_error();
+    e.launch[out_type](a, dim3((unsigned)grid), stream_of(stream));
+    return launched();
+}
+
+int64_t mpgemm_route_workspace(int64_t pairs, int64_t experts)
+{
+    if (pairs < 0 || pairs > ((int64_t)1 << 30) || experts < 1 || experts > MPGEMM_MAX_GROUPS)
+        return MPGEMM_EDIM;
+    const RoutePlan p = plan_route(pairs);
+    return p.blocks == 1 || pairs == 0 ? 0 : p.blocks * (experts + 1) * 4;
+}
+
+int mpgemm_route(int id_type, int64_t pairs, int64_t experts, const void *ids,
+                 int32_t *order, int32_t *position, int32_t *offsets,
+                 void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (id_type != MPGEMM_ID_I32 && id_type != MPGEMM_ID_I64)
+        return MPGEMM_ETYPE;
+    const int64_t need = mpgemm_route_workspace(pairs, experts);
+    if (need < 0)
+        return MPGEMM_EDIM;
+    if (offsets == nullptr || (pairs > 0 && (ids == nullptr || order == nullptr || position == nullptr)))
+        return MPGEMM_ENULL;
+    if (!aligned(ids, id_type == MPGEMM_ID_I64 ? 8 : 4) || !aligned(order, 4) || !aligned(position, 4) ||
+        !aligned(offsets, 4) || !aligned(workspace, 4))
+        return MPGEMM_EALIGN;
+    if (need > 0 && workspace == nullptr)
+        return MPGEMM_ENULL;
+    if (workspace_bytes < need)
+        return MPGEMM_EWORKSPACE;
+    forget_error();
+    if (pairs == 0) {
+        hipLaunchKernelGGL(mpg::route_none, dim3(1), dim3(mpg::kRouteThreads), 0, stream_of(stream), offsets,
+                           (int)experts);
+        return launched();
+    }
+    const RoutePlan p = plan_route(pairs);
+    mpg::RouteArgs a{};
+    a.ids = ids;
+    a.order = order;
+    a.position = position;
+    a.offsets = offsets;
+    a.hist = static_cast<int32_t *>(workspace);
+    a.pairs = (int32_t)pairs;
+    a.E = (int32_t)experts;
+    a.bits = 32 - __builtin_clz((unsigned)experts);
+    a.per_wave = (int32_t)p.per_wave;
+    if (id_type == MPGEMM_ID_I64)
+        launch_route<1>(a, p.blocks, stream_of(stream));
+    else
+        launch_route<0>(a, p.blocks, stream_of(stream));
+    return launched();
+}
+
+int mpgemm_gather_rows(int type, int64_t T, int64_t H, const void *X, int64_t ldx,
+                       const int32_t *order, int64_t R, int64_t top_k,
+                       void *Y, int64_t ldy, void *stream)
+{
+    if (!is_type(type))
+        return MPGEMM_ETYPE;
+    const int64_t es = size_of(type);
+    if (T < 0 || H < 0 || R < 0 || T > kMax32 || H > kMax32 / 4 || R > kMax32 || top_k < 1 || top_k > kMax32)
+        return MPGEMM_EDIM;
+    if (ldx < at_least_one(H) || ldy < at_least_one(H) || ldx > INT64_MAX / 4 || ldy > INT64_MAX / 4)
+        return MPGEMM_ELD;
+    if (R == 0 || H == 0)
+        return MPGEMM_OK;
+    if (order == nullptr || Y == nullptr || (T > 0 && X == nullptr))
+        return MPGEMM_ENULL;
+    if (!aligned(X, es) || !aligned(Y, es) || !aligned(order, 4))
+        return MPGEMM_EALIGN;
+    const mpg::GatherArgs a{static_cast<const uint8_t *>(X), static_cast<uint8_t *>(Y), order, ldx * es, ldy * es,
+                            (int32_t)T, (int32_t)R, (int32_t)top_k, (int32_t)(H * es)};
+    forget_error();
+    hipLaunchKernelGGL(mpg::gather_rows, dim3((unsigned)cdiv(R, 4)), dim3(256), 0, stream_of(stream), a);
+    return launched();
+}
+
+int mpgemm_combine_rows(int y_type, int o_type, int64_t T, int64_t top_k, int64_t H, int64_t R,
+                        const void *Y, int64_t ldy, const int32_t *position, const float *weights,
+                        void *O, int64_t ldo, void *stream)
+{
+    if (!is_type(y_type) || !is_type(o_type))
+        return MPGEMM_ETYPE;
+    if (T < 0 || H < 0 || R < 0 || top_k < 0 || T > kMax32 || H > kMax32 - 4096 || R > kMax32 || top_k > kMax32)
+        return MPGEMM_EDIM;
+    if (ldy < at_least_one(H) || ldo < at_least_one(H))
+        return MPGEMM_ELD;
+    if (T == 0 || H == 0)
+        return MPGEMM_OK;
+    if (O == nullptr || (top_k > 0 && (position == nullptr || (R > 0 && Y == nullptr))))
+        return MPGEMM_ENULL;
+    if (!aligned(Y, size_of(y_type)) || !aligned(O, size_of(o_type)) || !aligned(position, 4) || !aligned(weights, 4))
+        return MPGEMM_EALIGN;
+    const mpg::CombineArgs a{Y, O, position, weights, ldy, ldo, (int32_t)T, (int32_t)H, (int32_t)R, (int32_t)top_k};
+    const int64_t gy = cdiv(H, 1024);
+    const dim3 grid((unsigned)T, (unsigned)(gy < 65535 ? gy : 65535));
+    forget_error();
+    if (y_type == MPGEMM_T_F16)
+        launch_combine<mpg::kTF16>(o_type, a, grid, stream_of(stream));
+    else if (y_type == MPGEMM_T_BF16)
+        launch_combine<mpg::kTBF16>(o_type, a, grid, stream_of(stream));
+    else
+        launch_combine<mpg::kTF32>(o_type, a, grid, stream_of(stream));
+    return launched();
+}
+
+int mpgemm_combine_rows_backward(int d_type, int y_type, int dy_type,
+                                 int64_t T, int64_t top_k, int64_t H, int64_t R,
+                                 const void *dO, int64_t ldo, const void *Y, int64_t ldy,
+                                 const int32_t *position, const float *weights,
+                                 void *dY, int64_t lddy, float *dweights, void *stream)
+{
+    if (!is_type(d_type) || !is_type(y_type) || !is_type(dy_type))
+        return MPGEMM_ETYPE;
+    if (T < 0 || H < 0 || R < 0 || top_k < 0 || T > kMax32 || H > kMax32 || R > kMax32 || top_k > kMax32 ||
+        mul_sat(T, top_k) > kMax32)
+        return MPGEMM_EDIM;
+    if (ldo < at_least_one(H) || lddy < at_least_one(H) || (dweights && ldy < at_least_one(H)))
+        return MPGEMM_ELD;
+    if (T == 0 || top_k == 0)
+        return MPGEMM_OK;
+    if (position == nullptr || (H > 0 && (dO == nullptr || (R > 0 && (dY == nullptr || (dweights && Y == nullptr))))))
+        return MPGEMM_ENULL;
+    if (!aligned(dO, size_of(d_type)) || !aligned(dY, size_of(dy_type)) ||
+        (dweights && !aligned(Y, size_of(y_type))) || !aligned(position, 4) || !aligned(weights, 4) ||
+        !aligned(dweights, 4))
+        return MPGEMM_EALIGN;
+    const mpg::CombineBackArgs a{dO, Y, dY, dweights, position, weights, ldo, ldy, lddy,
+                                 (int32_t)T, (int32_t)H, (int32_t)R, (int32_t)top_k};
+    const dim3 grid((unsigned)cdiv(T * top_k, 4));
+    forget_error();
+    if (d_type == MPGEMM_T_F16)
+        launch_combine_backward<mpg::kTF16>(y_type, dy_type, a, grid, stream_of(stream));
+    else if (d_type == MPGEMM_T_BF16)
+        launch_combine_backward<mpg::kTBF16>(y_type, dy_type, a, grid, stream_of(stream));
+    else
+        launch_combine_backward<mpg::kTF32>(y_type, dy_type, a, grid, stream_of(stream));
+    return launched();
+}
+
+int mpgemm_grouped(int in_type, int layout_b, int64_t groups, int64_t R, int64_t N, int64_t K,
+                   const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb, int64_t stride_b,
+                   float *C, int64_t ldc, float alpha, float beta,
+                   const int32_t *offsets, void *stream)
+{
+    if (in_type != MPGEMM_IN_F16 && in_type != MPGEMM_IN_BF16)
+        return MPGEMM_ETYPE;
+    if (layout_b != MPGEMM_ROW_MAJOR && layout_b != MPGEMM_COL_MAJOR)
+        return MPGEMM_ELAYOUT;
+    if (groups < 1 || groups > MPGEMM_MAX_GROUPS || R < 0 || N < 0 || K < 0 || R > kMax32 || N > kMax32 || K > kMax32)
+        return MPGEMM_EDIM;
+    if (lda < at_least_one(K) || ldb < at_least_one(layout_b == MPGEMM_COL_MAJOR ? K : N) || ldc < at_least_one(N) ||
+        stride_b < 0)
+        return MPGEMM_ELD;
+    if (R == 0 || N == 0)
+        return MPGEMM_OK;
+    const bool reads = K > 0 && alpha != 0.0f;
+    if (C == nullptr || offsets == nullptr || (reads && (A == nullptr || B == nullptr)))
+        return MPGEMM_ENULL;
+    if (!aligned(C, 4) || !aligned(offsets, 4) || (reads && (!aligned(A, 2) || !aligned(B, 2))))
+        return MPGEMM_EALIGN;
+    const GroupedEntry &e = *grouped_family(kRowMajor, layout_b, in_type);
+    if (!grouped_fits(e, kRowMajor, layout_b, lda, ldb, ldc))
+        return MPGEMM_ELD;
+    const int64_t tiles_n = cdiv(N, e.bn);
+    const int64_t grid = mul_sat(row_tiles(R, groups, e.bm), tiles_n);
+    if (grid > kMax32 / 64)
+        return MPGEMM_EDIM;
+    GemmArgs a{};
+    a.A = A;
+    a.B = B;
+    a.C = C;
+    a.M = R;
+    a.N = N;
+    a.K = K;
+    a.lda = lda;
+    a.ldb = ldb;
+    a.ldc = ldc;
+    a.alpha = alpha;
+    a.beta = beta;
+    a.tiles_n = (int32_t)tiles_n;
+    a.group_m = 8;
+    a.splits = 1;
+    forget_error();
+    e.launch(a, GroupArgs{offsets, (int32_t)groups, (int32_t)R, stride_b}, dim3((unsigned)grid), stream_of(stream));
+    return launched();
+}
+
+int mpgemm_grouped_wgrad(int in_type, int64_t groups, int64_t R, int64_t M, int64_t N,
+                         const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb,
+                         float *C, int64_t ldc, int64_t stride_c, float alpha, float beta,
+                         const int32_t *offsets, void *stream)
+{
+    if (in_type != MPGEMM_IN_F16 && in_type != MPGEMM_IN_BF16)
+        return MPGEMM_ETYPE;
+    if (groups < 1 || groups > MPGEMM_MAX_GROUPS || R < 0 || M < 0 || N < 0 || R > kMax32 || M > kMax32 || N > kMax32)
+        return MPGEMM_EDIM;
+    if (lda < at_least_one(M) || ldb < at_least_one(N) || ldc < at_least_one(N) || stride_c < 0)
+        return MPGEMM_ELD;
+    if (M == 0 || N == 0)
+        return MPGEMM_OK;
+    // (one group's C may not run into the next one's)
+    if (groups > 1 && stride_c < add_sat(mul_sat(M - 1, ldc), N))
+        return MPGEMM_ELD;
+    const bool reads = R > 0 && alpha != 0.0f;
+    if (C == nullptr || offsets == nullptr || (reads && (A == nullptr || B == nullptr)))
+        return MPGEMM_ENULL;
+    if (!aligned(C, 4) || !aligned(offsets, 4) || (reads && (!aligned(A, 2) || !aligned(B, 2))))
+        return MPGEMM_EALIGN;
+    const GroupedEntry &e = *grouped_family(kColMajor, kRowMajor, in_type);
+    if (!grouped_fits(e, kColMajor, kRowMajor, lda, ldb, ldc))
+        return MPGEMM_ELD;
+    const int64_t tiles_m = cdiv(M, e.bm), tiles_n = cdiv(N, e.bn);
+    const int64_t grid = mul_sat(mul_sat(tiles_m, tiles_n), groups);
+    if (grid > kMax32 / 64)
+        return MPGEMM_EDIM;
+    GemmArgs a{};
+    a.A = A;
+    a.B = B;
+    a.C = C;
+    a.M = M;
+    a.N = N;
+    a.K = R;
+    a.lda = lda;
+    a.ldb = ldb;
+    a.ldc = ldc;
+    a.alpha = alpha;
+    a.beta = beta;
+    a.tiles_m = (int32_t)tiles_m;
+    a.tiles_n = (int32_t)tiles_n;
+    a.group_m = 8;
+    a.splits = 1;
+    forget_error();
+    e.launch(a, GroupArgs{offsets, (int32_t)groups, (int32_t)R, stride_c}, dim3((unsigned)grid), stream_of(stream));
+    return launched();
+}
+
+}  // extern "C"

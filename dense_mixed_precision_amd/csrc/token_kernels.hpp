@@ -1,0 +1,505 @@
+// token_kernels.hpp -- rows of tokens: 8-bit codes with a scale per row, the
+// order of (token, slot) pairs by expert, rows brought into that order and
+// back, and the gradients (gfx950).  Included by ops.hip in kernels.hpp's
+// namespace, after i8_kernels.hpp (element types).
+//
+// All of these stream their operands once; they are bound by HBM, and at
+// decoding sizes by the launch.  Index arrays are read as untrusted data:
+// an index outside the operands counts as absent.
+
+// Rows are read and written in vectors of 16 bytes at any element alignment.
+template <class E>
+struct VecOf {
+    static constexpr int N = 16 / sizeof(E);
+    typedef Pack<E, N> type;
+};
+
+// ---------------------------------------------------------------------------
+// Rows to 8-bit codes
+// ---------------------------------------------------------------------------
+// One row x: m = max|x|, scale = m/127, code = the whole number nearest
+// 127*x/m, the even one in the middle.  The quotient is compared exactly:
+// with x and m scaled by the power of two that brings m near 1 (exact),
+// p + lo = 127*x in two floats, q = rint(p*(1/m)) is off by one at most, and
+// d = p - q*m (one fma, exact: |d| is about m/2 and a multiple of the
+// operands' last places) plus lo against +-m/2 says which way.
+__device__ __forceinline__ int code_of(float x, float m, float inv)
+{
+    const float p = 127.0f * x;
+    const float lo = __builtin_fmaf(127.0f, x, -p);
+    float q = __builtin_rintf(p * inv);
+    const float d = __builtin_fmaf(-q, m, p);
+    const float h = 0.5f * m;
+    const float over = (d - h) + lo;    // > 0: above the middle of q and q + 1
+    const float under = (d + h) + lo;   // < 0: below the middle of q - 1 and q
+    const bool odd = ((int)q & 1) != 0;
+    if (over > 0.0f || (over == 0.0f && odd))
+        q += 1.0f;
+    else if (under < 0.0f || (under == 0.0f && odd))
+        q -= 1.0f;
+    return (int)q;
+}
+
+struct QuantArgs {
+    const void *X;
+    int8_t *Q;
+    float *scale;
+    const int32_t *order;    // or nullptr: row i of X
+    int64_t ldx, ldq;
+    int32_t T, H, R, top_k;
+};
+
+// One workgroup of NT threads per row.  The first CACHE vectors of each thread stay
+// in registers between the maximum and the codes; longer rows are read again.
+template <int XT, int NT>
+__global__ void __launch_bounds__(NT)
+quantize_rows(QuantArgs args)
+{
+    typedef typename ElemOf<XT>::type E;
+    constexpr int VN = VecOf<E>::N;
+    constexpr int CACHE = 4;
+    typedef typename VecOf<E>::type V;
+    __shared__ uint32_t part[NT / 64];
+    const int row = blockIdx.x;
+    int src = row;
+    if (args.order) {
+        const int pair = args.order[row];
+        src = pair < 0 ? -1 : pair / args.top_k;
+        if (src < 0 || src >= args.T)
+            return;  // no such row: what is there stays
+    }
+    const E *const x = (const E *)args.X + (int64_t)src * args.ldx;
+    const int H = args.H;
+    const int nv = H / VN;
+    V keep[CACHE];
+    uint32_t top = 0;  // |x| as bits: above every finite value for infinities and NaN
+    auto see = [&](E e) __attribute__((always_inline)) {
+        const float f = (float)e;
+        const uint32_t b = __builtin_bit_cast(uint32_t, f) & 0x7FFFFFFFu;
+        top = b > top ? b : top;
+    };
+#pragma unroll
+    for (int c = 0; c < CACHE; ++c) {
+        const int i = c * NT + threadIdx.x;
+        if (i < nv)
+            keep[c] = *(const V *)(x + (int64_t)i * VN);
+    }
+#pragma unroll
+    for (int c = 0; c < CACHE; ++c)
+        if (c * NT + (int)threadIdx.x < nv)
+#pragma unroll
+            for (int e = 0; e < VN; ++e)
+                see(keep[c].v[e]);
+    for (int i = CACHE * NT + threadIdx.x; i < nv; i += NT) {
+        const V v = *(const V *)(x + (int64_t)i * VN);
+#pragma unroll
+        for (int e = 0; e < VN; ++e)
+            see(v.v[e]);
+    }
+    for (int i = nv * VN + threadIdx.x; i < H; i += NT)
+        see(x[i]);
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) {
+        const uint32_t o = __shfl_xor((int)top, d);
+        top = o > top ? o : top;
+    }
+    if constexpr (NT > 64) {
+        if ((threadIdx.x & 63) == 0)
+            part[threadIdx.x / 64] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < NT / 64; ++w)
+            top = part[w] > top ? part[w] : top;
+    }
+    const float most = __builtin_bit_cast(float, top);
+    const bool finite = top < 0x7F800000u;
+    const bool live = finite && top != 0;
+    // the power of two that brings the maximum to [1, 2), as far as one
+    // float holds it
+    int ex = (int)(top >> 23) - 127;
+    ex = ex < -100 ? -100 : ex > 126 ? 126 : ex;
+    const float f = __builtin_bit_cast(float, (uint32_t)(127 - ex) << 23);
+    const float m = live ? most * f : 1.0f;
+    const float inv = 1.0f / m;
+    if (threadIdx.x == 0)
+        args.scale[row] = finite ? most / 127.0f : __builtin_nanf("");
+    int8_t *const q = args.Q + (int64_t)row * args.ldq;
+    auto code = [&](E e) __attribute__((always_inline)) {
+        return live ? code_of((float)e * f, m, inv) : 0;
+    };
+    auto emit = [&](int i, const V &v) __attribute__((always_inline)) {
+        Pack<int8_t, VN> o;
+#pragma unroll
+        for (int e = 0; e < VN; ++e)
+            o.v[e] = (int8_t)code(v.v[e]);
+        *(Pack<int8_t, VN> *)(q + (int64_t)i * VN) = o;
+    };
+#pragma unroll
+    for (int c = 0; c < CACHE; ++c)
+        if (c * NT + (int)threadIdx.x < nv)
+            emit(c * NT + threadIdx.x, keep[c]);
+    for (int i = CACHE * NT + threadIdx.x; i < nv; i += NT)
+        emit(i, *(const V *)(x + (int64_t)i * VN));
+    for (int i = nv * VN + threadIdx.x; i < H; i += NT)
+        q[i] = (int8_t)code(x[i]);
+}
+
+// ---------------------------------------------------------------------------
+// The order of pairs by expert
+// ---------------------------------------------------------------------------
+// A stable counting sort of `pairs` expert ids into experts 0 .. E-1; ids
+// outside are class E, behind the last expert.  order[p] = pair at sorted
+// position p (-1 behind the last expert), position[pair] = p (-1: no expert),
+// offsets[e] = first position of expert e.
+//
+// Each wave owns consecutive pairs and a row of counters in LDS, so equal
+// experts keep their order without atomics whose order matters: within 64
+// pairs the lanes of one expert are found by ballots over the id's bits, and
+// the counts before a lane are its rank.
+struct RouteArgs {
+    const void *ids;
+    int32_t *order, *position, *offsets;
+    int32_t *hist;      // [blocks][E + 1] counts (several blocks)
+    int32_t pairs, E, bits;
+    int32_t per_wave;   // pairs per wave, a multiple of 64
+};
+
+constexpr int kRouteWaves = 4;
+constexpr int kRouteThreads = 64 * kRouteWaves;
+
+template <int WIDE>
+__device__ __forceinline__ int expert_of(const RouteArgs &a, int i)
+{
+    if constexpr (WIDE != 0) {
+        const int64_t e = ((const int64_t *)a.ids)[i];
+        return e >= 0 && e < a.E ? (int)e : a.E;
+    } else {
+        const int32_t e = ((const int32_t *)a.ids)[i];
+        return e >= 0 && e < a.E ? e : a.E;
+    }
+}
+
+// Counts of one wave's pairs into its LDS row (zeroed here).
+template <int WIDE>
+__device__ __forceinline__ void route_count(const RouteArgs &a, int32_t *cnt, int first, int last, int lane)
+{
+    for (int e = lane; e <= a.E; e += 64)
+        cnt[e] = 0;
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    for (int i = first + lane; i < last; i += 64)
+        atomicAdd(&cnt[expert_of<WIDE>(a, i)], 1);
+}
+
+// Positions of one wave's pairs, from the counters at their first positions.
+template <int WIDE>
+__device__ __forceinline__ void route_place(const RouteArgs &a, int32_t *cnt, int first, int last, int lane)
+{
+    for (int i0 = first; i0 < last; i0 += 64) {
+        const int i = i0 + lane;
+        const bool ok = i < last;
+        const int e = ok ? expert_of<WIDE>(a, i) : a.E;
+        uint64_t same = __ballot(ok);
+        for (int b = 0; b < a.bits; ++b) {
+            const uint64_t set = __ballot((e >> b) & 1);
+            same &= ((e >> b) & 1) ? set : ~set;
+        }
+        const int rank = __builtin_popcountll(same & ((1ull << lane) - 1));
+        int base = 0;
+        if (ok && rank == 0)
+            base = atomicAdd(&cnt[e], __builtin_popcountll(same));
+        base = __shfl(base, ok ? __builtin_ctzll(same) : lane);
+        if (ok) {
+            const int p = base + rank;
+            a.order[p] = e < a.E ? i : -1;
+            a.position[i] = e < a.E ? p : -1;
+        }
+    }
+}
+
+// Exclusive prefix sum over the E + 1 values of `v` in LDS, by one workgroup
+// of kRouteThreads (each thread a run of consecutive values).
+__device__ __forceinline__ void route_scan(int32_t *v, int count, int32_t *sums)
+{
+    const int t = threadIdx.x;
+    const int per = (count + kRouteThreads - 1) / kRouteThreads;
+    const int lo = t * per < count ? t * per : count;
+    const int hi = lo + per < count ? lo + per : count;
+    int total = 0;
+    for (int i = lo; i < hi; ++i)
+        total += v[i];
+    int incl = total;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(incl, d);
+        if ((t & 63) >= d)
+            incl += o;
+    }
+    if ((t & 63) == 63)
+        sums[t / 64] = incl;
+    __syncthreads();
+    int before = incl - total;
+    for (int w = 0; w < t / 64; ++w)
+        before += sums[w];
+    for (int i = lo; i < hi; ++i) {
+        const int x = v[i];
+        v[i] = before;
+        before += x;
+    }
+    __syncthreads();
+}
+
+extern __shared__ int32_t route_lds[];
+
+// Few pairs: the whole sort by one workgroup.
+template <int WIDE>
+__global__ void __launch_bounds__(kRouteThreads)
+route_one(RouteArgs a)
+{
+    int32_t *const cnt = route_lds;                          // [waves][E + 1]
+    int32_t *const first = cnt + kRouteWaves * (a.E + 1);    // [E + 1]
+    int32_t *const sums = first + a.E + 1;                   // [waves]
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lo = min(wave * a.per_wave, a.pairs), hi = min(lo + a.per_wave, a.pairs);
+    route_count<WIDE>(a, cnt + wave * (a.E + 1), lo, hi, lane);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= a.E; e += kRouteThreads) {
+        int total = 0;
+        for (int w = 0; w < kRouteWaves; ++w)
+            total += cnt[w * (a.E + 1) + e];
+        first[e] = total;
+    }
+    __syncthreads();
+    route_scan(first, a.E + 1, sums);
+    for (int e = threadIdx.x; e <= a.E; e += kRouteThreads) {
+        int at = first[e];
+        a.offsets[e] = at;
+        for (int w = 0; w < kRouteWaves; ++w) {
+            const int n = cnt[w * (a.E + 1) + e];
+            cnt[w * (a.E + 1) + e] = at;
+            at += n;
+        }
+    }
+    __syncthreads();
+    route_place<WIDE>(a, cnt + wave * (a.E + 1), lo, hi, lane);
+}
+
+// Many pairs, first launch: each workgroup's counts per expert.
+template <int WIDE>
+__global__ void __launch_bounds__(kRouteThreads)
+route_hist(RouteArgs a)
+{
+    int32_t *const cnt = route_lds;  // [E + 1]
+    const int lo = min((int64_t)blockIdx.x * kRouteWaves * a.per_wave, (int64_t)a.pairs);
+    const int hi = min((int64_t)lo + kRouteWaves * a.per_wave, (int64_t)a.pairs);
+    for (int e = threadIdx.x; e <= a.E; e += kRouteThreads)
+        cnt[e] = 0;
+    __syncthreads();
+    for (int i = lo + threadIdx.x; i < hi; i += kRouteThreads)
+        atomicAdd(&cnt[expert_of<WIDE>(a, i)], 1);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= a.E; e += kRouteThreads)
+        a.hist[(int64_t)blockIdx.x * (a.E + 1) + e] = cnt[e];
+}
+
+// Second launch: every workgroup sums the counts of all and of those before
+// it, and places its pairs.
+template <int WIDE>
+__global__ void __launch_bounds__(kRouteThreads)
+route_place_blocks(RouteArgs a)
+{
+    int32_t *const cnt = route_lds;                          // [waves][E + 1]
+    int32_t *const first = cnt + kRouteWaves * (a.E + 1);    // [E + 1]
+    int32_t *const sums = first + a.E + 1;                   // [waves]
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t begin = ((int64_t)blockIdx.x * kRouteWaves + wave) * a.per_wave;
+    const int lo = (int)min(begin, (int64_t)a.pairs), hi = (int)min(begin + a.per_wave, (int64_t)a.pairs);
+    route_count<WIDE>(a, cnt + wave * (a.E + 1), lo, hi, lane);
+    int before[8];  // this thread's experts' counts in the blocks before (E + 1 <= 8 * threads)
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+        const int e = s * kRouteThreads + threadIdx.x;
+        before[s] = 0;
+        if (e <= a.E) {
+            int total = 0;
+#pragma unroll 8
+            for (int b = 0; b < (int)gridDim.x; ++b) {
+                const int n = a.hist[(int64_t)b * (a.E + 1) + e];
+                total += n;
+                before[s] += b < (int)blockIdx.x ? n : 0;
+            }
+            first[e] = total;
+        }
+    }
+    __syncthreads();
+    route_scan(first, a.E + 1, sums);
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+        const int e = s * kRouteThreads + threadIdx.x;
+        if (e <= a.E) {
+            int at = first[e];
+            if (blockIdx.x == 0)
+                a.offsets[e] = at;
+            at += before[s];
+            for (int w = 0; w < kRouteWaves; ++w) {
+                const int n = cnt[w * (a.E + 1) + e];
+                cnt[w * (a.E + 1) + e] = at;
+                at += n;
+            }
+        }
+    }
+    __syncthreads();
+    route_place<WIDE>(a, cnt + wave * (a.E + 1), lo, hi, lane);
+}
+
+// No pairs: every expert starts at 0.
+__global__ void __launch_bounds__(kRouteThreads)
+route_none(int32_t *offsets, int E)
+{
+    for (int e = threadIdx.x; e <= E; e += kRouteThreads)
+        offsets[e] = 0;
+}
+
+// ---------------------------------------------------------------------------
+// Rows into expert order, and back
+// ---------------------------------------------------------------------------
+struct GatherArgs {
+    const uint8_t *X;
+    uint8_t *Y;
+    const int32_t *order;
+    int64_t ldx, ldy;        // bytes
+    int32_t T, R, top_k;
+    int32_t row_bytes;
+};
+
+typedef Pack<uint8_t, 16> Bytes16;
+
+// Y[p] = X[order[p] / top_k]: one wave per row.
+__global__ void __launch_bounds__(256)
+gather_rows(GatherArgs a)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t p = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (p >= a.R)
+        return;
+    const int pair = a.order[p];
+    const int t = pair < 0 ? -1 : pair / a.top_k;
+    if (t < 0 || t >= a.T)
+        return;
+    const uint8_t *const x = a.X + (int64_t)t * a.ldx;
+    uint8_t *const y = a.Y + p * a.ldy;
+    const int nv = a.row_bytes / 16;
+    for (int i = lane; i < nv; i += 64)
+        *(Bytes16 *)(y + (int64_t)i * 16) = *(const Bytes16 *)(x + (int64_t)i * 16);
+    for (int i = nv * 16 + lane; i < a.row_bytes; i += 64)
+        y[i] = x[i];
+}
+
+struct CombineArgs {
+    const void *Y;           // R x H, the experts' rows
+    void *O;                 // T x H
+    const int32_t *position; // T x top_k
+    const float *weights;    // T x top_k, or nullptr: ones
+    int64_t ldy, ldo;
+    int32_t T, H, R, top_k;
+};
+
+// O[t] = sum_s weights[t][s] * Y[position[t][s]], in FP32, slots ascending;
+// one thread per 4 columns of a token.
+template <int YT, int OT>
+__global__ void __launch_bounds__(256)
+combine_rows(CombineArgs a)
+{
+    typedef typename ElemOf<YT>::type EY;
+    typedef typename ElemOf<OT>::type EO;
+    const int64_t t = blockIdx.x;
+    for (int c = 4 * (blockIdx.y * 256 + threadIdx.x); c < a.H; c += 4 * 256 * gridDim.y) {
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = 0; s < a.top_k; ++s) {
+            const int p = a.position[t * a.top_k + s];
+            if (p < 0 || p >= a.R)
+                continue;
+            const float w = a.weights ? a.weights[t * a.top_k + s] : 1.0f;
+            const EY *const y = (const EY *)a.Y + (int64_t)p * a.ldy + c;
+            if (c + 4 <= a.H) {
+                const Pack<EY, 4> v = *(const Pack<EY, 4> *)y;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[e] = __builtin_fmaf(w, (float)v.v[e], acc[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < a.H)
+                        acc[e] = __builtin_fmaf(w, (float)y[e], acc[e]);
+            }
+        }
+        i8_store<OT, 4>((EO *)a.O + t * a.ldo, c, a.H - c, acc);
+    }
+}
+
+struct CombineBackArgs {
+    const void *dO;          // T x H
+    const void *Y;           // R x H, or nullptr with dweights
+    void *dY;                // R x H
+    float *dweights;         // T x top_k, or nullptr
+    const int32_t *position;
+    const float *weights;
+    int64_t ldo, ldy, lddy;
+    int32_t T, H, R, top_k;
+};
+
+// Of each pair (t, s) with a position p: dY[p] = weights[t][s] * dO[t] and
+// dweights[t][s] = <dO[t], Y[p]>, the products summed in FP32; a pair without
+// one has dweights 0.  One wave per pair; the slots of a token are
+// neighbours, so dO[t] comes from memory once.
+template <int DT, int YT, int GT>
+__global__ void __launch_bounds__(256)
+combine_rows_backward(CombineBackArgs a)
+{
+    typedef typename ElemOf<DT>::type ED;
+    typedef typename ElemOf<YT>::type EY;
+    typedef typename ElemOf<GT>::type EG;
+    constexpr int VN = 8;
+    const int lane = threadIdx.x & 63;
+    const int64_t pair = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (pair >= (int64_t)a.T * a.top_k)
+        return;
+    const int p = a.position[pair];
+    if (p < 0 || p >= a.R) {
+        if (a.dweights && lane == 0)
+            a.dweights[pair] = 0.0f;
+        return;
+    }
+    const float w = a.weights ? a.weights[pair] : 1.0f;
+    const ED *const d = (const ED *)a.dO + (pair / a.top_k) * a.ldo;
+    const EY *const y = (const EY *)a.Y + (int64_t)p * a.ldy;
+    EG *const g = (EG *)a.dY + (int64_t)p * a.lddy;
+    const int nv = a.H / VN;
+    float dot = 0.0f;
+    for (int i = lane; i < nv; i += 64) {
+        const Pack<ED, VN> dv = *(const Pack<ED, VN> *)(d + (int64_t)i * VN);
+        Pack<EG, VN> gv;
+        if (a.dweights) {
+            const Pack<EY, VN> yv = *(const Pack<EY, VN> *)(y + (int64_t)i * VN);
+#pragma unroll
+            for (int e = 0; e < VN; ++e)
+                dot = __builtin_fmaf((float)dv.v[e], (float)yv.v[e], dot);
+        }
+#pragma unroll
+        for (int e = 0; e < VN; ++e)
+            gv.v[e] = (EG)(w * (float)dv.v[e]);
+        *(Pack<EG, VN> *)(g + (int64_t)i * VN) = gv;
+    }
+    for (int i = nv * VN + lane; i < a.H; i += 64) {
+        const float dv = (float)d[i];
+        if (a.dweights)
+            dot = __builtin_fmaf(dv, (float)y[i], dot);
+        g[i] = (EG)(w * dv);
+    }
+    if (a.dweights) {
+#pragma unroll
+        for (int s = 32; s > 0; s /= 2)
+            dot += __shfl_xor(dot, s);
+        if (lane == 0)
+            a.dweights[pair] = dot;
+    }
+}
