@@ -38,7 +38,7 @@ PROBES_SRC = os.path.join(CSRC, "probes.hip")
 DEPS = [SRC, os.path.join(CSRC, "kernels.hpp"), os.path.join(ROOT, "include", "mpgemm.h")]
 OPS_SRC = os.path.join(CSRC, "ops.hip")
 OPS_DEPS = [OPS_SRC, os.path.join(ROOT, "include", "mpgemm_ops.h"), *DEPS[1:],
-            *(os.path.join(CSRC, f) for f in ("groups.hpp", "i8_kernels.hpp", "token_kernels.hpp"))]
+            *(os.path.join(CSRC, f) for f in ("groups.hpp", "i8_kernels.hpp", "narrow_rows.hpp", "token_kernels.hpp"))]
 LIB = os.path.join(HERE, "libmpgemm.so")
 OPS_LIB = os.path.join(HERE, "libmpgemm_ops.so")
 PROBES_LIB = os.path.join(HERE, "libmpgemm_probes.so")

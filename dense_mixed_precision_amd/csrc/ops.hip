@@ -13,6 +13,7 @@
 
 namespace mpg {
 #include "i8_kernels.hpp"
+#include "narrow_rows.hpp"
 #include "token_kernels.hpp"
 }  // namespace mpg
 
@@ -28,6 +29,7 @@ using mpg::kInF16;
 using mpg::kRowMajor;
 using mpg::PipeCfg;
 
+constexpr int kNumCu = 256;
 constexpr int64_t kMax32 = 0x7FFFFFFF;
 constexpr int64_t kMaxSpan = 0x7FFFFFF0;  // bytes a 32-bit buffer offset may reach
 
@@ -96,8 +98,49 @@ constexpr I8Entry i8_entry()
 }
 
 const I8Entry kI8Table[] = {
-    i8_entry<I8Cfg<64, 64, 128, 2, 2, 2>>(),
+    i8_entry<I8Cfg<256, 256, 128, 2, 4, 2>>(),
+    i8_entry<I8Cfg<128, 128, 128, 2, 4, 3>>(),
+    i8_entry<I8Cfg<64, 64, 256, 2, 2, 2>>(),
 };
+enum : int { kI8Big = 0, kI8Mid = 1, kI8Small = 2 };
+
+bool i8_fits(const I8Entry &e, int64_t lda, int64_t ldw, int64_t K)
+{
+    return span_fits(e.bm, lda, K, 1) && span_fits(e.bn, ldw, K, 1);
+}
+
+using narrow_launch = void (*)(const mpg::NarrowArgs &, dim3, hipStream_t);
+
+template <int IN, int OUT>
+void launch_narrow(const mpg::NarrowArgs &a, dim3 grid, hipStream_t s)
+{
+    hipLaunchKernelGGL((mpg::narrow_rows<IN, OUT, 8>), grid, dim3(512), 0, s, a);
+}
+
+const narrow_launch kNarrowI8Launch[3] = {&launch_narrow<mpg::kNarrowI8, mpg::kTF16>,
+                                          &launch_narrow<mpg::kNarrowI8, mpg::kTBF16>,
+                                          &launch_narrow<mpg::kNarrowI8, mpg::kTF32>};
+
+// Tiles that `rows` rows in `groups` groups of about the same size make.
+int64_t likely_tiles(int64_t rows, int64_t groups, int64_t bm, int64_t tiles_n)
+{
+    return mul_sat(mul_sat(cdiv(cdiv(rows, groups), bm), groups), tiles_n);
+}
+
+// Table entry of an 8-bit product, or -1 for the narrow kernel.
+int select_i8(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldw)
+{
+    const int64_t per = cdiv(M, groups);
+    if (per <= 16)
+        return -1;
+    const int64_t t256 = likely_tiles(M, groups, 256, cdiv(N, 256));
+    const int64_t t128 = likely_tiles(M, groups, 128, cdiv(N, 128));
+    if (per > 128 && N > 128 && 3 * cdiv(t256, kNumCu) <= cdiv(t128, kNumCu) && i8_fits(kI8Table[kI8Big], lda, ldw, K))
+        return kI8Big;
+    if (t128 >= kNumCu / 2 && i8_fits(kI8Table[kI8Mid], lda, ldw, K))
+        return kI8Mid;
+    return i8_fits(kI8Table[kI8Small], lda, ldw, K) ? kI8Small : -1;
+}
 
 // ---------------------------------------------------------------------------
 // Grouped 16-bit products
@@ -125,10 +168,13 @@ template <int LA, int LB, int IN>
 const GroupedEntry *grouped_table()
 {
     static constexpr GroupedEntry table[] = {
+        grouped_entry<PipeCfg<256, 256, 64, 2, 4, 2, LA, LB, IN, 1, 16>>(),
+        grouped_entry<PipeCfg<128, 128, 128, 2, 4, 2, LA, LB, IN, 1, 32, 2>>(),
         grouped_entry<PipeCfg<64, 64, 64, 2, 2, 2, LA, LB, IN>>(),
     };
     return table;
 }
+enum : int { kGroupedBig = 0, kGroupedMid = 1, kGroupedSmall = 2 };
 
 const GroupedEntry *grouped_family(int la, int lb, int in)
 {
@@ -147,6 +193,43 @@ bool grouped_fits(const GroupedEntry &e, int la, int lb, int64_t lda, int64_t ld
     return (la == kRowMajor ? span_fits(e.bm, lda, e.bk, 2) : span_fits(e.bk, lda, e.bm, 2)) &&
            (lb == kRowMajor ? span_fits(e.bk, ldb, e.bn, 2) : span_fits(e.bn, ldb, e.bk, 2)) &&
            span_fits(e.bm, ldc, e.bn, 4);
+}
+
+// Table entry of a grouped product whose row tiles the groups split, or -1
+// for the narrow kernel (column-major B).
+int select_grouped(const GroupedEntry *table, int lb, int64_t groups, int64_t R, int64_t N, int64_t lda, int64_t ldb,
+                   int64_t ldc)
+{
+    const int64_t per = cdiv(R, groups);
+    if (per <= 16 && lb == kColMajor)
+        return -1;
+    const int64_t t256 = likely_tiles(R, groups, 256, cdiv(N, 256));
+    const int64_t t128 = likely_tiles(R, groups, 128, cdiv(N, 128));
+    if (per > 128 && N > 128 && 3 * cdiv(t256, kNumCu) <= cdiv(t128, kNumCu) &&
+        grouped_fits(table[kGroupedBig], kRowMajor, lb, lda, ldb, ldc))
+        return kGroupedBig;
+    if (t128 >= kNumCu / 2 && grouped_fits(table[kGroupedMid], kRowMajor, lb, lda, ldb, ldc))
+        return kGroupedMid;
+    return kGroupedSmall;
+}
+
+// Table entry of a gradient by the weights: `tiles` of M x N per group.
+int select_wgrad(const GroupedEntry *table, int64_t groups, int64_t M, int64_t N, int64_t lda, int64_t ldb, int64_t ldc)
+{
+    const int64_t t256 = mul_sat(mul_sat(cdiv(M, 256), cdiv(N, 256)), groups);
+    const int64_t t128 = mul_sat(mul_sat(cdiv(M, 128), cdiv(N, 128)), groups);
+    if (M > 128 && N > 128 && 3 * cdiv(t256, kNumCu) <= cdiv(t128, kNumCu) &&
+        grouped_fits(table[kGroupedBig], kColMajor, kRowMajor, lda, ldb, ldc))
+        return kGroupedBig;
+    if (t128 >= kNumCu / 2 && grouped_fits(table[kGroupedMid], kColMajor, kRowMajor, lda, ldb, ldc))
+        return kGroupedMid;
+    return kGroupedSmall;
+}
+
+template <int IN>
+void launch_grouped_narrow(const mpg::NarrowArgs &a, dim3 grid, hipStream_t s)
+{
+    hipLaunchKernelGGL((mpg::narrow_rows<IN, mpg::kTF32, 8>), grid, dim3(512), 0, s, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -275,11 +358,37 @@ int mpgemm_i8_gemm(int out_type, int64_t groups, int64_t M, int64_t N, int64_t K
     if (!aligned(C, size_of(out_type)) || !aligned(scale_a, 4) || !aligned(scale_w, 4) || !aligned(bias, 4) ||
         !aligned(offsets, 4))
         return MPGEMM_EALIGN;
-    const I8Entry &e = kI8Table[0];
-    if (!span_fits(e.bm, lda, K, 1) || !span_fits(e.bn, ldw, K, 1))
+    const GroupArgs group_args{offsets, (int32_t)groups, (int32_t)M, stride_w};
+    if (!span_fits(16, lda, K, 1) || !span_fits(16, ldw, K, 1))
         return MPGEMM_ELD;
+    const int id = select_i8(offsets ? groups : 1, M, N, K, lda, ldw);
+    if (id < 0) {
+        const int64_t tiles_n = cdiv(N, 16);
+        const int64_t grid = mul_sat(row_tiles(M, offsets ? groups : 1, 16), tiles_n);
+        if (grid > kMax32 / 64)
+            return MPGEMM_EDIM;
+        mpg::NarrowArgs a{};
+        a.A = reinterpret_cast<const uint8_t *>(A);
+        a.W = reinterpret_cast<const uint8_t *>(W);
+        a.C = C;
+        a.lda = lda;
+        a.ldw = ldw;
+        a.ldc = ldc;
+        a.stride_w = stride_w;
+        a.N = (int32_t)N;
+        a.KB = (int32_t)K;
+        a.tiles_n = (int32_t)tiles_n;
+        a.groups = group_args;
+        a.scale_a = scale_a;
+        a.scale_w = scale_w;
+        a.bias = bias;
+        forget_error();
+        kNarrowI8Launch[out_type](a, dim3((unsigned)grid), stream_of(stream));
+        return launched();
+    }
+    const I8Entry &e = kI8Table[id];
     const int64_t tiles_n = cdiv(N, e.bn);
-    const int64_t grid = mul_sat(offsets ? row_tiles(M, groups, e.bm) : cdiv(M, e.bm), tiles_n);
+    const int64_t grid = mul_sat(row_tiles(M, offsets ? groups : 1, e.bm), tiles_n);
     if (grid > kMax32 / 64)
         return MPGEMM_EDIM;
     I8Args a{};
@@ -296,7 +405,7 @@ int mpgemm_i8_gemm(int out_type, int64_t groups, int64_t M, int64_t N, int64_t K
     a.K = (int32_t)K;
     a.tiles_n = (int32_t)tiles_n;
     a.group_m = 8;
-    a.groups = GroupArgs{offsets, (int32_t)groups, (int32_t)M, stride_w};
+    a.groups = group_args;
     forget_error();
     e.launch[out_type](a, dim3((unsigned)grid), stream_of(stream));
     return launched();
@@ -460,7 +569,36 @@ int mpgemm_grouped(int in_type, int layout_b, int64_t groups, int64_t R, int64_t
         return MPGEMM_ENULL;
     if (!aligned(C, 4) || !aligned(offsets, 4) || (reads && (!aligned(A, 2) || !aligned(B, 2))))
         return MPGEMM_EALIGN;
-    const GroupedEntry &e = *grouped_family(kRowMajor, layout_b, in_type);
+    const GroupArgs group_args{offsets, (int32_t)groups, (int32_t)R, stride_b};
+    const GroupedEntry *const table = grouped_family(kRowMajor, layout_b, in_type);
+    const int id = select_grouped(table, layout_b, groups, R, N, lda, ldb, ldc);
+    if (id < 0 && span_fits(16, lda, K, 2) && span_fits(16, ldb, K, 2)) {
+        const int64_t tiles_n = cdiv(N, 16);
+        const int64_t grid = mul_sat(row_tiles(R, groups, 16), tiles_n);
+        if (grid > kMax32 / 64)
+            return MPGEMM_EDIM;
+        mpg::NarrowArgs a{};
+        a.A = reinterpret_cast<const uint8_t *>(A);
+        a.W = reinterpret_cast<const uint8_t *>(B);
+        a.C = C;
+        a.lda = 2 * lda;
+        a.ldw = 2 * ldb;
+        a.ldc = ldc;
+        a.stride_w = 2 * stride_b;
+        a.N = (int32_t)N;
+        a.KB = (int32_t)(2 * K);
+        a.tiles_n = (int32_t)tiles_n;
+        a.groups = group_args;
+        a.alpha = alpha;
+        a.beta = beta;
+        forget_error();
+        if (in_type == MPGEMM_IN_BF16)
+            launch_grouped_narrow<kInBF16>(a, dim3((unsigned)grid), stream_of(stream));
+        else
+            launch_grouped_narrow<kInF16>(a, dim3((unsigned)grid), stream_of(stream));
+        return launched();
+    }
+    const GroupedEntry &e = table[id < 0 ? kGroupedSmall : id];
     if (!grouped_fits(e, kRowMajor, layout_b, lda, ldb, ldc))
         return MPGEMM_ELD;
     const int64_t tiles_n = cdiv(N, e.bn);
@@ -483,7 +621,7 @@ int mpgemm_grouped(int in_type, int layout_b, int64_t groups, int64_t R, int64_t
     a.group_m = 8;
     a.splits = 1;
     forget_error();
-    e.launch(a, GroupArgs{offsets, (int32_t)groups, (int32_t)R, stride_b}, dim3((unsigned)grid), stream_of(stream));
+    e.launch(a, group_args, dim3((unsigned)grid), stream_of(stream));
     return launched();
 }
 
@@ -508,7 +646,8 @@ int mpgemm_grouped_wgrad(int in_type, int64_t groups, int64_t R, int64_t M, int6
         return MPGEMM_ENULL;
     if (!aligned(C, 4) || !aligned(offsets, 4) || (reads && (!aligned(A, 2) || !aligned(B, 2))))
         return MPGEMM_EALIGN;
-    const GroupedEntry &e = *grouped_family(kColMajor, kRowMajor, in_type);
+    const GroupedEntry *const table = grouped_family(kColMajor, kRowMajor, in_type);
+    const GroupedEntry &e = table[select_wgrad(table, groups, M, N, lda, ldb, ldc)];
     if (!grouped_fits(e, kColMajor, kRowMajor, lda, ldb, ldc))
         return MPGEMM_ELD;
     const int64_t tiles_m = cdiv(M, e.bm), tiles_n = cdiv(N, e.bn);

@@ -294,6 +294,22 @@ def test_grouped_shapes(col, N, K, gap, shift):
     check_grouped([7, 0, 70, 1], 90, N, K, torch.float16, col, alpha=1.5, beta=-0.5, gap=gap, shift=shift)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("col", [False, True])
+def test_grouped_every_tile_size(dtype, col):
+    """Sizes at which the 128x128 and 256x256 tiles and the narrow kernel are
+    chosen, with ragged edges in every direction."""
+    check_grouped([1, 700, 0, 1299, 490], 2500, 1100, 77, dtype, col)
+    check_grouped([1, 4000, 0, 5, 4901], 9000, 1100, 69, dtype, col, beta=0.5)
+    check_grouped([1, 9, 0, 16, 17], 50, 300, 1003, dtype, col, alpha=0.5, beta=2.0, gap=1, shift=1)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_wgrad_every_tile_size(dtype):
+    check_wgrad([100, 0, 37, 1], 140, 900, 1100, dtype)
+    check_wgrad([30, 7, 0], 40, 2200, 3300, dtype, beta=0.5)
+
+
 def test_grouped_scalars_and_empty():
     check_grouped([3, 4], 8, 20, 0, torch.float16, True, beta=0.5)
     check_grouped([3, 4], 8, 20, 0, torch.float16, False)

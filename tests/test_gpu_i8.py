@@ -182,6 +182,20 @@ def test_i8_sizes(dtype, M, N, K):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,N,K,gap", [(1500, 1400, 200, 0), (2600, 4100, 141, 0), (2570, 4353, 300, 3),
+                                       (16, 4100, 1000, 0), (12, 300, 5001, 1)])
+def test_i8_every_tile_size(dtype, M, N, K, gap):
+    """Sizes at which the 128x128 and 256x256 tiles and the narrow kernel are
+    chosen, with ragged edges in every direction."""
+    check_i8(M, N, K, dtype, gap=gap)
+
+
+def test_i8_groups_every_tile_size():
+    check_i8(2500, 1100, 200, torch.bfloat16, sizes=[1, 700, 0, 1299, 490])
+    check_i8(9000, 1100, 133, torch.float32, sizes=[1, 4000, 0, 5, 4901], gap=1)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("gap,shift", [(0, 1), (1, 0), (3, 3), (16, 0)])
 def test_i8_alignments(dtype, gap, shift):
     check_i8(70, 83, 300, dtype, gap=gap, shift=shift, seed=gap + 8 * shift)
