@@ -110,7 +110,7 @@ struct I8Cfg {
     static constexpr int COPY_WINDOW = STAGES == 2 ? (NCOPY < KS * FM ? NCOPY : KS * FM) : KS * FM;
     static_assert(WTM % 16 == 0 && WTN % 16 == 0, "wave tiles are multiples of the instruction's");
     static_assert(KS >= 2, "a K tile holds two k-steps at least");
-    static_assert(STAGES >= 2 && STAGES <= 4, "2..4 LDS stages");
+    static_assert(STAGES >= 2 && STAGES <= 8, "2..8 LDS stages");
     static_assert(NCOPY * (STAGES - 1) < 64, "vmcnt is 6 bits");
     static_assert(LDS_BYTES <= 160 * 1024, "gfx950 has 160 KiB of LDS per workgroup");
 };
@@ -142,6 +142,20 @@ __device__ __forceinline__ void i8_store(typename ElemOf<OUT>::type *row, int co
         for (int e = 0; e < COUNT; ++e)
             if (e < left)
                 row[col + e] = (E)v[e];
+    }
+}
+
+// Wait until at most `newer` whole tiles' copies (0 .. MOST) are in flight.
+template <class Cfg, int MOST>
+__device__ __forceinline__ void wait_tiles(int newer)
+{
+    if constexpr (MOST <= 0) {
+        wait_vmcnt<0>();
+    } else {
+        if (newer >= MOST)
+            wait_vmcnt<MOST * Cfg::NCOPY>();
+        else
+            wait_tiles<Cfg, MOST - 1>(newer);
     }
 }
 
@@ -280,14 +294,9 @@ i8_tile(I8Args args)
         if (t == num_k - 1 && (klast & 15) != 0) {
             wait_vmcnt<0>();
             fill(buf);
-        } else if (newer <= 0) {
-            wait_vmcnt<0>();
-        } else if (newer == 1) {
-            wait_vmcnt<NCOPY>();
-        } else if (newer == 2) {
-            wait_vmcnt<(S > 2 ? 2 : 1) * NCOPY>();
         } else {
-            wait_vmcnt<(S > 3 ? 3 : 1) * NCOPY>();
+            // (the counts are compile-time operands of the wait)
+            wait_tiles<Cfg, S - 1>(newer);
         }
         __syncthreads();
     };

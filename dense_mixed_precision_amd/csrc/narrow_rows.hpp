@@ -42,14 +42,14 @@ struct NarrowAcc<kNarrowI8> {
     static constexpr int ES = 1;
 };
 
-template <int IN, int OUT, int DEPTH>
-__global__ void __launch_bounds__(512)
+template <int IN, int OUT, int DEPTH, int WAVES, int NB = 1, int POLICY = 0>
+__global__ void __launch_bounds__(64 * WAVES)
 narrow_rows(NarrowArgs args)
 {
     typedef typename NarrowAcc<IN>::type Acc;
     typedef typename ElemOf<OUT>::type E;
     constexpr int ES = NarrowAcc<IN>::ES;
-    __shared__ Acc part[8][64];
+    __shared__ Acc part[WAVES][NB][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     GroupTile gt;
@@ -57,39 +57,48 @@ narrow_rows(NarrowArgs args)
         return;
     const int row0 = gt.start + gt.tm * 16;
     const int rows = min(gt.rows - gt.tm * 16, 16);
-    const int n0 = gt.tn * 16;
-    const int cols = min(args.N - n0, 16);
+    const int n0 = gt.tn * 16 * NB;
+    const int cols = args.N - n0;
     const int KB = (IN != kNarrowI8 && args.alpha == 0.0f) ? 0 : args.KB;
     const int r = lane & 15;          // token of the second operand, channel of the first
     const int kq = 16 * (lane >> 4);  // this lane's bytes within a 64-byte step
-    const bool a_ok = r < rows, w_ok = r < cols;
+    const bool a_ok = r < rows;
     const uint8_t *const Ap = args.A + (int64_t)row0 * args.lda;
     const uint8_t *const Wp = args.W + (int64_t)gt.group * args.stride_w + (int64_t)n0 * args.ldw;
     const __amdgpu_buffer_rsrc_t rsA = make_rsrc(Ap), rsW = make_rsrc(Wp);
     // 32-bit offsets: the host checks that 16 rows span less than 2 GiB
-    const uint32_t offA = (uint32_t)(r * (int)args.lda + kq), offW = (uint32_t)(r * (int)args.ldw + kq);
+    const uint32_t offA = (uint32_t)(r * (int)args.lda + kq);
+    uint32_t offW[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+        offW[b] = 16 * b + r < cols ? (uint32_t)((16 * b + r) * (int)args.ldw + kq) : kOOB;
 
     // this wave's 64-byte steps of the whole vectors; the last KB % 16 bytes
     // are a step of their own
     const int whole = KB & ~15;
     const int steps = (whole + 63) / 64;
-    const int per = (steps + 7) / 8;
+    const int per = (steps + WAVES - 1) / WAVES;
     const int s0 = min(wave * per, steps), s1 = min(s0 + per, steps);
-    u32x4 ra[DEPTH], rw[DEPTH];
+    u32x4 ra[DEPTH], rw[DEPTH][NB];
     auto issue = [&](int d, int s) __attribute__((always_inline)) {
         const bool k_ok = 64 * s + kq < whole;
-        rw[d] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsW, (w_ok && k_ok) ? offW + 64 * s : kOOB,
-                                                                                0, kStoreNT));
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            rw[d][b] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsW, k_ok ? offW[b] : kOOB, 64 * s,
+                                                                                       POLICY));
         ra[d] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsA, (a_ok && k_ok) ? offA + 64 * s : kOOB,
                                                                                 0, 0));
     };
-    Acc acc = Acc{0};
-    auto multiply = [&](const u32x4 &w, const u32x4 &a) __attribute__((always_inline)) {
+    Acc acc[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+        acc[b] = Acc{0};
+    auto multiply = [&](int b, const u32x4 &w, const u32x4 &a) __attribute__((always_inline)) {
         if constexpr (IN == kNarrowI8)
-            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4v, w), __builtin_bit_cast(i32x4v, a),
-                                                        acc, 0, 0, 0);
+            acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4v, w), __builtin_bit_cast(i32x4v, a),
+                                                           acc[b], 0, 0, 0);
         else
-            acc = mfma16<IN>(__builtin_bit_cast(half8, w), __builtin_bit_cast(half8, a), acc);
+            acc[b] = mfma16<IN>(__builtin_bit_cast(half8, w), __builtin_bit_cast(half8, a), acc[b]);
     };
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d)
@@ -99,7 +108,9 @@ narrow_rows(NarrowArgs args)
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) {
             if (s + d < s1) {
-                multiply(rw[d], ra[d]);
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                    multiply(b, rw[d][b], ra[d]);
                 if (s + d + DEPTH < s1)
                     issue(d, s + d + DEPTH);
             }
@@ -107,38 +118,42 @@ narrow_rows(NarrowArgs args)
     }
     // the last KB % 16 bytes, in the first 16 lanes: element loads, zeros
     // behind the row
-    if (wave == 7 && whole < KB) {
-        uint32_t w[4] = {0, 0, 0, 0}, a[4] = {0, 0, 0, 0};
+    if (wave == WAVES - 1 && whole < KB) {
         const int left = lane < 16 ? KB - whole : 0;
+        auto tail = [&](const __amdgpu_buffer_rsrc_t &rs, uint32_t off) __attribute__((always_inline)) {
+            uint32_t v[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < 16 / ES; ++e) {
-            const int at = ES * e;
-            const bool ok = at < left;
-            const uint32_t ow = ok && w_ok ? offW + whole + at : kOOB, oa = ok && a_ok ? offA + whole + at : kOOB;
-            uint32_t vw, va;
-            if constexpr (ES == 1) {
-                vw = __builtin_amdgcn_raw_buffer_load_b8(rsW, ow, 0, 0) & 0xFFu;
-                va = __builtin_amdgcn_raw_buffer_load_b8(rsA, oa, 0, 0) & 0xFFu;
-            } else {
-                vw = __builtin_amdgcn_raw_buffer_load_b16(rsW, ow, 0, 0) & 0xFFFFu;
-                va = __builtin_amdgcn_raw_buffer_load_b16(rsA, oa, 0, 0) & 0xFFFFu;
+            for (int e = 0; e < 16 / ES; ++e) {
+                const int at = ES * e;
+                const uint32_t o = at < left && off != kOOB ? off + whole + at : kOOB;
+                uint32_t x;
+                if constexpr (ES == 1)
+                    x = __builtin_amdgcn_raw_buffer_load_b8(rs, o, 0, 0) & 0xFFu;
+                else
+                    x = __builtin_amdgcn_raw_buffer_load_b16(rs, o, 0, 0) & 0xFFFFu;
+                v[at / 4] |= x << (8 * (at % 4));
             }
-            w[at / 4] |= vw << (8 * (at % 4));
-            a[at / 4] |= va << (8 * (at % 4));
-        }
-        multiply(u32x4{w[0], w[1], w[2], w[3]}, u32x4{a[0], a[1], a[2], a[3]});
+            return u32x4{v[0], v[1], v[2], v[3]};
+        };
+        const u32x4 a = tail(rsA, a_ok ? offA : kOOB);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            multiply(b, tail(rsW, offW[b]), a);
     }
 
-    part[wave][lane] = acc;
-    __syncthreads();
-    if (wave != 0)
-        return;
-    Acc sum = part[0][lane];
 #pragma unroll
-    for (int w = 1; w < 8; ++w)
-        sum += part[w][lane];
+    for (int b = 0; b < NB; ++b)
+        part[wave][b][lane] = acc[b];
+    __syncthreads();
+    if (wave >= NB)
+        return;
+    // wave b finishes channel block b
+    Acc sum = part[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w)
+        sum += part[w][wave][lane];
 
-    const int c = 4 * (lane >> 4);
+    const int c = 16 * wave + 4 * (lane >> 4);
     const int left = cols - c;
     if (!a_ok || left <= 0)
         return;

@@ -100,22 +100,34 @@ constexpr I8Entry i8_entry()
 const I8Entry kI8Table[] = {
     i8_entry<I8Cfg<256, 256, 128, 2, 4, 2>>(),
     i8_entry<I8Cfg<128, 128, 128, 2, 4, 3>>(),
-    i8_entry<I8Cfg<64, 64, 256, 2, 2, 2>>(),
+    i8_entry<I8Cfg<64, 128, 128, 2, 4, 3>>(),
+    i8_entry<I8Cfg<64, 64, 256, 2, 4, 3>>(),
+    i8_entry<I8Cfg<16, 64, 256, 1, 4, 4>>(),
 };
-enum : int { kI8Big = 0, kI8Mid = 1, kI8Small = 2 };
+enum : int { kI8Big = 0, kI8Mid = 1, kI8Half = 2, kI8Small = 3, kI8Few = 4 };
 
 bool i8_fits(const I8Entry &e, int64_t lda, int64_t ldw, int64_t K)
 {
     return span_fits(e.bm, lda, K, 1) && span_fits(e.bn, ldw, K, 1);
 }
 
-using narrow_launch = void (*)(const mpg::NarrowArgs &, dim3, hipStream_t);
+// The narrow kernel by the size of its grid: 4 waves with 8 loads in flight
+// each where there are workgroups enough to fill the compute units several
+// times over, else 8 waves with 4 (8-bit codes, 64 rows over 64 experts of
+// 2048x2048, 8192 workgroups: 48.0 against 58.9 us; 16x4096x4096, 256
+// workgroups: 6.7 against 6.4; 1x1024x16384, 64: 12.2 against 11.3).
+constexpr int64_t kNarrowManyWgs = 1024;
 
 template <int IN, int OUT>
-void launch_narrow(const mpg::NarrowArgs &a, dim3 grid, hipStream_t s)
+void launch_narrow(const mpg::NarrowArgs &a, int64_t grid, hipStream_t s)
 {
-    hipLaunchKernelGGL((mpg::narrow_rows<IN, OUT, 8>), grid, dim3(512), 0, s, a);
+    if (grid >= kNarrowManyWgs)
+        hipLaunchKernelGGL((mpg::narrow_rows<IN, OUT, 8, 4>), dim3((unsigned)grid), dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((mpg::narrow_rows<IN, OUT, 4, 8>), dim3((unsigned)grid), dim3(512), 0, s, a);
 }
+
+using narrow_launch = void (*)(const mpg::NarrowArgs &, int64_t, hipStream_t);
 
 const narrow_launch kNarrowI8Launch[3] = {&launch_narrow<mpg::kNarrowI8, mpg::kTF16>,
                                           &launch_narrow<mpg::kNarrowI8, mpg::kTBF16>,
@@ -127,19 +139,37 @@ int64_t likely_tiles(int64_t rows, int64_t groups, int64_t bm, int64_t tiles_n)
     return mul_sat(mul_sat(cdiv(cdiv(rows, groups), bm), groups), tiles_n);
 }
 
-// Table entry of an 8-bit product, or -1 for the narrow kernel.
+// Table entry of an 8-bit product, or -1 for the narrow kernel.  By sweeps of
+// every entry (us, graph-replayed, K and N first where one number stands):
+//   up to 16 rows a group: narrow (8x8192x8192 15.1, 16x64 tiles 15.8;
+//     16x4096x4096 6.4 against 9.3), but 64x128 tiles for 5 rows and more
+//     a group over at least 512 of them (512 rows over 64 experts of
+//     2048x2048 50.2 against 60.9; 64 rows 48.0 narrow against 59);
+//   256x256 where its rounds of workgroups over the compute units take at
+//     most a third of the 128x128 tiles' (4096^3 64.2 against 88.9);
+//   128x128 from 192 tiles (512x8192x8192 49.0, 64x128 54.0; 2048^3 15.2
+//     against 16.0; below, 256x8192x8192, 128 tiles, 40.0 against 32.9);
+//   64x128 from 129 tiles (1024x2048x2048 10.5, 64x64 14.5; 128x8192x8192,
+//     128 tiles, 32.5 against 22.6);
+//   64x64 from 128 tiles above 32 rows (128x8192x8192 22.6, 16x64 39.4;
+//     512x2048x2048 8.2 against 13.9; 32x8192x8192 19.3 against 16.7);
+//   else 16x64 (128x2048x2048, 64 tiles of 64x64: 6.1 against 7.1).
 int select_i8(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldw)
 {
     const int64_t per = cdiv(M, groups);
+    auto tiles = [&](int64_t bm, int64_t bn) { return likely_tiles(M, groups, bm, cdiv(N, bn)); };
+    auto fits = [&](int id) { return i8_fits(kI8Table[id], lda, ldw, K); };
     if (per <= 16)
-        return -1;
-    const int64_t t256 = likely_tiles(M, groups, 256, cdiv(N, 256));
-    const int64_t t128 = likely_tiles(M, groups, 128, cdiv(N, 128));
-    if (per > 128 && N > 128 && 3 * cdiv(t256, kNumCu) <= cdiv(t128, kNumCu) && i8_fits(kI8Table[kI8Big], lda, ldw, K))
+        return per > 4 && groups > 1 && tiles(64, 128) >= 512 && fits(kI8Half) ? kI8Half : -1;
+    if (per > 128 && N > 128 && 3 * cdiv(tiles(256, 256), kNumCu) <= cdiv(tiles(128, 128), kNumCu) && fits(kI8Big))
         return kI8Big;
-    if (t128 >= kNumCu / 2 && i8_fits(kI8Table[kI8Mid], lda, ldw, K))
+    if (per > 64 && tiles(128, 128) >= 192 && fits(kI8Mid))
         return kI8Mid;
-    return i8_fits(kI8Table[kI8Small], lda, ldw, K) ? kI8Small : -1;
+    if (tiles(64, 128) > 128 && fits(kI8Half))
+        return kI8Half;
+    if (per > 32 && tiles(64, 64) >= 128 && fits(kI8Small))
+        return kI8Small;
+    return fits(kI8Few) ? kI8Few : -1;
 }
 
 // ---------------------------------------------------------------------------
@@ -164,28 +194,43 @@ constexpr GroupedEntry grouped_entry()
     return GroupedEntry{Cfg::BM, Cfg::BN, Cfg::BK, &launch_grouped<Cfg>};
 }
 
-template <int LA, int LB, int IN>
-const GroupedEntry *grouped_table()
+// The tiles of one form of the product.  Where the groups split the rows
+// (A row-major): 256x256, 128x256, 128x128, 64x128 and 32x64; where they split
+// K (A column-major): 256x256, 128x256, 128x128 and 64x64.
+enum : int { kGroupedBig = 0, kGroupedWide = 1, kGroupedMid = 2, kGroupedHalf = 3, kGroupedFew = 4, kGroupedSmall = 3 };
+
+template <int LB, int IN>
+const GroupedEntry *rows_table()
 {
     static constexpr GroupedEntry table[] = {
-        grouped_entry<PipeCfg<256, 256, 64, 2, 4, 2, LA, LB, IN, 1, 16>>(),
-        grouped_entry<PipeCfg<128, 128, 128, 2, 4, 2, LA, LB, IN, 1, 32, 2>>(),
-        grouped_entry<PipeCfg<64, 64, 64, 2, 2, 2, LA, LB, IN>>(),
+        grouped_entry<PipeCfg<256, 256, 64, 2, 4, 2, kRowMajor, LB, IN, 1, 16>>(),
+        grouped_entry<PipeCfg<128, 256, 64, 2, 4, 3, kRowMajor, LB, IN, 1, 16>>(),
+        grouped_entry<PipeCfg<128, 128, 128, 2, 4, 2, kRowMajor, LB, IN, 1, 32>>(),
+        grouped_entry<PipeCfg<64, 128, 64, 2, 4, 3, kRowMajor, LB, IN, 1, 16>>(),
+        grouped_entry<PipeCfg<32, 64, 128, 2, 4, 3, kRowMajor, LB, IN, 1, 16>>(),
     };
     return table;
 }
-enum : int { kGroupedBig = 0, kGroupedMid = 1, kGroupedSmall = 2 };
+
+template <int IN>
+const GroupedEntry *wgrad_table()
+{
+    static constexpr GroupedEntry table[] = {
+        grouped_entry<PipeCfg<256, 256, 64, 2, 4, 2, kColMajor, kRowMajor, IN, 1, 16>>(),
+        grouped_entry<PipeCfg<128, 256, 64, 2, 4, 3, kColMajor, kRowMajor, IN, 1, 16>>(),
+        grouped_entry<PipeCfg<128, 128, 128, 2, 4, 2, kColMajor, kRowMajor, IN, 1, 32>>(),
+        grouped_entry<PipeCfg<64, 64, 64, 2, 2, 2, kColMajor, kRowMajor, IN>>(),
+    };
+    return table;
+}
 
 const GroupedEntry *grouped_family(int la, int lb, int in)
 {
     if (la == kColMajor)
-        return in == kInBF16 ? grouped_table<kColMajor, kRowMajor, kInBF16>()
-                             : grouped_table<kColMajor, kRowMajor, kInF16>();
+        return in == kInBF16 ? wgrad_table<kInBF16>() : wgrad_table<kInF16>();
     if (lb == kColMajor)
-        return in == kInBF16 ? grouped_table<kRowMajor, kColMajor, kInBF16>()
-                             : grouped_table<kRowMajor, kColMajor, kInF16>();
-    return in == kInBF16 ? grouped_table<kRowMajor, kRowMajor, kInBF16>()
-                         : grouped_table<kRowMajor, kRowMajor, kInF16>();
+        return in == kInBF16 ? rows_table<kColMajor, kInBF16>() : rows_table<kColMajor, kInF16>();
+    return in == kInBF16 ? rows_table<kRowMajor, kInBF16>() : rows_table<kRowMajor, kInF16>();
 }
 
 bool grouped_fits(const GroupedEntry &e, int la, int lb, int64_t lda, int64_t ldb, int64_t ldc)
@@ -195,41 +240,62 @@ bool grouped_fits(const GroupedEntry &e, int la, int lb, int64_t lda, int64_t ld
            span_fits(e.bm, ldc, e.bn, 4);
 }
 
-// Table entry of a grouped product whose row tiles the groups split, or -1
-// for the narrow kernel (column-major B).
+// 256x256 tiles where they take at most a third of the 128x128 tiles' rounds
+// over the compute units (32768 rows over 32 experts of 2048x2048: 271 us,
+// 128x256 329, 128x128 443; gradient by the weights 332, 396, 498).
+bool big_tiles_win(int64_t t256, int64_t t128) { return 3 * cdiv(t256, kNumCu) <= cdiv(t128, kNumCu); }
+
+// 128x256 tiles take 1.8 times as long as 128x128 (gradient by the weights,
+// 32768 rows over 8 experts of 1024x1024: one round 74 us, two of 128x128 83).
+bool wide_tiles_win(int64_t twide, int64_t t128) { return 9 * cdiv(twide, kNumCu) <= 5 * cdiv(t128, kNumCu); }
+
+// Table entry of a grouped product whose rows the groups split, or -1 for the
+// narrow kernel (column-major B).  By sweeps of every entry (us,
+// graph-replayed; "per" rows a group, N = K = 2048, 32 or 64 experts where
+// nothing else stands), besides the rules above:
+//   up to 16 per and B column-major: narrow for at most 4 per (1 per over 64
+//     experts 95, 32x64 106) or few tiles, else 32x64 (8 per over 64 experts
+//     108 against 123);
+//   128x128 above 64 per from 128 tiles (3000 rows, 13 experts of 617x800,
+//     182 tiles: 12.6, 64x128 15.0);
+//   64x128 from 192 tiles above 32 per (64 per: 67, 32x64 77; 54 against 78
+//     with B row-major), or at any per with B row-major (32 per: 52 against
+//     58; B column-major 65 against 58);
+//   else 32x64 (300 rows, 13 experts of 617x800: 6.8, 64x128 9.0).
 int select_grouped(const GroupedEntry *table, int lb, int64_t groups, int64_t R, int64_t N, int64_t lda, int64_t ldb,
                    int64_t ldc)
 {
     const int64_t per = cdiv(R, groups);
-    if (per <= 16 && lb == kColMajor)
+    auto tiles = [&](int64_t bm, int64_t bn) { return likely_tiles(R, groups, bm, cdiv(N, bn)); };
+    auto fits = [&](int id) { return grouped_fits(table[id], kRowMajor, lb, lda, ldb, ldc); };
+    if (per <= 16 && lb == kColMajor && (per <= 4 || tiles(32, 64) < 512))
         return -1;
-    const int64_t t256 = likely_tiles(R, groups, 256, cdiv(N, 256));
-    const int64_t t128 = likely_tiles(R, groups, 128, cdiv(N, 128));
-    if (per > 128 && N > 128 && 3 * cdiv(t256, kNumCu) <= cdiv(t128, kNumCu) &&
-        grouped_fits(table[kGroupedBig], kRowMajor, lb, lda, ldb, ldc))
-        return kGroupedBig;
-    if (t128 >= kNumCu / 2 && grouped_fits(table[kGroupedMid], kRowMajor, lb, lda, ldb, ldc))
+    if (per > 64 && N > 128) {
+        if (per > 128 && big_tiles_win(tiles(256, 256), tiles(128, 128)) && fits(kGroupedBig))
+            return kGroupedBig;
+        if (wide_tiles_win(tiles(128, 256), tiles(128, 128)) && fits(kGroupedWide))
+            return kGroupedWide;
+    }
+    if (per > 64 && tiles(128, 128) >= kNumCu / 2 && fits(kGroupedMid))
         return kGroupedMid;
-    return kGroupedSmall;
+    if ((per > 32 || lb == kRowMajor) && tiles(64, 128) >= 192 && fits(kGroupedHalf))
+        return kGroupedHalf;
+    return kGroupedFew;
 }
 
-// Table entry of a gradient by the weights: `tiles` of M x N per group.
+// Table entry of a gradient by the weights (M x N per group; the groups split
+// K).  Below 128 tiles of 128x128, 64x64.
 int select_wgrad(const GroupedEntry *table, int64_t groups, int64_t M, int64_t N, int64_t lda, int64_t ldb, int64_t ldc)
 {
-    const int64_t t256 = mul_sat(mul_sat(cdiv(M, 256), cdiv(N, 256)), groups);
-    const int64_t t128 = mul_sat(mul_sat(cdiv(M, 128), cdiv(N, 128)), groups);
-    if (M > 128 && N > 128 && 3 * cdiv(t256, kNumCu) <= cdiv(t128, kNumCu) &&
-        grouped_fits(table[kGroupedBig], kColMajor, kRowMajor, lda, ldb, ldc))
+    auto tiles = [&](int64_t bm, int64_t bn) { return mul_sat(mul_sat(cdiv(M, bm), cdiv(N, bn)), groups); };
+    auto fits = [&](int id) { return grouped_fits(table[id], kColMajor, kRowMajor, lda, ldb, ldc); };
+    if (M > 128 && N > 128 && big_tiles_win(tiles(256, 256), tiles(128, 128)) && fits(kGroupedBig))
         return kGroupedBig;
-    if (t128 >= kNumCu / 2 && grouped_fits(table[kGroupedMid], kColMajor, kRowMajor, lda, ldb, ldc))
+    if (N > 128 && wide_tiles_win(tiles(128, 256), tiles(128, 128)) && fits(kGroupedWide))
+        return kGroupedWide;
+    if (tiles(128, 128) >= kNumCu / 2 && fits(kGroupedMid))
         return kGroupedMid;
     return kGroupedSmall;
-}
-
-template <int IN>
-void launch_grouped_narrow(const mpg::NarrowArgs &a, dim3 grid, hipStream_t s)
-{
-    hipLaunchKernelGGL((mpg::narrow_rows<IN, mpg::kTF32, 8>), grid, dim3(512), 0, s, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -383,7 +449,7 @@ int mpgemm_i8_gemm(int out_type, int64_t groups, int64_t M, int64_t N, int64_t K
         a.scale_w = scale_w;
         a.bias = bias;
         forget_error();
-        kNarrowI8Launch[out_type](a, dim3((unsigned)grid), stream_of(stream));
+        kNarrowI8Launch[out_type](a, grid, stream_of(stream));
         return launched();
     }
     const I8Entry &e = kI8Table[id];
@@ -593,12 +659,12 @@ int mpgemm_grouped(int in_type, int layout_b, int64_t groups, int64_t R, int64_t
         a.beta = beta;
         forget_error();
         if (in_type == MPGEMM_IN_BF16)
-            launch_grouped_narrow<kInBF16>(a, dim3((unsigned)grid), stream_of(stream));
+            launch_narrow<kInBF16, mpg::kTF32>(a, grid, stream_of(stream));
         else
-            launch_grouped_narrow<kInF16>(a, dim3((unsigned)grid), stream_of(stream));
+            launch_narrow<kInF16, mpg::kTF32>(a, grid, stream_of(stream));
         return launched();
     }
-    const GroupedEntry &e = table[id < 0 ? kGroupedSmall : id];
+    const GroupedEntry &e = table[id < 0 ? kGroupedFew : id];
     if (!grouped_fits(e, kRowMajor, layout_b, lda, ldb, ldc))
         return MPGEMM_ELD;
     const int64_t tiles_n = cdiv(N, e.bn);

@@ -162,8 +162,8 @@ int mpgemm_combine_rows_backward(int d_type, int y_type, int dy_type,
  * A: R x K row-major, C: R x N FP32 row-major, B_g at B + g*stride_b, K x N
  * in storage order layout_b.  The gradient by A is this call on C's gradient
  * with B in the other storage order (N and K exchanged).
- * 16 rows of A, C or a column-major B, and 128 of a row-major B, within 2 GiB
- * (else MPGEMM_ELD).  R, N and K below 2^31.
+ * 128 stored rows of A, of one group's B and of C within 2 GiB (else
+ * MPGEMM_ELD).  R, N and K below 2^31.
  */
 int mpgemm_grouped(int in_type, int layout_b, int64_t groups, int64_t R, int64_t N, int64_t K,
                    const uint16_t *A, int64_t lda, const uint16_t *B, int64_t ldb, int64_t stride_b,
