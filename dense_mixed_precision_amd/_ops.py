@@ -122,16 +122,24 @@ def _type(t, name, types=(MPGEMM_T_F16, MPGEMM_T_BF16, MPGEMM_T_F32)):
 
 def _rows(t, name, dtype):
     """Leading dimension of a row-major 2-D GPU tensor."""
+    import torch
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.dim() == 2:
+        # the ordinary case at once; the rest, and what is refused, below
+        ld, step = t.stride()
+        rows, cols = t.shape
+        if step == 1 and rows > 1 and ld >= cols > 0:
+            return ld
     return _check_tensor(t, name, dtype)[1]
 
 
 def _flat(t, name, dtype, shape):
-    """Pointer of a contiguous GPU tensor of one dtype and shape."""
+    """Pointer of a contiguous GPU tensor of one dtype and shape (None: any)."""
     import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         raise TypeError(f"{name} must be a {str(dtype).replace('torch.', '')} tensor")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous, of shape {tuple(shape)}, got {tuple(t.shape)}")
+    if (shape is not None and t.shape != shape) or not t.is_contiguous():
+        want = "" if shape is None else f", of shape {tuple(shape)}, got {tuple(t.shape)}"
+        raise ValueError(f"{name} must be contiguous{want}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU")
     return t.data_ptr()
@@ -160,34 +168,35 @@ def _matrices(t, name, dtype):
     return groups, rows, cols, layout, ld, (sg if groups > 1 else 0)
 
 
-class _On:
-    """The device and stream of a call: every tensor on one GPU, the launch on
-    that GPU's current stream or the one given, with that GPU current."""
+def _on(stream, *tensors):
+    """(device, stream handle) of a call: every tensor on one GPU, the launch
+    on that GPU's current stream or the one given."""
+    import torch
+    device = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors are on {device} and {t.device}: one GPU is needed")
+    if stream is None:
+        # the handle alone: a Stream object costs as much as a small launch
+        return device, torch._C._cuda_getCurrentRawStream(device.index)
+    if hasattr(stream, "cuda_stream"):
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        return device, stream.cuda_stream
+    return device, int(stream)
 
-    def __init__(self, stream, *tensors):
-        import torch
-        self.device = tensors[0].device
-        for t in tensors[1:]:
-            if t is not None and t.device != self.device:
-                raise ValueError(f"tensors are on {self.device} and {t.device}: one GPU is needed")
-        if stream is None:
-            self.handle = torch.cuda.current_stream(self.device).cuda_stream
-        elif hasattr(stream, "cuda_stream"):
-            if stream.device != self.device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
-            self.handle = stream.cuda_stream
-        else:
-            self.handle = int(stream)
 
-    def call(self, fn, *args):
-        import torch
-        if torch.cuda.current_device() == self.device.index:
-            rc = fn(*args, self.handle)
-        else:
-            with torch.cuda.device(self.device):
-                rc = fn(*args, self.handle)
-        if rc != MPGEMM_OK:
-            raise MpgemmError(rc, fn.__name__)
+def _call(fn, on, *args):
+    """fn(*args, stream) with the tensors' GPU current; raises on an error."""
+    import torch
+    device, handle = on
+    if torch._C._cuda_getDevice() == device.index:
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, handle)
+    if rc != MPGEMM_OK:
+        raise MpgemmError(rc, fn.__name__)
 
 
 def quantize_rows(X, Q, scale, order=None, top_k: int = 1, stream=None):
@@ -209,8 +218,8 @@ def quantize_rows(X, Q, scale, order=None, top_k: int = 1, stream=None):
         raise ValueError(f"shape mismatch: X {tuple(X.shape)}, Q {tuple(Q.shape)}")
     sp = _flat(scale, "scale", torch.float32, (R,))
     op = 0 if order is None else _flat(order, "order", torch.int32, (R,))
-    _On(stream, X, Q, scale, order).call(mpgemm_quantize_rows, xt, T, H, X.data_ptr(), ldx, op, R, int(top_k),
-                                         Q.data_ptr(), ldq, sp)
+    _call(load_ops().mpgemm_quantize_rows, _on(stream, X, Q, scale, order), xt, T, H, X.data_ptr(), ldx, op, R,
+          int(top_k), Q.data_ptr(), ldq, sp)
     return Q, scale
 
 
@@ -252,9 +261,8 @@ def gemm_i8(A, B, C, scale_a, scale_b, bias=None, offsets=None, stream=None):
     sb = _flat(scale_b, "scale_b", torch.float32, wide)
     bp = 0 if bias is None else _flat(bias, "bias", torch.float32, wide)
     op = 0 if offsets is None else _flat(offsets, "offsets", torch.int32, (G + 1,))
-    _On(stream, C, A, B, scale_a, scale_b, bias, offsets).call(
-        mpgemm_i8_gemm, ot, G, M, N, K, A.data_ptr(), lda, B.data_ptr(), ldw, stride, C.data_ptr(), ldc, sa, sb, bp,
-        op)
+    _call(load_ops().mpgemm_i8_gemm, _on(stream, C, A, B, scale_a, scale_b, bias, offsets), ot, G, M, N, K,
+          A.data_ptr(), lda, B.data_ptr(), ldw, stride, C.data_ptr(), ldc, sa, sb, bp, op)
     return C
 
 
@@ -285,10 +293,10 @@ def route(experts, num_experts: int, out=None, workspace=None, stream=None):
     if workspace is not None and (not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.int32
                                   or not workspace.is_contiguous() or not workspace.is_cuda):
         raise TypeError("workspace must be a contiguous int32 tensor on the GPU")
-    on = _On(stream, experts, *given, workspace)
+    on = _on(stream, experts, *given, workspace)
 
     def allocate():
-        new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=on.device)  # noqa: E731
+        new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=on[0])  # noqa: E731
         return (given or (new(pairs), new(*experts.shape), new(E + 1)),
                 new(need // 4) if workspace is None and need else workspace)
 
@@ -297,15 +305,15 @@ def route(experts, num_experts: int, out=None, workspace=None, stream=None):
     else:
         # memory from the launch's own stream: what the current stream freed
         # may still be in use there
-        with torch.cuda.stream(torch.cuda.ExternalStream(on.handle, device=on.device)):
+        with torch.cuda.stream(torch.cuda.ExternalStream(on[1], device=on[0])):
             given, workspace = allocate()
     order, position, offsets = given
     op = _flat(order, "order", torch.int32, (pairs,))
     pp = _flat(position, "position", torch.int32, experts.shape)
     fp = _flat(offsets, "offsets", torch.int32, (E + 1,))
-    on.call(mpgemm_route, MPGEMM_ID_I64 if experts.dtype == torch.int64 else MPGEMM_ID_I32, pairs, E,
-            experts.data_ptr(), op, pp, fp, 0 if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else 4 * workspace.numel())
+    _call(load_ops().mpgemm_route, on, MPGEMM_ID_I64 if experts.dtype == torch.int64 else MPGEMM_ID_I32, pairs, E,
+          experts.data_ptr(), op, pp, fp, 0 if workspace is None else workspace.data_ptr(),
+          0 if workspace is None else 4 * workspace.numel())
     return order, position, offsets
 
 
@@ -321,8 +329,8 @@ def gather_rows(X, order, Y, top_k: int = 1, stream=None):
     if X.shape[1] != Y.shape[1]:
         raise ValueError(f"shape mismatch: X {tuple(X.shape)}, Y {tuple(Y.shape)}")
     op = _flat(order, "order", torch.int32, (Y.shape[0],))
-    _On(stream, Y, X, order).call(mpgemm_gather_rows, ty, X.shape[0], X.shape[1], X.data_ptr(), ldx, op, Y.shape[0],
-                                  int(top_k), Y.data_ptr(), ldy)
+    _call(load_ops().mpgemm_gather_rows, _on(stream, Y, X, order), ty, X.shape[0], X.shape[1], X.data_ptr(), ldx,
+          op, Y.shape[0], int(top_k), Y.data_ptr(), ldy)
     return Y
 
 
@@ -345,11 +353,11 @@ def combine_rows(Y, position, out, weights=None, stream=None):
     T, H = out.shape
     if Y.shape[1] != H:
         raise ValueError(f"shape mismatch: Y {tuple(Y.shape)}, out {tuple(out.shape)}")
-    pp = _flat(position, "position", torch.int32, position.shape)
+    pp = _flat(position, "position", torch.int32, None)
     k = _slots(position, T)
     wp = 0 if weights is None else _flat(weights, "weights", torch.float32, (T, k))
-    _On(stream, out, Y, position, weights).call(mpgemm_combine_rows, yt, ot, T, k, H, Y.shape[0], Y.data_ptr(), ldy,
-                                                pp, wp, out.data_ptr(), ldo)
+    _call(load_ops().mpgemm_combine_rows, _on(stream, out, Y, position, weights), yt, ot, T, k, H, Y.shape[0],
+          Y.data_ptr(), ldy, pp, wp, out.data_ptr(), ldo)
     return out
 
 
@@ -375,13 +383,12 @@ def combine_rows_backward(dout, Y, position, weights, dY, dweights=None, stream=
         raise ValueError("dweights needs Y")
     if dY.shape[1] != H:
         raise ValueError(f"shape mismatch: dout {tuple(dout.shape)}, dY {tuple(dY.shape)}")
-    pp = _flat(position, "position", torch.int32, position.shape)
+    pp = _flat(position, "position", torch.int32, None)
     k = _slots(position, T)
     wp = 0 if weights is None else _flat(weights, "weights", torch.float32, (T, k))
     gp = 0 if dweights is None else _flat(dweights, "dweights", torch.float32, (T, k))
-    _On(stream, dY, dout, Y, position, weights, dweights).call(
-        mpgemm_combine_rows_backward, dt, yt, gt, T, k, H, dY.shape[0], dout.data_ptr(), ldo, yp, ldy, pp, wp,
-        dY.data_ptr(), ldg, gp)
+    _call(load_ops().mpgemm_combine_rows_backward, _on(stream, dY, dout, Y, position, weights, dweights), dt, yt,
+          gt, T, k, H, dY.shape[0], dout.data_ptr(), ldo, yp, ldy, pp, wp, dY.data_ptr(), ldg, gp)
     return dY, dweights
 
 
@@ -401,8 +408,8 @@ def gemm_grouped(A, B, C, offsets, alpha: float = 1.0, beta: float = 0.0, stream
     if K2 != K or tuple(C.shape) != (R, N):
         raise ValueError(f"shape mismatch: A {tuple(A.shape)}, B {tuple(B.shape)}, C {tuple(C.shape)}")
     op = _flat(offsets, "offsets", torch.int32, (G + 1,))
-    _On(stream, C, A, B, offsets).call(mpgemm_grouped, it, layout, G, R, N, K, A.data_ptr(), lda, B.data_ptr(), ldb,
-                                       stride, C.data_ptr(), ldc, float(alpha), float(beta), op)
+    _call(load_ops().mpgemm_grouped, _on(stream, C, A, B, offsets), it, layout, G, R, N, K, A.data_ptr(), lda,
+          B.data_ptr(), ldb, stride, C.data_ptr(), ldc, float(alpha), float(beta), op)
     return C
 
 
@@ -425,6 +432,6 @@ def gemm_grouped_wgrad(A, B, C, offsets, alpha: float = 1.0, beta: float = 0.0, 
     if tuple(A.shape) != (M, R) or B.shape[1] != N:
         raise ValueError(f"shape mismatch: A {tuple(A.shape)}, B {tuple(B.shape)}, C {tuple(C.shape)}")
     op = _flat(offsets, "offsets", torch.int32, (G + 1,))
-    _On(stream, C, A, B, offsets).call(mpgemm_grouped_wgrad, it, G, R, M, N, A.data_ptr(), lda, B.data_ptr(), ldb,
-                                       C.data_ptr(), ldc, stride, float(alpha), float(beta), op)
+    _call(load_ops().mpgemm_grouped_wgrad, _on(stream, C, A, B, offsets), it, G, R, M, N, A.data_ptr(), lda,
+          B.data_ptr(), ldb, C.data_ptr(), ldc, stride, float(alpha), float(beta), op)
     return C

@@ -304,7 +304,13 @@ int select_wgrad(const GroupedEntry *table, int64_t groups, int64_t M, int64_t N
 template <int XT>
 void launch_quantize(const mpg::QuantArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((mpg::quantize_rows<XT, 256>), dim3((unsigned)a.R), dim3(256), 0, s, a);
+    // One wave per row where there are rows for every wave slot and a wave
+    // holds a row in 8 vectors per lane; else one workgroup per row.
+    constexpr int64_t kWaveRow = 64 * 8 * (XT == mpg::kTF32 ? 4 : 8);
+    if (a.R >= 8 * kNumCu && a.H <= kWaveRow)
+        hipLaunchKernelGGL((mpg::quantize_rows<XT, 64, 8>), dim3((unsigned)cdiv(a.R, 4)), dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((mpg::quantize_rows<XT, 256, 4>), dim3((unsigned)a.R), dim3(256), 0, s, a);
 }
 
 template <int YT>
@@ -568,7 +574,7 @@ int mpgemm_combine_rows(int y_type, int o_type, int64_t T, int64_t top_k, int64_
     if (!aligned(Y, size_of(y_type)) || !aligned(O, size_of(o_type)) || !aligned(position, 4) || !aligned(weights, 4))
         return MPGEMM_EALIGN;
     const mpg::CombineArgs a{Y, O, position, weights, ldy, ldo, (int32_t)T, (int32_t)H, (int32_t)R, (int32_t)top_k};
-    const int64_t gy = cdiv(H, 1024);
+    const int64_t gy = cdiv(H, y_type == MPGEMM_T_F32 ? 1024 : 2048);
     const dim3 grid((unsigned)T, (unsigned)(gy < 65535 ? gy : 65535));
     forget_error();
     if (y_type == MPGEMM_T_F16)

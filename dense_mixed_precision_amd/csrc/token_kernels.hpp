@@ -18,26 +18,42 @@ struct VecOf {
 // Rows to 8-bit codes
 // ---------------------------------------------------------------------------
 // One row x: m = max|x|, scale = m/127, code = the whole number nearest
-// 127*x/m, the even one in the middle.  The quotient is compared exactly:
-// with x and m scaled by the power of two that brings m near 1 (exact),
-// p + lo = 127*x in two floats, q = rint(p*(1/m)) is off by one at most, and
-// d = p - q*m (one fma, exact: |d| is about m/2 and a multiple of the
+// 127*x/m, the even one in the middle, decided exactly.  x and m are first
+// scaled by the power of two that brings m to [1, 2) (exact).
+//
+// 16-bit x: p = 127*x is exact, and p/m rounded correctly to FP32 decides.  In
+// whole numbers p = P*2^j, m = A*2^i with A < 2^11 and j <= i (or the same with
+// j = i): a quotient that is no middle lies at least 2^(j-i)/(2A) > 2^(j-i-12)
+// from one, and p/m < 2^(j-i+8) has an FP32 error below 2^(j-i-16); a middle
+// is an FP32 number itself.  The quotient is p*inv plus its exact remainder
+// times inv, which is correctly rounded as inv is.
+//
+// FP32 x: p + lo = 127*x in two floats, q = rint(p*inv) is off by one at most,
+// and d = p - q*m (one fma, exact: |d| is about m/2 and a multiple of the
 // operands' last places) plus lo against +-m/2 says which way.
-__device__ __forceinline__ int code_of(float x, float m, float inv)
+template <int XT>
+__device__ __forceinline__ int code_of(float x, float f, float f127, float m, float inv)
 {
-    const float p = 127.0f * x;
-    const float lo = __builtin_fmaf(127.0f, x, -p);
-    float q = __builtin_rintf(p * inv);
-    const float d = __builtin_fmaf(-q, m, p);
-    const float h = 0.5f * m;
-    const float over = (d - h) + lo;    // > 0: above the middle of q and q + 1
-    const float under = (d + h) + lo;   // < 0: below the middle of q - 1 and q
-    const bool odd = ((int)q & 1) != 0;
-    if (over > 0.0f || (over == 0.0f && odd))
-        q += 1.0f;
-    else if (under < 0.0f || (under == 0.0f && odd))
-        q -= 1.0f;
-    return (int)q;
+    if constexpr (XT != kTF32) {
+        const float p = x * f127;
+        const float t = p * inv;
+        return (int)__builtin_rintf(__builtin_fmaf(__builtin_fmaf(-t, m, p), inv, t));
+    } else {
+        x *= f;
+        const float p = 127.0f * x;
+        const float lo = __builtin_fmaf(127.0f, x, -p);
+        float q = __builtin_rintf(p * inv);
+        const float d = __builtin_fmaf(-q, m, p);
+        const float h = 0.5f * m;
+        const float over = (d - h) + lo;    // > 0: above the middle of q and q + 1
+        const float under = (d + h) + lo;   // < 0: below the middle of q - 1 and q
+        const bool odd = ((int)q & 1) != 0;
+        if (over > 0.0f || (over == 0.0f && odd))
+            q += 1.0f;
+        else if (under < 0.0f || (under == 0.0f && odd))
+            q -= 1.0f;
+        return (int)q;
+    }
 }
 
 struct QuantArgs {
@@ -49,26 +65,31 @@ struct QuantArgs {
     int32_t T, H, R, top_k;
 };
 
-// One workgroup of NT threads per row.  The first CACHE vectors of each thread stay
-// in registers between the maximum and the codes; longer rows are read again.
-template <int XT, int NT>
-__global__ void __launch_bounds__(NT)
+// NT threads per row, 256 / NT rows per workgroup.  The first CACHE vectors
+// of each thread stay in registers between the maximum and the codes; longer
+// rows are read again.  With NT = 64 a row is one wave's: no barrier, and the
+// 32 waves of a compute unit keep as many rows in flight.
+template <int XT, int NT, int CACHE>
+__global__ void __launch_bounds__(256)
 quantize_rows(QuantArgs args)
 {
     typedef typename ElemOf<XT>::type E;
     constexpr int VN = VecOf<E>::N;
-    constexpr int CACHE = 4;
     typedef typename VecOf<E>::type V;
-    __shared__ uint32_t part[NT / 64];
-    const int row = blockIdx.x;
-    int src = row;
+    __shared__ uint32_t part[4];
+    const int tid = threadIdx.x % NT;
+    const int64_t row = (int64_t)blockIdx.x * (256 / NT) +
+                        (NT == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : 0);
+    if (row >= args.R)
+        return;
+    int64_t src = row;
     if (args.order) {
         const int pair = args.order[row];
         src = pair < 0 ? -1 : pair / args.top_k;
         if (src < 0 || src >= args.T)
             return;  // no such row: what is there stays
     }
-    const E *const x = (const E *)args.X + (int64_t)src * args.ldx;
+    const E *const x = (const E *)args.X + src * args.ldx;
     const int H = args.H;
     const int nv = H / VN;
     V keep[CACHE];
@@ -80,23 +101,23 @@ quantize_rows(QuantArgs args)
     };
 #pragma unroll
     for (int c = 0; c < CACHE; ++c) {
-        const int i = c * NT + threadIdx.x;
+        const int i = c * NT + tid;
         if (i < nv)
             keep[c] = *(const V *)(x + (int64_t)i * VN);
     }
 #pragma unroll
     for (int c = 0; c < CACHE; ++c)
-        if (c * NT + (int)threadIdx.x < nv)
+        if (c * NT + tid < nv)
 #pragma unroll
             for (int e = 0; e < VN; ++e)
                 see(keep[c].v[e]);
-    for (int i = CACHE * NT + threadIdx.x; i < nv; i += NT) {
+    for (int i = CACHE * NT + tid; i < nv; i += NT) {
         const V v = *(const V *)(x + (int64_t)i * VN);
 #pragma unroll
         for (int e = 0; e < VN; ++e)
             see(v.v[e]);
     }
-    for (int i = nv * VN + threadIdx.x; i < H; i += NT)
+    for (int i = nv * VN + tid; i < H; i += NT)
         see(x[i]);
 #pragma unroll
     for (int d = 32; d > 0; d /= 2) {
@@ -104,8 +125,8 @@ quantize_rows(QuantArgs args)
         top = o > top ? o : top;
     }
     if constexpr (NT > 64) {
-        if ((threadIdx.x & 63) == 0)
-            part[threadIdx.x / 64] = top;
+        if ((tid & 63) == 0)
+            part[tid / 64] = top;
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < NT / 64; ++w)
@@ -115,17 +136,18 @@ quantize_rows(QuantArgs args)
     const bool finite = top < 0x7F800000u;
     const bool live = finite && top != 0;
     // the power of two that brings the maximum to [1, 2), as far as one
-    // float holds it
+    // float holds it; a row of zeros or with no scale has codes 0 by f = 0
     int ex = (int)(top >> 23) - 127;
     ex = ex < -100 ? -100 : ex > 126 ? 126 : ex;
-    const float f = __builtin_bit_cast(float, (uint32_t)(127 - ex) << 23);
+    const float f = live ? __builtin_bit_cast(float, (uint32_t)(127 - ex) << 23) : 0.0f;
+    const float f127 = 127.0f * f;
     const float m = live ? most * f : 1.0f;
     const float inv = 1.0f / m;
-    if (threadIdx.x == 0)
+    if (tid == 0)
         args.scale[row] = finite ? most / 127.0f : __builtin_nanf("");
-    int8_t *const q = args.Q + (int64_t)row * args.ldq;
+    int8_t *const q = args.Q + row * args.ldq;
     auto code = [&](E e) __attribute__((always_inline)) {
-        return live ? code_of((float)e * f, m, inv) : 0;
+        return finite ? code_of<XT>((float)e, f, f127, m, inv) : 0;
     };
     auto emit = [&](int i, const V &v) __attribute__((always_inline)) {
         Pack<int8_t, VN> o;
@@ -136,11 +158,11 @@ quantize_rows(QuantArgs args)
     };
 #pragma unroll
     for (int c = 0; c < CACHE; ++c)
-        if (c * NT + (int)threadIdx.x < nv)
-            emit(c * NT + threadIdx.x, keep[c]);
-    for (int i = CACHE * NT + threadIdx.x; i < nv; i += NT)
+        if (c * NT + tid < nv)
+            emit(c * NT + tid, keep[c]);
+    for (int i = CACHE * NT + tid; i < nv; i += NT)
         emit(i, *(const V *)(x + (int64_t)i * VN));
-    for (int i = nv * VN + threadIdx.x; i < H; i += NT)
+    for (int i = nv * VN + tid; i < H; i += NT)
         q[i] = (int8_t)code(x[i]);
 }
 
@@ -388,8 +410,18 @@ gather_rows(GatherArgs a)
     const uint8_t *const x = a.X + (int64_t)t * a.ldx;
     uint8_t *const y = a.Y + p * a.ldy;
     const int nv = a.row_bytes / 16;
-    for (int i = lane; i < nv; i += 64)
-        *(Bytes16 *)(y + (int64_t)i * 16) = *(const Bytes16 *)(x + (int64_t)i * 16);
+    // 4 KiB at a time: the loads first, so that they are in flight together
+    for (int i0 = lane; i0 < nv; i0 += 256) {
+        Bytes16 v[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (i0 + 64 * c < nv)
+                v[c] = *(const Bytes16 *)(x + (int64_t)(i0 + 64 * c) * 16);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (i0 + 64 * c < nv)
+                *(Bytes16 *)(y + (int64_t)(i0 + 64 * c) * 16) = v[c];
+    }
     for (int i = nv * 16 + lane; i < a.row_bytes; i += 64)
         y[i] = x[i];
 }
@@ -404,35 +436,54 @@ struct CombineArgs {
 };
 
 // O[t] = sum_s weights[t][s] * Y[position[t][s]], in FP32, slots ascending;
-// one thread per 4 columns of a token.
+// one thread per 16 bytes of a row of Y.  Four slots' rows are loaded before the
+// first is used.
 template <int YT, int OT>
 __global__ void __launch_bounds__(256)
 combine_rows(CombineArgs a)
 {
     typedef typename ElemOf<YT>::type EY;
     typedef typename ElemOf<OT>::type EO;
+    constexpr int VN = VecOf<EY>::N;
+    typedef typename VecOf<EY>::type V;
     const int64_t t = blockIdx.x;
-    for (int c = 4 * (blockIdx.y * 256 + threadIdx.x); c < a.H; c += 4 * 256 * gridDim.y) {
-        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int s = 0; s < a.top_k; ++s) {
-            const int p = a.position[t * a.top_k + s];
-            if (p < 0 || p >= a.R)
-                continue;
-            const float w = a.weights ? a.weights[t * a.top_k + s] : 1.0f;
-            const EY *const y = (const EY *)a.Y + (int64_t)p * a.ldy + c;
-            if (c + 4 <= a.H) {
-                const Pack<EY, 4> v = *(const Pack<EY, 4> *)y;
+    const int32_t *const at = a.position + t * a.top_k;
+    for (int64_t c = (int64_t)VN * (blockIdx.y * 256 + threadIdx.x); c < a.H; c += (int64_t)VN * 256 * gridDim.y) {
+        const int left = (int)(a.H - c);
+        float acc[VN];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[e] = __builtin_fmaf(w, (float)v.v[e], acc[e]);
-            } else {
+        for (int e = 0; e < VN; ++e)
+            acc[e] = 0.0f;
+        for (int s0 = 0; s0 < a.top_k; s0 += 4) {
+            V v[4];
+            float w[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (c + e < a.H)
-                        acc[e] = __builtin_fmaf(w, (float)y[e], acc[e]);
+            for (int j = 0; j < 4; ++j) {
+                const int p = s0 + j < a.top_k ? at[s0 + j] : -1;
+                w[j] = 0.0f;
+#pragma unroll
+                for (int e = 0; e < VN; ++e)
+                    v[j].v[e] = (EY)0.0f;
+                if (p >= 0 && p < a.R) {
+                    w[j] = a.weights ? a.weights[t * a.top_k + s0 + j] : 1.0f;
+                    const EY *const y = (const EY *)a.Y + (int64_t)p * a.ldy + c;
+                    if (left >= VN) {
+                        v[j] = *(const V *)y;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < VN; ++e)
+                            if (e < left)
+                                v[j].v[e] = y[e];
+                    }
+                }
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < VN; ++e)
+                    acc[e] = __builtin_fmaf(w[j], (float)v[j].v[e], acc[e]);
         }
-        i8_store<OT, 4>((EO *)a.O + t * a.ldo, c, a.H - c, acc);
+        i8_store<OT, VN>((EO *)a.O + t * a.ldo + c, 0, left, acc);
     }
 }
 
