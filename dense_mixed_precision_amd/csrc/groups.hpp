@@ -35,6 +35,19 @@ __device__ __forceinline__ int xcd_order(int bid, int nb)
     return (xcd < rem) ? xcd * (per + 1) + local : rem * (per + 1) + (xcd - rem) * per + local;
 }
 
+// The same with the tiles dealt to the XCDs in runs of 16: a group's tiles
+// take as long as it has rows, so whole groups per XCD would leave the XCDs of
+// the short ones idle.
+__device__ __forceinline__ int dealt_order(int bid, int nb)
+{
+    constexpr int RUN = 16;
+    if (bid >= nb / (RUN * kNumXcd) * (RUN * kNumXcd))
+        return bid;
+    const int xcd = bid % kNumXcd;
+    const int local = bid / kNumXcd;
+    return ((local / RUN) * kNumXcd + xcd) * RUN + local % RUN;
+}
+
 // Tile of this workgroup among all groups' ceil(rows/bm) x tiles_n tiles,
 // groups one after the other.  Every wave works it out for itself (64 groups
 // at a time, one per lane, a prefix sum over lanes), so no barrier and no
@@ -129,7 +142,7 @@ __device__ __forceinline__ bool locate_group(GemmArgs &args, const GroupArgs &ga
         tn = t.tn;
     } else {
         const int per = args.tiles_m * args.tiles_n;
-        const int t = xcd_order(blockIdx.x, gridDim.x);
+        const int t = dealt_order(blockIdx.x, gridDim.x);
         const int g = t / per;
         const int start = clamp_row(ga.offsets[g], 0, ga.rows);
         const int rows = clamp_row(ga.offsets[g + 1], start, ga.rows) - start;
@@ -138,10 +151,11 @@ __device__ __forceinline__ bool locate_group(GemmArgs &args, const GroupArgs &ga
         args.C += (int64_t)g * ga.stride;
         args.K = args.alpha == 0.0f ? 0 : rows;
         const int local = t - g * per;
-        const int band = args.group_m * args.tiles_n;
-        const int first_m = (local / band) * args.group_m;
+        // (bands of 4 tile rows: 16 tiles in a row are a 4x4 block)
+        const int band = 4 * args.tiles_n;
+        const int first_m = (local / band) * 4;
         const int in_band = local % band;
-        const int height = min(args.tiles_m - first_m, args.group_m);
+        const int height = min(args.tiles_m - first_m, 4);
         tm = first_m + in_band % height;
         tn = in_band / height;
     }

@@ -325,6 +325,23 @@ i8_tile(I8Args args)
             read_w(0, 0, 0, f);
     }
     int buf = 0;
+    // A wave whose part of the tile lies outside the product only copies: the
+    // matrix cores are left to the waves with work.
+    if (wm * Cfg::WTM >= rows_left || wn * Cfg::WTN >= cols_left) {
+        for (int kt = 0; kt < num_k; ++kt) {
+            const int nbuf = (buf + 1 == S) ? 0 : buf + 1;
+            if (kt + 1 < num_k) {
+                const int newer = num_k - 2 - kt;
+                publish(kt + 1, nbuf, newer < S - 2 ? newer : S - 2);
+            }
+            begin_copies(kt + S, buf);
+#pragma unroll
+            for (int c = 0; c < NCOPY; ++c)
+                copy_one(c);
+            buf = nbuf;
+        }
+        return;
+    }
     for (int kt = 0; kt < num_k; ++kt) {
         const int nbuf = (buf + 1 == S) ? 0 : buf + 1;
 #pragma unroll

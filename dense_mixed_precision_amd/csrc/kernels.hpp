@@ -895,6 +895,27 @@ gemm_pipe(GemmArgs args_in)
             read_group(0, ks0, 0, grp);
     }
     int buf = 0;
+#ifdef MPGEMM_GROUPED
+    // A wave whose part of the tile lies outside the product (the last tile
+    // of a group's rows) only copies: the matrix cores are left to the
+    // waves with work.
+    static_assert(Cfg::KGROUPS == 1, "every wave has a part of the tile");
+    if (wm * Cfg::WTM >= rows_left || wn * Cfg::WTN >= cols_left) {
+        for (int64_t kt = 0; kt < num_k; ++kt) {
+            const int nbuf = (buf + 1 == S) ? 0 : buf + 1;
+            if (kt + 1 < num_k) {
+                const int64_t newer = num_k - 2 - kt;
+                publish(kt + 1, nbuf, (int)(newer < S - 2 ? newer : S - 2));
+            }
+            begin_copies(kt + S, buf);
+#pragma unroll
+            for (int c = 0; c < NCOPY; ++c)
+                copy_one(c);
+            buf = nbuf;
+        }
+        return;
+    }
+#endif
     for (int64_t kt = 0; kt < num_k; ++kt) {
         const int nbuf = (buf + 1 == S) ? 0 : buf + 1;
 

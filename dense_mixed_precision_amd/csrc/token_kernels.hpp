@@ -201,6 +201,19 @@ __device__ __forceinline__ int expert_of(const RouteArgs &a, int i)
     }
 }
 
+// Up to kRouteRun pairs of a wave's at a time, their experts loaded together.
+constexpr int kRouteRun = 8;
+
+template <int WIDE>
+__device__ __forceinline__ void load_experts(const RouteArgs &a, int i0, int last, int lane, int (&e)[kRouteRun])
+{
+#pragma unroll
+    for (int r = 0; r < kRouteRun; ++r) {
+        const int i = i0 + 64 * r + lane;
+        e[r] = i < last ? expert_of<WIDE>(a, i) : -1;
+    }
+}
+
 // Counts of one wave's pairs into its LDS row (zeroed here).
 template <int WIDE>
 __device__ __forceinline__ void route_count(const RouteArgs &a, int32_t *cnt, int first, int last, int lane)
@@ -208,32 +221,45 @@ __device__ __forceinline__ void route_count(const RouteArgs &a, int32_t *cnt, in
     for (int e = lane; e <= a.E; e += 64)
         cnt[e] = 0;
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    for (int i = first + lane; i < last; i += 64)
-        atomicAdd(&cnt[expert_of<WIDE>(a, i)], 1);
+    for (int i0 = first; i0 < last; i0 += 64 * kRouteRun) {
+        int e[kRouteRun];
+        load_experts<WIDE>(a, i0, last, lane, e);
+#pragma unroll
+        for (int r = 0; r < kRouteRun; ++r)
+            if (e[r] >= 0)
+                atomicAdd(&cnt[e[r]], 1);
+    }
 }
 
 // Positions of one wave's pairs, from the counters at their first positions.
 template <int WIDE>
 __device__ __forceinline__ void route_place(const RouteArgs &a, int32_t *cnt, int first, int last, int lane)
 {
-    for (int i0 = first; i0 < last; i0 += 64) {
-        const int i = i0 + lane;
-        const bool ok = i < last;
-        const int e = ok ? expert_of<WIDE>(a, i) : a.E;
-        uint64_t same = __ballot(ok);
-        for (int b = 0; b < a.bits; ++b) {
-            const uint64_t set = __ballot((e >> b) & 1);
-            same &= ((e >> b) & 1) ? set : ~set;
-        }
-        const int rank = __builtin_popcountll(same & ((1ull << lane) - 1));
-        int base = 0;
-        if (ok && rank == 0)
-            base = atomicAdd(&cnt[e], __builtin_popcountll(same));
-        base = __shfl(base, ok ? __builtin_ctzll(same) : lane);
-        if (ok) {
-            const int p = base + rank;
-            a.order[p] = e < a.E ? i : -1;
-            a.position[i] = e < a.E ? p : -1;
+    for (int i0 = first; i0 < last; i0 += 64 * kRouteRun) {
+        int ex[kRouteRun];
+        load_experts<WIDE>(a, i0, last, lane, ex);
+#pragma unroll
+        for (int r = 0; r < kRouteRun; ++r) {
+            const int i = i0 + 64 * r + lane;
+            const int e = ex[r];
+            const bool ok = e >= 0;
+            uint64_t same = __ballot(ok);
+            if (same == 0)
+                break;
+            for (int b = 0; b < a.bits; ++b) {
+                const uint64_t set = __ballot((e >> b) & 1);
+                same &= ((e >> b) & 1) ? set : ~set;
+            }
+            const int rank = __builtin_popcountll(same & ((1ull << lane) - 1));
+            int base = 0;
+            if (ok && rank == 0)
+                base = atomicAdd(&cnt[e], __builtin_popcountll(same));
+            base = __shfl(base, ok ? __builtin_ctzll(same) : lane);
+            if (ok) {
+                const int p = base + rank;
+                a.order[p] = e < a.E ? i : -1;
+                a.position[i] = e < a.E ? p : -1;
+            }
         }
     }
 }
