@@ -35,7 +35,7 @@ mpgemm_timeline_clear() -- per-workgroup stamps of the pipelined kernel.
 
 Operators beside the GEMM (libmpgemm_ops.so, include/mpgemm_ops.h): raw entry
 points mpgemm_quantize_rows, mpgemm_i8_gemm, mpgemm_route_workspace,
-mpgemm_route, mpgemm_gather_rows, mpgemm_combine_rows,
+mpgemm_route, mpgemm_rows_workspace, mpgemm_gather_rows, mpgemm_combine_rows,
 mpgemm_combine_rows_backward, mpgemm_grouped and mpgemm_grouped_wgrad, and
 for torch tensors
     quantize_rows(X, Q, scale, order, top_k)      rows to 8-bit codes
@@ -135,6 +135,7 @@ from ._ops import (  # noqa: F401
     mpgemm_quantize_rows,
     mpgemm_route,
     mpgemm_route_workspace,
+    mpgemm_rows_workspace,
     quantize_rows,
     route,
 )

@@ -34,11 +34,12 @@ def load_ops():
     lib = ctypes.CDLL(OPS_PATH)
     i64, f32, vp, i32 = ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_int
     for name, args, res in (
-            ("mpgemm_quantize_rows", [i32, i64, i64, vp, i64, vp, i64, i64, vp, i64, vp, vp], i32),
+            ("mpgemm_quantize_rows", [i32, i64, i64, vp, i64, vp, i64, i64, vp, i64, vp, vp, i64, vp], i32),
+            ("mpgemm_rows_workspace", [i32, i64, i64, i64, i64], i64),
             ("mpgemm_i8_gemm", [i32, i64, i64, i64, i64, vp, i64, vp, i64, i64, vp, i64, vp, vp, vp, vp, vp], i32),
             ("mpgemm_route_workspace", [i64, i64], i64),
             ("mpgemm_route", [i32, i64, i64, vp, vp, vp, vp, vp, i64, vp], i32),
-            ("mpgemm_gather_rows", [i32, i64, i64, vp, i64, vp, i64, i64, vp, i64, vp], i32),
+            ("mpgemm_gather_rows", [i32, i64, i64, vp, i64, vp, i64, i64, vp, i64, vp, i64, vp], i32),
             ("mpgemm_combine_rows", [i32, i32, i64, i64, i64, i64, vp, i64, vp, vp, vp, i64, vp], i32),
             ("mpgemm_combine_rows_backward",
              [i32, i32, i32, i64, i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, vp], i32),
@@ -53,8 +54,16 @@ def load_ops():
 
 # ---- raw entry points (same names and argument order as the C ABI) ----------
 
-def mpgemm_quantize_rows(x_type, T, H, X, ldx, order, R, top_k, Q, ldq, scale, stream=0) -> int:
-    return load_ops().mpgemm_quantize_rows(x_type, T, H, X, ldx, order, R, top_k, Q, ldq, scale, stream)
+def mpgemm_quantize_rows(x_type, T, H, X, ldx, order, R, top_k, Q, ldq, scale, workspace=0, workspace_bytes=0,
+                         stream=0) -> int:
+    return load_ops().mpgemm_quantize_rows(x_type, T, H, X, ldx, order, R, top_k, Q, ldq, scale, workspace,
+                                           workspace_bytes, stream)
+
+
+def mpgemm_rows_workspace(type_, T, H, R, top_k) -> int:
+    """Bytes of workspace that lets mpgemm_quantize_rows and mpgemm_gather_rows
+    read each token once, 0 if none does, or a negative code."""
+    return load_ops().mpgemm_rows_workspace(type_, T, H, R, top_k)
 
 
 def mpgemm_i8_gemm(out_type, groups, M, N, K, A, lda, W, ldw, stride_w, C, ldc, scale_a, scale_w, bias=0,
@@ -74,8 +83,10 @@ def mpgemm_route(id_type, pairs, experts, ids, order, position, offsets, workspa
                                    workspace_bytes, stream)
 
 
-def mpgemm_gather_rows(type_, T, H, X, ldx, order, R, top_k, Y, ldy, stream=0) -> int:
-    return load_ops().mpgemm_gather_rows(type_, T, H, X, ldx, order, R, top_k, Y, ldy, stream)
+def mpgemm_gather_rows(type_, T, H, X, ldx, order, R, top_k, Y, ldy, workspace=0, workspace_bytes=0,
+                       stream=0) -> int:
+    return load_ops().mpgemm_gather_rows(type_, T, H, X, ldx, order, R, top_k, Y, ldy, workspace, workspace_bytes,
+                                         stream)
 
 
 def mpgemm_combine_rows(y_type, o_type, T, top_k, H, R, Y, ldy, position, weights, O, ldo, stream=0) -> int:
@@ -186,6 +197,30 @@ def _on(stream, *tensors):
     return device, int(stream)
 
 
+def _new(on, stream, *shapes):
+    """Uninitialised int32 tensors that belong to the launch's stream: memory
+    that another stream freed may still be in use there."""
+    import torch
+    if stream is None:
+        return [torch.empty(shape, dtype=torch.int32, device=on[0]) for shape in shapes]
+    with torch.cuda.stream(torch.cuda.ExternalStream(on[1], device=on[0])):
+        return [torch.empty(shape, dtype=torch.int32, device=on[0]) for shape in shapes]
+
+
+def _workspace(on, stream, given, need):
+    """(pointer, bytes, tensor) of a workspace: the caller's, or one of `need`
+    bytes allocated here."""
+    import torch
+    if given is not None:
+        if not isinstance(given, torch.Tensor) or given.dtype is not torch.int32 or not given.is_contiguous():
+            raise TypeError("workspace must be a contiguous int32 tensor on the GPU")
+        return given.data_ptr(), 4 * given.numel(), given
+    if need <= 0:
+        return 0, 0, None
+    ws, = _new(on, stream, (need + 3) // 4)
+    return ws.data_ptr(), 4 * ws.numel(), ws
+
+
 def _call(fn, on, *args):
     """fn(*args, stream) with the tensors' GPU current; raises on an error."""
     import torch
@@ -199,7 +234,7 @@ def _call(fn, on, *args):
         raise MpgemmError(rc, fn.__name__)
 
 
-def quantize_rows(X, Q, scale, order=None, top_k: int = 1, stream=None):
+def quantize_rows(X, Q, scale, order=None, top_k: int = 1, workspace=None, stream=None):
     """Rows of X to 8-bit codes: scale = max|row| / 127 and the codes nearest
     to 127 * row / max|row| (ties to even).  Returns (Q, scale).
 
@@ -207,7 +242,9 @@ def quantize_rows(X, Q, scale, order=None, top_k: int = 1, stream=None):
     row-major.  scale: float32, R values.  Without ``order`` R == T; with it
     (int32, R values from :func:`route`) row p of Q is row order[p] // top_k
     of X, and rows whose order is -1 keep what they hold.  A row with an
-    infinity or a NaN has a NaN scale and codes 0."""
+    infinity or a NaN has a NaN scale and codes 0.  ``workspace``: a contiguous
+    int32 tensor of mpgemm_rows_workspace bytes, allocated when None and of
+    use."""
     import torch
     xt = _type(X, "X")
     ldx = _rows(X, "X", X.dtype)
@@ -218,8 +255,10 @@ def quantize_rows(X, Q, scale, order=None, top_k: int = 1, stream=None):
         raise ValueError(f"shape mismatch: X {tuple(X.shape)}, Q {tuple(Q.shape)}")
     sp = _flat(scale, "scale", torch.float32, (R,))
     op = 0 if order is None else _flat(order, "order", torch.int32, (R,))
-    _call(load_ops().mpgemm_quantize_rows, _on(stream, X, Q, scale, order), xt, T, H, X.data_ptr(), ldx, op, R,
-          int(top_k), Q.data_ptr(), ldq, sp)
+    lib, on = load_ops(), _on(stream, X, Q, scale, order, workspace)
+    wp, wb, _ws = (0, 0, None) if order is None else _workspace(
+        on, stream, workspace, lib.mpgemm_rows_workspace(xt, T, H, R, int(top_k)))
+    _call(lib.mpgemm_quantize_rows, on, xt, T, H, X.data_ptr(), ldx, op, R, int(top_k), Q.data_ptr(), ldq, sp, wp, wb)
     return Q, scale
 
 
@@ -290,47 +329,36 @@ def route(experts, num_experts: int, out=None, workspace=None, stream=None):
     given = () if out is None else tuple(out)
     if out is not None and len(given) != 3:
         raise ValueError("out must be (order, position, offsets)")
-    if workspace is not None and (not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.int32
-                                  or not workspace.is_contiguous() or not workspace.is_cuda):
-        raise TypeError("workspace must be a contiguous int32 tensor on the GPU")
     on = _on(stream, experts, *given, workspace)
-
-    def allocate():
-        new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=on[0])  # noqa: E731
-        return (given or (new(pairs), new(*experts.shape), new(E + 1)),
-                new(need // 4) if workspace is None and need else workspace)
-
-    if stream is None:
-        given, workspace = allocate()
-    else:
-        # memory from the launch's own stream: what the current stream freed
-        # may still be in use there
-        with torch.cuda.stream(torch.cuda.ExternalStream(on[1], device=on[0])):
-            given, workspace = allocate()
+    wp, wb, _ws = _workspace(on, stream, workspace, need)
+    if not given:
+        given = _new(on, stream, pairs, experts.shape, E + 1)
     order, position, offsets = given
     op = _flat(order, "order", torch.int32, (pairs,))
     pp = _flat(position, "position", torch.int32, experts.shape)
     fp = _flat(offsets, "offsets", torch.int32, (E + 1,))
     _call(load_ops().mpgemm_route, on, MPGEMM_ID_I64 if experts.dtype == torch.int64 else MPGEMM_ID_I32, pairs, E,
-          experts.data_ptr(), op, pp, fp, 0 if workspace is None else workspace.data_ptr(),
-          0 if workspace is None else 4 * workspace.numel())
+          experts.data_ptr(), op, pp, fp, wp, wb)
     return order, position, offsets
 
 
-def gather_rows(X, order, Y, top_k: int = 1, stream=None):
+def gather_rows(X, order, Y, top_k: int = 1, workspace=None, stream=None):
     """Y[p] = X[order[p] // top_k]: tokens' rows into expert order.  Returns Y.
 
     X (T x H) and Y (R x H): float16, bfloat16 or float32, the same, row-major.
     order: int32, R values from :func:`route`; rows whose order is -1 keep
-    what they hold.  The gradient by X is ``combine_rows(dY, position, dX)``."""
+    what they hold.  ``workspace``: a contiguous int32 tensor of
+    mpgemm_rows_workspace bytes, allocated when None and of use.  The gradient by X is ``combine_rows(dY, position, dX)``."""
     import torch
     ty = _type(X, "X")
     ldx, ldy = _rows(X, "X", X.dtype), _rows(Y, "Y", X.dtype)
     if X.shape[1] != Y.shape[1]:
         raise ValueError(f"shape mismatch: X {tuple(X.shape)}, Y {tuple(Y.shape)}")
     op = _flat(order, "order", torch.int32, (Y.shape[0],))
-    _call(load_ops().mpgemm_gather_rows, _on(stream, Y, X, order), ty, X.shape[0], X.shape[1], X.data_ptr(), ldx,
-          op, Y.shape[0], int(top_k), Y.data_ptr(), ldy)
+    lib, on = load_ops(), _on(stream, Y, X, order, workspace)
+    T, H, R = X.shape[0], X.shape[1], Y.shape[0]
+    wp, wb, _ws = _workspace(on, stream, workspace, lib.mpgemm_rows_workspace(ty, T, H, R, int(top_k)))
+    _call(lib.mpgemm_gather_rows, on, ty, T, H, X.data_ptr(), ldx, op, R, int(top_k), Y.data_ptr(), ldy, wp, wb)
     return Y
 
 

@@ -301,12 +301,39 @@ int select_wgrad(const GroupedEntry *table, int64_t groups, int64_t M, int64_t N
 // ---------------------------------------------------------------------------
 // Launches of the row kernels by type
 // ---------------------------------------------------------------------------
+// Rows in expert order are made token by token, through the inverse of the
+// order in a workspace, where the rows are many: PLACEHOLDER
+constexpr int64_t kByTokensBytes = (int64_t)64 << 20;
+
+int64_t inverse_bytes(int64_t T, int64_t R, int64_t top_k, int64_t row_bytes)
+{
+    const int64_t pairs = mul_sat(T, top_k);
+    return top_k >= 2 && pairs <= 2 * R && pairs <= kMax32 && mul_sat(R, row_bytes) >= kByTokensBytes ? 4 * pairs : 0;
+}
+
+void launch_fill(int32_t *v, int64_t count, hipStream_t s)
+{
+    const int64_t blocks = cdiv(count, 1024);
+    hipLaunchKernelGGL(mpg::fill_absent, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, s, v, count);
+}
+
+// `inverse`: the workspace for the way by tokens, or nullptr.
 template <int XT>
-void launch_quantize(const mpg::QuantArgs &a, hipStream_t s)
+void launch_quantize(mpg::QuantArgs a, int32_t *inverse, hipStream_t s)
 {
     // One wave per row where there are rows for every wave slot and a wave
     // holds a row in 8 vectors per lane; else one workgroup per row.
     constexpr int64_t kWaveRow = 64 * 8 * (XT == mpg::kTF32 ? 4 : 8);
+    if (inverse) {
+        launch_fill(inverse, (int64_t)a.T * a.top_k, s);
+        hipLaunchKernelGGL((mpg::quantize_invert<XT>), dim3((unsigned)cdiv(a.R, 256)), dim3(256), 0, s, a, inverse);
+        a.inverse = inverse;
+        if (a.H <= kWaveRow)
+            hipLaunchKernelGGL((mpg::quantize_rows<XT, 64, 8, true>), dim3((unsigned)cdiv(a.T, 4)), dim3(256), 0, s, a);
+        else
+            hipLaunchKernelGGL((mpg::quantize_rows<XT, 256, 4, true>), dim3((unsigned)a.T), dim3(256), 0, s, a);
+        return;
+    }
     if (a.R >= 8 * kNumCu && a.H <= kWaveRow)
         hipLaunchKernelGGL((mpg::quantize_rows<XT, 64, 8>), dim3((unsigned)cdiv(a.R, 4)), dim3(256), 0, s, a);
     else
@@ -383,7 +410,8 @@ extern "C" {
 
 int mpgemm_quantize_rows(int x_type, int64_t T, int64_t H, const void *X, int64_t ldx,
                          const int32_t *order, int64_t R, int64_t top_k,
-                         int8_t *Q, int64_t ldq, float *scale, void *stream)
+                         int8_t *Q, int64_t ldq, float *scale,
+                         void *workspace, int64_t workspace_bytes, void *stream)
 {
     if (!is_type(x_type))
         return MPGEMM_ETYPE;
@@ -397,16 +425,18 @@ int mpgemm_quantize_rows(int x_type, int64_t T, int64_t H, const void *X, int64_
         return MPGEMM_OK;
     if (scale == nullptr || (H > 0 && (Q == nullptr || (T > 0 && X == nullptr))))
         return MPGEMM_ENULL;
-    if (!aligned(X, size_of(x_type)) || !aligned(order, 4) || !aligned(scale, 4))
+    if (!aligned(X, size_of(x_type)) || !aligned(order, 4) || !aligned(scale, 4) || !aligned(workspace, 4))
         return MPGEMM_EALIGN;
-    const mpg::QuantArgs a{X, Q, scale, order, ldx, ldq, (int32_t)T, (int32_t)H, (int32_t)R, (int32_t)top_k};
+    const mpg::QuantArgs a{X, Q, scale, order, nullptr, ldx, ldq, (int32_t)T, (int32_t)H, (int32_t)R, (int32_t)top_k};
+    const int64_t need = order ? inverse_bytes(T, R, top_k, H * size_of(x_type)) : 0;
+    int32_t *const inverse = need > 0 && workspace_bytes >= need ? static_cast<int32_t *>(workspace) : nullptr;
     forget_error();
     if (x_type == MPGEMM_T_F16)
-        launch_quantize<mpg::kTF16>(a, stream_of(stream));
+        launch_quantize<mpg::kTF16>(a, inverse, stream_of(stream));
     else if (x_type == MPGEMM_T_BF16)
-        launch_quantize<mpg::kTBF16>(a, stream_of(stream));
+        launch_quantize<mpg::kTBF16>(a, inverse, stream_of(stream));
     else
-        launch_quantize<mpg::kTF32>(a, stream_of(stream));
+        launch_quantize<mpg::kTF32>(a, inverse, stream_of(stream));
     return launched();
 }
 
@@ -533,9 +563,18 @@ int mpgemm_route(int id_type, int64_t pairs, int64_t experts, const void *ids,
     return launched();
 }
 
+int64_t mpgemm_rows_workspace(int type, int64_t T, int64_t H, int64_t R, int64_t top_k)
+{
+    if (!is_type(type))
+        return MPGEMM_ETYPE;
+    if (T < 0 || H < 0 || R < 0 || top_k < 1 || T > kMax32 || H > kMax32 || R > kMax32 || top_k > kMax32)
+        return MPGEMM_EDIM;
+    return inverse_bytes(T, R, top_k, H * size_of(type));
+}
+
 int mpgemm_gather_rows(int type, int64_t T, int64_t H, const void *X, int64_t ldx,
                        const int32_t *order, int64_t R, int64_t top_k,
-                       void *Y, int64_t ldy, void *stream)
+                       void *Y, int64_t ldy, void *workspace, int64_t workspace_bytes, void *stream)
 {
     if (!is_type(type))
         return MPGEMM_ETYPE;
@@ -548,12 +587,21 @@ int mpgemm_gather_rows(int type, int64_t T, int64_t H, const void *X, int64_t ld
         return MPGEMM_OK;
     if (order == nullptr || Y == nullptr || (T > 0 && X == nullptr))
         return MPGEMM_ENULL;
-    if (!aligned(X, es) || !aligned(Y, es) || !aligned(order, 4))
+    if (!aligned(X, es) || !aligned(Y, es) || !aligned(order, 4) || !aligned(workspace, 4))
         return MPGEMM_EALIGN;
     const mpg::GatherArgs a{static_cast<const uint8_t *>(X), static_cast<uint8_t *>(Y), order, ldx * es, ldy * es,
                             (int32_t)T, (int32_t)R, (int32_t)top_k, (int32_t)(H * es)};
     forget_error();
-    hipLaunchKernelGGL(mpg::gather_rows, dim3((unsigned)cdiv(R, 4)), dim3(256), 0, stream_of(stream), a);
+    const int64_t need = inverse_bytes(T, R, top_k, H * es);
+    if (need > 0 && workspace != nullptr && workspace_bytes >= need) {
+        int32_t *const inverse = static_cast<int32_t *>(workspace);
+        launch_fill(inverse, T * top_k, stream_of(stream));
+        hipLaunchKernelGGL(mpg::gather_invert, dim3((unsigned)cdiv(R, 256)), dim3(256), 0, stream_of(stream), a,
+                           inverse);
+        hipLaunchKernelGGL(mpg::gather_tokens, dim3((unsigned)cdiv(T, 4)), dim3(256), 0, stream_of(stream), a, inverse);
+    } else {
+        hipLaunchKernelGGL(mpg::gather_rows, dim3((unsigned)cdiv(R, 4)), dim3(256), 0, stream_of(stream), a);
+    }
     return launched();
 }
 

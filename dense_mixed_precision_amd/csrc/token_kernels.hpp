@@ -7,6 +7,28 @@
 // decoding sizes by the launch.  Index arrays are read as untrusted data:
 // an index outside the operands counts as absent.
 
+// Whole numbers of `count` values, all -1.
+__global__ void __launch_bounds__(256)
+fill_absent(int32_t *v, int64_t count)
+{
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256)
+        v[i] = -1;
+}
+
+// The inverse of `order` (R values) over `pairs` pairs, filled with -1 before:
+// inverse[order[p]] = p.  A pair that stands in `order` more than once keeps one
+// row here; redo(pair, row) sees to each of the others.
+template <class Redo>
+__device__ __forceinline__ void invert_one(const int32_t *order, int32_t *inverse, int64_t p, int64_t pairs, Redo redo)
+{
+    const int pair = order[p];
+    if (pair < 0 || pair >= pairs)
+        return;
+    const int old = atomicExch(&inverse[pair], (int)p);
+    if (old >= 0)
+        redo(pair, old);
+}
+
 // Rows are read and written in vectors of 16 bytes at any element alignment.
 template <class E>
 struct VecOf {
@@ -56,11 +78,39 @@ __device__ __forceinline__ int code_of(float x, float f, float f127, float m, fl
     }
 }
 
+// A row's scale and codes, from its largest magnitude as bits (at or above
+// 0x7F800000: the row holds an infinity or a NaN).
+struct RowScale {
+    float scale, f, f127, m, inv;
+    bool finite;
+    __device__ __forceinline__ explicit RowScale(uint32_t top)
+    {
+        const float most = __builtin_bit_cast(float, top);
+        finite = top < 0x7F800000u;
+        const bool live = finite && top != 0;
+        scale = finite ? most / 127.0f : __builtin_nanf("");
+        // the power of two that brings the maximum to [1, 2), as far as one
+        // float holds it; a row of zeros has codes 0 by f = 0
+        int ex = (int)(top >> 23) - 127;
+        ex = ex < -100 ? -100 : ex > 126 ? 126 : ex;
+        f = live ? __builtin_bit_cast(float, (uint32_t)(127 - ex) << 23) : 0.0f;
+        f127 = 127.0f * f;
+        m = live ? most * f : 1.0f;
+        inv = 1.0f / m;
+    }
+    template <int XT>
+    __device__ __forceinline__ int code(float x) const
+    {
+        return finite ? code_of<XT>(x, f, f127, m, inv) : 0;
+    }
+};
+
 struct QuantArgs {
     const void *X;
     int8_t *Q;
     float *scale;
     const int32_t *order;    // or nullptr: row i of X
+    const int32_t *inverse;  // TOKENS: T x top_k, the rows of Q of each token's pairs
     int64_t ldx, ldq;
     int32_t T, H, R, top_k;
 };
@@ -69,7 +119,9 @@ struct QuantArgs {
 // of each thread stay in registers between the maximum and the codes; longer
 // rows are read again.  With NT = 64 a row is one wave's: no barrier, and the
 // 32 waves of a compute unit keep as many rows in flight.
-template <int XT, int NT, int CACHE>
+// TOKENS: a row is a token's, read and coded once and written to each row of
+// Q that one of its pairs has (see invert_order).
+template <int XT, int NT, int CACHE, bool TOKENS = false>
 __global__ void __launch_bounds__(256)
 quantize_rows(QuantArgs args)
 {
@@ -80,10 +132,10 @@ quantize_rows(QuantArgs args)
     const int tid = threadIdx.x % NT;
     const int64_t row = (int64_t)blockIdx.x * (256 / NT) +
                         (NT == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : 0);
-    if (row >= args.R)
+    if (row >= (TOKENS ? args.T : args.R))
         return;
     int64_t src = row;
-    if (args.order) {
+    if (!TOKENS && args.order) {
         const int pair = args.order[row];
         src = pair < 0 ? -1 : pair / args.top_k;
         if (src < 0 || src >= args.T)
@@ -132,38 +184,72 @@ quantize_rows(QuantArgs args)
         for (int w = 0; w < NT / 64; ++w)
             top = part[w] > top ? part[w] : top;
     }
-    const float most = __builtin_bit_cast(float, top);
-    const bool finite = top < 0x7F800000u;
-    const bool live = finite && top != 0;
-    // the power of two that brings the maximum to [1, 2), as far as one
-    // float holds it; a row of zeros or with no scale has codes 0 by f = 0
-    int ex = (int)(top >> 23) - 127;
-    ex = ex < -100 ? -100 : ex > 126 ? 126 : ex;
-    const float f = live ? __builtin_bit_cast(float, (uint32_t)(127 - ex) << 23) : 0.0f;
-    const float f127 = 127.0f * f;
-    const float m = live ? most * f : 1.0f;
-    const float inv = 1.0f / m;
-    if (tid == 0)
-        args.scale[row] = finite ? most / 127.0f : __builtin_nanf("");
-    int8_t *const q = args.Q + row * args.ldq;
-    auto code = [&](E e) __attribute__((always_inline)) {
-        return finite ? code_of<XT>((float)e, f, f127, m, inv) : 0;
-    };
-    auto emit = [&](int i, const V &v) __attribute__((always_inline)) {
+    const RowScale r(top);
+    auto code = [&](E e) __attribute__((always_inline)) { return r.code<XT>((float)e); };
+    auto codes = [&](const V &v) __attribute__((always_inline)) {
         Pack<int8_t, VN> o;
 #pragma unroll
         for (int e = 0; e < VN; ++e)
             o.v[e] = (int8_t)code(v.v[e]);
-        *(Pack<int8_t, VN> *)(q + (int64_t)i * VN) = o;
+        return o;
     };
+    // the rows of Q, up to 8 at a time
+    constexpr int SLOTS = TOKENS ? 8 : 1;
+    for (int s0 = 0; s0 < (TOKENS ? args.top_k : 1); s0 += SLOTS) {
+        int to[SLOTS];
 #pragma unroll
-    for (int c = 0; c < CACHE; ++c)
-        if (c * NT + tid < nv)
-            emit(c * NT + tid, keep[c]);
-    for (int i = CACHE * NT + tid; i < nv; i += NT)
-        emit(i, *(const V *)(x + (int64_t)i * VN));
-    for (int i = nv * VN + tid; i < H; i += NT)
-        q[i] = (int8_t)code(x[i]);
+        for (int s = 0; s < SLOTS; ++s) {
+            to[s] = (int)row;
+            if constexpr (TOKENS)
+                to[s] = s0 + s < args.top_k ? args.inverse[row * args.top_k + s0 + s] : -1;
+            if (to[s] >= 0 && tid == 0)
+                args.scale[to[s]] = r.scale;
+        }
+        auto emit = [&](int i, const V &v) __attribute__((always_inline)) {
+            const Pack<int8_t, VN> o = codes(v);
+#pragma unroll
+            for (int s = 0; s < SLOTS; ++s)
+                if (to[s] >= 0)
+                    *(Pack<int8_t, VN> *)(args.Q + to[s] * args.ldq + (int64_t)i * VN) = o;
+        };
+#pragma unroll
+        for (int c = 0; c < CACHE; ++c)
+            if (c * NT + tid < nv)
+                emit(c * NT + tid, keep[c]);
+        for (int i = CACHE * NT + tid; i < nv; i += NT)
+            emit(i, *(const V *)(x + (int64_t)i * VN));
+        for (int i = nv * VN + tid; i < H; i += NT) {
+            const int8_t o = (int8_t)code(x[i]);
+#pragma unroll
+            for (int s = 0; s < SLOTS; ++s)
+                if (to[s] >= 0)
+                    args.Q[to[s] * args.ldq + i] = o;
+        }
+    }
+}
+
+// The inverse of the order for quantize_rows<.., TOKENS>.  A row of Q whose
+// pair stands in `order` again is coded here, by one thread.
+template <int XT>
+__global__ void __launch_bounds__(256)
+quantize_invert(QuantArgs args, int32_t *inverse)
+{
+    typedef typename ElemOf<XT>::type E;
+    const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (p >= args.R)
+        return;
+    invert_one(args.order, inverse, p, (int64_t)args.T * args.top_k, [&](int pair, int old) {
+        const E *const x = (const E *)args.X + (int64_t)(pair / args.top_k) * args.ldx;
+        uint32_t top = 0;
+        for (int i = 0; i < args.H; ++i) {
+            const uint32_t b = __builtin_bit_cast(uint32_t, (float)x[i]) & 0x7FFFFFFFu;
+            top = b > top ? b : top;
+        }
+        const RowScale r(top);
+        args.scale[old] = r.scale;
+        for (int i = 0; i < args.H; ++i)
+            args.Q[old * args.ldq + i] = (int8_t)r.code<XT>((float)x[i]);
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -421,6 +507,13 @@ struct GatherArgs {
 
 typedef Pack<uint8_t, 16> Bytes16;
 
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+
+__device__ __forceinline__ void store_streaming(uint8_t *to, const Bytes16 &v)
+{
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), (u32x4_any *)to);
+}
+
 // Y[p] = X[order[p] / top_k]: one wave per row.
 __global__ void __launch_bounds__(256)
 gather_rows(GatherArgs a)
@@ -450,6 +543,57 @@ gather_rows(GatherArgs a)
     }
     for (int i = nv * 16 + lane; i < a.row_bytes; i += 64)
         y[i] = x[i];
+}
+
+__global__ void __launch_bounds__(256)
+gather_invert(GatherArgs a, int32_t *inverse)
+{
+    const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (p >= a.R)
+        return;
+    invert_one(a.order, inverse, p, (int64_t)a.T * a.top_k, [&](int pair, int old) {
+        const uint8_t *const x = a.X + (int64_t)(pair / a.top_k) * a.ldx;
+        uint8_t *const y = a.Y + (int64_t)old * a.ldy;
+        for (int i = 0; i < a.row_bytes; ++i)
+            y[i] = x[i];
+    });
+}
+
+// Many rows: each token's row is read once and written to the rows of its
+// pairs.  By rows of Y (gather_rows) the reads of a token's row lie far apart
+// and come from beyond the L2 top_k times.  The stores stream past the caches.
+__global__ void __launch_bounds__(256)
+gather_tokens(GatherArgs a, const int32_t *inverse)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (t >= a.T)
+        return;
+    const uint8_t *const x = a.X + t * a.ldx;
+    const int nv = a.row_bytes / 16;
+    for (int i0 = lane; i0 < nv; i0 += 256) {
+        Bytes16 v[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            if (i0 + 64 * c < nv)
+                v[c] = *(const Bytes16 *)(x + (int64_t)(i0 + 64 * c) * 16);
+        for (int s = 0; s < a.top_k; ++s) {
+            const int p = inverse[t * a.top_k + s];
+            if (p < 0)
+                continue;
+            uint8_t *const y = a.Y + p * a.ldy;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (i0 + 64 * c < nv)
+                    store_streaming(y + (int64_t)(i0 + 64 * c) * 16, v[c]);
+        }
+    }
+    for (int i = nv * 16 + lane; i < a.row_bytes; i += 64)
+        for (int s = 0; s < a.top_k; ++s) {
+            const int p = inverse[t * a.top_k + s];
+            if (p >= 0)
+                a.Y[p * a.ldy + i] = x[i];
+        }
 }
 
 struct CombineArgs {

@@ -73,11 +73,12 @@ extern "C" {
  * scale: R floats.  order NULL: row i of Q is row i of X, R == T.  Otherwise
  * row p of Q is row order[p] / top_k of X (R values from mpgemm_route), and
  * rows whose order is outside 0 .. T*top_k-1 keep what they hold.
- * T, H and R below 2^31.
+ * T, H and R below 2^31.  workspace: see mpgemm_rows_workspace.
  */
 int mpgemm_quantize_rows(int x_type, int64_t T, int64_t H, const void *X, int64_t ldx,
                          const int32_t *order, int64_t R, int64_t top_k,
-                         int8_t *Q, int64_t ldq, float *scale, void *stream);
+                         int8_t *Q, int64_t ldq, float *scale,
+                         void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
  * Product of 8-bit codes:
@@ -122,12 +123,22 @@ int mpgemm_route(int id_type, int64_t pairs, int64_t experts, const void *ids,
 /*
  * Rows into expert order:  Y[p] = X[order[p] / top_k],  p < R.
  * X: T x H, Y: R x H, both of `type`; rows whose order is outside 0 ..
- * T*top_k-1 keep what they hold.  The gradient by X is mpgemm_combine_rows
- * of Y's gradient with weights NULL.
+ * T*top_k-1 keep what they hold.  workspace: see mpgemm_rows_workspace.  The
+ * gradient by X is mpgemm_combine_rows of Y's gradient with weights NULL.
  */
 int mpgemm_gather_rows(int type, int64_t T, int64_t H, const void *X, int64_t ldx,
                        const int32_t *order, int64_t R, int64_t top_k,
-                       void *Y, int64_t ldy, void *stream);
+                       void *Y, int64_t ldy, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Workspace with which mpgemm_quantize_rows and mpgemm_gather_rows read each
+ * token's row once when the rows in expert order are many: bytes, 4-byte
+ * aligned, 0 where they do without.  A smaller one, or NULL, is no error: the
+ * rows are then made one by one.  The results are the same.  Calls that share a workspace must
+ * not overlap in time.  `type` is X's; no HIP call is made; a negative code
+ * for arguments that those calls refuse.
+ */
+int64_t mpgemm_rows_workspace(int type, int64_t T, int64_t H, int64_t R, int64_t top_k);
 
 /*
  * Experts' rows back to tokens:

@@ -110,6 +110,32 @@ def test_gather_rows(dtype, T, k, E, H, gap, shift):
     assert torch.equal(Y.flat, want)
 
 
+@pytest.mark.parametrize("dtype,T,k,H,gap,shift", [(torch.bfloat16, 6000, 3, 2051, 1, 1), (torch.float32, 4100, 2, 2304, 0, 0),
+                                                   (torch.float16, 700, 9, 6000, 8, 0)])
+def test_gather_many_rows(dtype, T, k, H, gap, shift):
+    """Rows enough for the way by tokens, equal to the way by rows, also where
+    the order is no permutation: pairs absent, twice, outside."""
+    g = torch.Generator().manual_seed(H)
+    order, _, _ = mp.route(make_ids(T, k, 37, H, drop=0.1).to(device()), 37)
+    R = T * k
+    assert mp.mpgemm_rows_workspace(mp.MPGEMM_T_F32 if dtype == torch.float32 else 0, T, H, R, k) > 0
+    x = torch.randn(T, H, generator=g).to(dtype)
+    X, Y = Buffer(T, H, dtype, x, gap, shift), Buffer(R, H, dtype, gap=gap, shift=shift)
+    want = Y.before.clone()
+    wv = torch.as_strided(want, Y.view.shape, Y.view.stride(), Y.view.storage_offset())
+    for odd in (False, True):
+        if odd:
+            order[5], order[R // 2], order[R // 3] = order[0], order[0], order[1]
+            order[7], order[8], order[9] = R, -2, (1 << 31) - 1
+            Y.flat.copy_(Y.before)
+            want.copy_(Y.before)
+        mp.gather_rows(X.view, order, Y.view, top_k=k)
+        torch.cuda.synchronize()
+        there = (order >= 0) & (order < R)
+        wv[there] = X.view[(order[there] // k).long()]
+        assert torch.equal(Y.flat, want)
+
+
 def test_gather_rows_wrong_indices():
     X = Buffer(4, 32, torch.float32, torch.randn(4, 32))
     Y = Buffer(6, 32, torch.float32)

@@ -104,6 +104,35 @@ def test_quantize_by_order(dtype):
     check_quantize(x[:0], dtype, order=[0, -1, 3])
 
 
+@pytest.mark.parametrize("dtype,T,k,H,gap,shift", [(torch.bfloat16, 6000, 3, 2051, 1, 1), (torch.float32, 4100, 2, 2304, 0, 0),
+                                                   (torch.float16, 700, 9, 6000, 8, 0)])
+def test_quantize_many_rows(dtype, T, k, H, gap, shift):
+    """Rows enough for the way by tokens, also where the order is no
+    permutation: pairs absent, twice, outside."""
+    g = torch.Generator().manual_seed(H)
+    R = T * k
+    order = torch.randperm(R, generator=g, dtype=torch.int64).to(torch.int32)
+    order[5], order[R // 2], order[R // 3] = int(order[0]), int(order[0]), int(order[1])
+    order[7], order[8], order[9], order[10:400] = R, -2, (1 << 31) - 1, -1
+    assert mp.mpgemm_rows_workspace(mp.MPGEMM_T_F32 if dtype == torch.float32 else 0, T, H, R, k) > 0
+    x = torch.randn(T, H, generator=g)
+    x[3, 5], x[4] = float("inf"), 0.0
+    X = Buffer(T, H, dtype, x.to(dtype), gap, shift)
+    Q, S = Buffer(R, H, torch.int8, gap=gap, shift=shift), Buffer(1, R, torch.float32)
+    mp.quantize_rows(X.view, Q.view, S.view.reshape(-1), order=order.to(device()), top_k=k)
+    torch.cuda.synchronize()
+    codes, scale = codes_of(X.view)
+    there = ((order >= 0) & (order < R)).nonzero().reshape(-1)
+    src = (order[there] // k).long()
+    wq = torch.as_strided(Q.before, Q.view.shape, Q.view.stride(), Q.view.storage_offset()).cpu().clone()
+    ws = torch.as_strided(S.before, (R,), (1,), S.view.storage_offset()).cpu().clone()
+    wq[there], ws[there] = codes[src], scale[src]
+    got_s = S.view.reshape(-1).cpu()
+    assert torch.equal(Q.view.cpu(), wq) and Q.outside_untouched() and S.outside_untouched()
+    assert torch.equal(torch.isnan(got_s), torch.isnan(ws))
+    assert torch.equal(torch.nan_to_num(got_s), torch.nan_to_num(ws))
+
+
 def test_quantize_another_stream_and_a_graph():
     x = torch.randn(16, 512, device=device())
     q = torch.zeros(16, 512, dtype=torch.int8, device=device())

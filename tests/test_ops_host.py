@@ -25,7 +25,7 @@ def declared():
 
 def test_library_exports_its_header_and_the_gemm_library_none_of_it():
     names = declared()
-    assert len(names) == 9
+    assert len(names) == 10
     lib = mp.load_ops()
     assert not [n for n in names if not hasattr(lib, n)]
     product = ctypes.CDLL(mp.lib_path())
@@ -55,7 +55,7 @@ QUANT = dict(x_type=0, T=4, H=8, X=P, ldx=8, order=0, R=4, top_k=1, Q=P, ldq=8, 
     (dict(X=0), mp.MPGEMM_ENULL), (dict(Q=0), mp.MPGEMM_ENULL), (dict(scale=0), mp.MPGEMM_ENULL),
     (dict(X=P + 1), mp.MPGEMM_EALIGN), (dict(x_type=2, X=P + 2), mp.MPGEMM_EALIGN),
     (dict(order=P + 2), mp.MPGEMM_EALIGN), (dict(scale=P + 2), mp.MPGEMM_EALIGN),
-    (dict(T=0, R=0, X=0, Q=0, scale=0), 0), (dict(order=P, R=0, Q=0, scale=0), 0),
+    (dict(T=0, R=0, X=0, Q=0, scale=0), 0), (dict(order=P, R=0, Q=0, scale=0), 0), (dict(order=P, workspace=P + 2), mp.MPGEMM_EALIGN),
 ])
 def test_quantize_codes(change, expect):
     assert call(mp.mpgemm_quantize_rows, QUANT, **change) == expect
@@ -121,10 +121,22 @@ GATHER = dict(type_=0, T=4, H=8, X=P, ldx=8, order=P, R=8, top_k=2, Y=P, ldy=8)
     (dict(R=1 << 31), mp.MPGEMM_EDIM), (dict(ldx=7), mp.MPGEMM_ELD), (dict(ldy=7), mp.MPGEMM_ELD),
     (dict(X=0), mp.MPGEMM_ENULL), (dict(Y=0), mp.MPGEMM_ENULL), (dict(order=0), mp.MPGEMM_ENULL),
     (dict(X=P + 1), mp.MPGEMM_EALIGN), (dict(type_=2, Y=P + 2), mp.MPGEMM_EALIGN), (dict(order=P + 2), mp.MPGEMM_EALIGN),
-    (dict(R=0, Y=0), 0), (dict(H=0, X=0, Y=0), 0),
+    (dict(R=0, Y=0), 0), (dict(H=0, X=0, Y=0), 0), (dict(workspace=P + 1), mp.MPGEMM_EALIGN),
 ])
 def test_gather_codes(change, expect):
     assert call(mp.mpgemm_gather_rows, GATHER, **change) == expect
+
+
+@pytest.mark.parametrize("type_,T,H,R,top_k,expect", [
+    (1, 16384, 2048, 131072, 8, 4 * 131072),        # 512 MiB of rows
+    (1, 16384, 2048, 131072, 1, 0),                 # every token once
+    (1, 64, 2048, 256, 4, 0),                       # few rows
+    (1, 16384, 2048, 16384, 8, 0),                  # most pairs have no row
+    (3, 1, 1, 1, 1, mp.MPGEMM_ETYPE), (0, -1, 1, 1, 1, mp.MPGEMM_EDIM), (0, 1, 1, 1, 0, mp.MPGEMM_EDIM),
+    (2, (1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 1, 0),
+])
+def test_rows_workspace(type_, T, H, R, top_k, expect):
+    assert mp.mpgemm_rows_workspace(type_, T, H, R, top_k) == expect
 
 
 COMBINE = dict(y_type=2, o_type=1, T=4, top_k=2, H=8, R=8, Y=P, ldy=8, position=P, weights=P, O=P, ldo=8)
