@@ -21,6 +21,16 @@ MPGEMM_MAX_GROUPS = 1024
 MPGEMM_I8_MAX_K = 131071
 
 _lib = None
+#: torch, imported by the first call that takes tensors (the raw entry points
+#: need none); not by an import in each function, which a small launch notices
+torch = None
+
+
+def _with_torch():
+    global torch, _TYPES
+    import torch as module
+    torch = module
+    _TYPES = {torch.float16: MPGEMM_T_F16, torch.bfloat16: MPGEMM_T_BF16, torch.float32: MPGEMM_T_F32}
 
 
 def load_ops():
@@ -113,15 +123,11 @@ def mpgemm_grouped_wgrad(in_type, groups, R, M, N, A, lda, B, ldb, C, ldc, strid
 
 # ---- torch tensors ----------------------------------------------------------
 
-_TYPES = None
+_TYPES: dict = {}
 
 
 def _type(t, name, types=(MPGEMM_T_F16, MPGEMM_T_BF16, MPGEMM_T_F32)):
     """MPGEMM_T_* of a tensor's dtype, one of `types`."""
-    global _TYPES
-    import torch
-    if _TYPES is None:
-        _TYPES = {torch.float16: MPGEMM_T_F16, torch.bfloat16: MPGEMM_T_BF16, torch.float32: MPGEMM_T_F32}
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     code = _TYPES.get(t.dtype)
@@ -133,7 +139,6 @@ def _type(t, name, types=(MPGEMM_T_F16, MPGEMM_T_BF16, MPGEMM_T_F32)):
 
 def _rows(t, name, dtype):
     """Leading dimension of a row-major 2-D GPU tensor."""
-    import torch
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.dim() == 2:
         # the ordinary case at once; the rest, and what is refused, below
         ld, step = t.stride()
@@ -145,7 +150,6 @@ def _rows(t, name, dtype):
 
 def _flat(t, name, dtype, shape):
     """Pointer of a contiguous GPU tensor of one dtype and shape (None: any)."""
-    import torch
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         raise TypeError(f"{name} must be a {str(dtype).replace('torch.', '')} tensor")
     if (shape is not None and t.shape != shape) or not t.is_contiguous():
@@ -159,7 +163,6 @@ def _flat(t, name, dtype, shape):
 def _matrices(t, name, dtype):
     """(groups, rows, cols, layout, leading dimension, group stride) of a 3-D
     GPU tensor of matrices, each row- or column-major."""
-    import torch
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         raise TypeError(f"{name} must be a {str(dtype).replace('torch.', '')} tensor")
     if t.dim() != 3 or t.shape[0] < 1:
@@ -182,7 +185,6 @@ def _matrices(t, name, dtype):
 def _on(stream, *tensors):
     """(device, stream handle) of a call: every tensor on one GPU, the launch
     on that GPU's current stream or the one given."""
-    import torch
     device = tensors[0].device
     for t in tensors:
         if t is not None and t.device != device:
@@ -200,7 +202,6 @@ def _on(stream, *tensors):
 def _new(on, stream, *shapes):
     """Uninitialised int32 tensors that belong to the launch's stream: memory
     that another stream freed may still be in use there."""
-    import torch
     if stream is None:
         return [torch.empty(shape, dtype=torch.int32, device=on[0]) for shape in shapes]
     with torch.cuda.stream(torch.cuda.ExternalStream(on[1], device=on[0])):
@@ -210,7 +211,6 @@ def _new(on, stream, *shapes):
 def _workspace(on, stream, given, need):
     """(pointer, bytes, tensor) of a workspace: the caller's, or one of `need`
     bytes allocated here."""
-    import torch
     if given is not None:
         if not isinstance(given, torch.Tensor) or given.dtype is not torch.int32 or not given.is_contiguous():
             raise TypeError("workspace must be a contiguous int32 tensor on the GPU")
@@ -223,7 +223,6 @@ def _workspace(on, stream, given, need):
 
 def _call(fn, on, *args):
     """fn(*args, stream) with the tensors' GPU current; raises on an error."""
-    import torch
     device, handle = on
     if torch._C._cuda_getDevice() == device.index:
         rc = fn(*args, handle)
@@ -245,7 +244,8 @@ def quantize_rows(X, Q, scale, order=None, top_k: int = 1, workspace=None, strea
     infinity or a NaN has a NaN scale and codes 0.  ``workspace``: a contiguous
     int32 tensor of mpgemm_rows_workspace bytes, allocated when None and of
     use."""
-    import torch
+    if torch is None:
+        _with_torch()
     xt = _type(X, "X")
     ldx = _rows(X, "X", X.dtype)
     ldq = _rows(Q, "Q", torch.int8)
@@ -273,7 +273,8 @@ def gemm_i8(A, B, C, scale_a, scale_b, bias=None, offsets=None, stream=None):
     is groups x K x N and scale_b and bias are groups x N: rows offsets[g] ..
     offsets[g+1]-1 of A and C use group g's, other rows of C keep what they
     hold."""
-    import torch
+    if torch is None:
+        _with_torch()
     ot = _type(C, "C")
     lda = _rows(A, "A", torch.int8)
     ldc = _rows(C, "C", C.dtype)
@@ -317,7 +318,8 @@ def route(experts, num_experts: int, out=None, workspace=None, stream=None):
     ``out``: the three tensors to write (allocated when None).
     ``workspace``: a contiguous int32 tensor of at least
     mpgemm_route_workspace bytes; allocated when None and needed."""
-    import torch
+    if torch is None:
+        _with_torch()
     if not isinstance(experts, torch.Tensor) or experts.dtype not in (torch.int32, torch.int64):
         raise TypeError("experts must be an int32 or int64 tensor")
     if not experts.is_cuda or not experts.is_contiguous():
@@ -329,16 +331,17 @@ def route(experts, num_experts: int, out=None, workspace=None, stream=None):
     given = () if out is None else tuple(out)
     if out is not None and len(given) != 3:
         raise ValueError("out must be (order, position, offsets)")
-    on = _on(stream, experts, *given, workspace)
+    on = _on(stream, experts, workspace, *given)
     wp, wb, _ws = _workspace(on, stream, workspace, need)
-    if not given:
-        given = _new(on, stream, pairs, experts.shape, E + 1)
-    order, position, offsets = given
-    op = _flat(order, "order", torch.int32, (pairs,))
-    pp = _flat(position, "position", torch.int32, experts.shape)
-    fp = _flat(offsets, "offsets", torch.int32, (E + 1,))
+    if given:
+        order, position, offsets = given
+        _flat(order, "order", torch.int32, (pairs,))
+        _flat(position, "position", torch.int32, experts.shape)
+        _flat(offsets, "offsets", torch.int32, (E + 1,))
+    else:
+        order, position, offsets = _new(on, stream, pairs, experts.shape, E + 1)
     _call(load_ops().mpgemm_route, on, MPGEMM_ID_I64 if experts.dtype == torch.int64 else MPGEMM_ID_I32, pairs, E,
-          experts.data_ptr(), op, pp, fp, wp, wb)
+          experts.data_ptr(), order.data_ptr(), position.data_ptr(), offsets.data_ptr(), wp, wb)
     return order, position, offsets
 
 
@@ -349,7 +352,8 @@ def gather_rows(X, order, Y, top_k: int = 1, workspace=None, stream=None):
     order: int32, R values from :func:`route`; rows whose order is -1 keep
     what they hold.  ``workspace``: a contiguous int32 tensor of
     mpgemm_rows_workspace bytes, allocated when None and of use.  The gradient by X is ``combine_rows(dY, position, dX)``."""
-    import torch
+    if torch is None:
+        _with_torch()
     ty = _type(X, "X")
     ldx, ldy = _rows(X, "X", X.dtype), _rows(Y, "Y", X.dtype)
     if X.shape[1] != Y.shape[1]:
@@ -375,7 +379,8 @@ def combine_rows(Y, position, out, weights=None, stream=None):
     Y (R x H) and out (T x H): float16, bfloat16 or float32 each, row-major.
     position: int32, T x top_k from :func:`route`; pairs at -1 add nothing.
     weights: float32, T x top_k, or None for ones."""
-    import torch
+    if torch is None:
+        _with_torch()
     yt, ot = _type(Y, "Y"), _type(out, "out")
     ldy, ldo = _rows(Y, "Y", Y.dtype), _rows(out, "out", out.dtype)
     T, H = out.shape
@@ -398,7 +403,8 @@ def combine_rows_backward(dout, Y, position, weights, dY, dweights=None, stream=
     row-major.  weights: float32, T x top_k, or None for ones.  dweights:
     float32, T x top_k, 0 for pairs at -1; None: not computed (Y may be None).
     Rows of dY that no pair has keep what they hold."""
-    import torch
+    if torch is None:
+        _with_torch()
     dt, gt = _type(dout, "dout"), _type(dY, "dY")
     ldo, ldg = _rows(dout, "dout", dout.dtype), _rows(dY, "dY", dY.dtype)
     T, H = dout.shape
@@ -428,7 +434,8 @@ def gemm_grouped(A, B, C, offsets, alpha: float = 1.0, beta: float = 0.0, stream
     both float16 or both bfloat16.  C (R x N): float32, row-major; rows of no
     group keep what they hold.  offsets: int32, groups + 1 values.  The
     gradient by A is ``gemm_grouped(dC, B.mT, dA, offsets)``."""
-    import torch
+    if torch is None:
+        _with_torch()
     it = _type(A, "A", (MPGEMM_T_F16, MPGEMM_T_BF16))
     lda, ldc = _rows(A, "A", A.dtype), _rows(C, "C", torch.float32)
     G, K2, N, layout, ldb, stride = _matrices(B, "B", A.dtype)
@@ -448,7 +455,8 @@ def gemm_grouped_wgrad(A, B, C, offsets, alpha: float = 1.0, beta: float = 0.0, 
     A (M x R, column-major: the transpose view of R x M rows) and B (R x N,
     row-major): both float16 or both bfloat16.  C (groups x M x N): float32,
     each row-major; a group without rows has beta * C[g]."""
-    import torch
+    if torch is None:
+        _with_torch()
     it = _type(A, "A", (MPGEMM_T_F16, MPGEMM_T_BF16))
     if A.dim() != 2:
         raise ValueError("A must be 2-D")

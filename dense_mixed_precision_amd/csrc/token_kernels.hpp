@@ -505,14 +505,8 @@ struct GatherArgs {
     int32_t row_bytes;
 };
 
-typedef Pack<uint8_t, 16> Bytes16;
-
+// 16 bytes at any address
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
-
-__device__ __forceinline__ void store_streaming(uint8_t *to, const Bytes16 &v)
-{
-    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), (u32x4_any *)to);
-}
 
 // Y[p] = X[order[p] / top_k]: one wave per row.
 __global__ void __launch_bounds__(256)
@@ -531,15 +525,15 @@ gather_rows(GatherArgs a)
     const int nv = a.row_bytes / 16;
     // 4 KiB at a time: the loads first, so that they are in flight together
     for (int i0 = lane; i0 < nv; i0 += 256) {
-        Bytes16 v[4];
+        u32x4 v[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
             if (i0 + 64 * c < nv)
-                v[c] = *(const Bytes16 *)(x + (int64_t)(i0 + 64 * c) * 16);
+                v[c] = *(const u32x4_any *)(x + (int64_t)(i0 + 64 * c) * 16);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
             if (i0 + 64 * c < nv)
-                *(Bytes16 *)(y + (int64_t)(i0 + 64 * c) * 16) = v[c];
+                *(u32x4_any *)(y + (int64_t)(i0 + 64 * c) * 16) = v[c];
     }
     for (int i = nv * 16 + lane; i < a.row_bytes; i += 64)
         y[i] = x[i];
@@ -572,11 +566,11 @@ gather_tokens(GatherArgs a, const int32_t *inverse)
     const uint8_t *const x = a.X + t * a.ldx;
     const int nv = a.row_bytes / 16;
     for (int i0 = lane; i0 < nv; i0 += 256) {
-        Bytes16 v[4];
+        u32x4 v[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
             if (i0 + 64 * c < nv)
-                v[c] = *(const Bytes16 *)(x + (int64_t)(i0 + 64 * c) * 16);
+                v[c] = *(const u32x4_any *)(x + (int64_t)(i0 + 64 * c) * 16);
         for (int s = 0; s < a.top_k; ++s) {
             const int p = inverse[t * a.top_k + s];
             if (p < 0)
@@ -585,7 +579,7 @@ gather_tokens(GatherArgs a, const int32_t *inverse)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
                 if (i0 + 64 * c < nv)
-                    store_streaming(y + (int64_t)(i0 + 64 * c) * 16, v[c]);
+                    __builtin_nontemporal_store(v[c], (u32x4_any *)(y + (int64_t)(i0 + 64 * c) * 16));
         }
     }
     for (int i = nv * 16 + lane; i < a.row_bytes; i += 64)
