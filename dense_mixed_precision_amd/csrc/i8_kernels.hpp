@@ -105,7 +105,12 @@ struct I8Cfg {
     using TA = I8Tile<BM, BKB, NW, false>;
     using TW = I8Tile<BN, BKB, NW, PAIR>;
     static constexpr int STAGE_BYTES = TA::BYTES + TW::BYTES;
-    static constexpr int LDS_BYTES = STAGES * STAGE_BYTES;
+    static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+    // behind the ring: scale_a of the tile's rows, scale_w and bias of its
+    // columns, in units of 64 floats
+    static constexpr int UA = (BM + 63) / 64, UW = (BN + 63) / 64;
+    static constexpr int UNITS = UA + 2 * UW;
+    static constexpr int LDS_BYTES = RING_BYTES + UNITS * 256;
     static constexpr int NCOPY = TA::PW + TW::PW;
     static constexpr int COPY_WINDOW = STAGES == 2 ? (NCOPY < KS * FM ? NCOPY : KS * FM) : KS * FM;
     static_assert(WTM % 16 == 0 && WTN % 16 == 0, "wave tiles are multiples of the instruction's");
@@ -157,6 +162,15 @@ __device__ __forceinline__ void wait_tiles(int newer)
         else
             wait_tiles<Cfg, MOST - 1>(newer);
     }
+}
+
+// One wave instruction: lane l copies 4 bytes from rsrc at voff into LDS at
+// byte address lds_addr + 4*l (see dma16).
+__device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t lds_addr, uint32_t voff)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 ::"s"(lds_addr), "v"(voff), "s"(rsrc)
+                 : "memory", "m0");
 }
 
 template <class Cfg, int OUT>
@@ -308,6 +322,25 @@ i8_tile(I8Args args)
                 copy_one(c);
     };
 
+    // The scales and the bias go to LDS ahead of the ring, so that the epilogue
+    // does not start with a trip to memory.
+#pragma unroll
+    for (int u0 = 0; u0 < Cfg::UNITS; u0 += Cfg::NW) {
+        const int u = u0 + wave;
+        if (u < Cfg::UNITS) {
+            const bool is_a = u < Cfg::UA, is_w = u < Cfg::UA + Cfg::UW;
+            const int at = 64 * (is_a ? u : is_w ? u - Cfg::UA : u - Cfg::UA - Cfg::UW) + lane;
+            const float *const src = is_a ? args.scale_a + row0
+                                          : (is_w ? args.scale_w : args.bias) + (int64_t)gt.group * args.N + n0;
+            if (is_w || args.bias)
+                dma4(make_rsrc4(src), lds_base + Cfg::RING_BYTES + 256 * u,
+                     at < (is_a ? rows_left : cols_left) ? (uint32_t)(4 * at) : kOOB);
+        }
+    }
+    if (num_k == 0) {
+        wait_vmcnt<0>();
+        __syncthreads();
+    }
     if (num_k > 0) {
 #pragma unroll
         for (int t = 0; t < S; ++t) {
@@ -391,12 +424,13 @@ i8_tile(I8Args args)
     constexpr int NP = Cfg::PAIR ? FN / 2 : FN;
     const int lrow = wm * Cfg::WTM + (lane & 15);
     const int lcol = wn * Cfg::WTN + COUNT * (lane >> 4);
-    const float *const sw_p = args.scale_w + (int64_t)gt.group * args.N + n0;
-    const float *const bias_p = args.bias ? args.bias + (int64_t)gt.group * args.N + n0 : nullptr;
+    const __attribute__((address_space(3))) float *const sc =
+        (const __attribute__((address_space(3))) float *)(lds + Cfg::RING_BYTES);
+    const bool has_bias = args.bias != nullptr;
     float sa[FM];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
-        sa[i] = lrow + 16 * i < rows_left ? args.scale_a[row0 + lrow + 16 * i] : 0.0f;
+        sa[i] = sc[lrow + 16 * i];
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
         const int c = lcol + 4 * COUNT * p;
@@ -406,8 +440,8 @@ i8_tile(I8Args args)
         float sw[COUNT], bv[COUNT];
 #pragma unroll
         for (int e = 0; e < COUNT; ++e) {
-            sw[e] = e < left ? sw_p[c + e] : 0.0f;
-            bv[e] = bias_p && e < left ? bias_p[c + e] : 0.0f;
+            sw[e] = sc[64 * Cfg::UA + c + e];
+            bv[e] = has_bias ? sc[64 * (Cfg::UA + Cfg::UW) + c + e] : 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
@@ -417,7 +451,7 @@ i8_tile(I8Args args)
 #pragma unroll
             for (int e = 0; e < COUNT; ++e) {
                 const int32_t sum = acc[i][Cfg::PAIR ? 2 * p + e / 4 : p][e % 4];
-                v[e] = i8_value(sum, sa[i], sw[e], bv[e], bias_p != nullptr);
+                v[e] = i8_value(sum, sa[i], sw[e], bv[e], has_bias);
             }
             i8_store<OUT, COUNT>((E *)args.C + (int64_t)(row0 + lrow + 16 * i) * args.ldc + n0, c, left, v);
         }

@@ -248,7 +248,7 @@ def test_m0_is_only_written_by_the_copy_sequence(device_asm):
     assert uses
     for i in uses:
         assert re.fullmatch(r"s_mov_b32 m0, s\d+", ins[i]), ins[i]
-        assert ins[i + 1] == "s_nop 0" and ins[i + 2].startswith("buffer_load_dwordx4") and ins[i + 2].endswith(" lds")
+        assert ins[i + 1] == "s_nop 0" and ins[i + 2].startswith("buffer_load_dword") and ins[i + 2].endswith(" lds")
 
 
 def test_no_private_scratch_and_no_packed_fp32(device_asm):
