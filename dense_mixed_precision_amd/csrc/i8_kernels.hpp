@@ -60,6 +60,9 @@ struct ElemOf<kTF32> {
     typedef float type;
 };
 
+// 16 bytes at any address
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+
 // N elements at any element-aligned address (the vector memory of gfx9
 // devices runs in unaligned mode under ROCm).
 template <class E, int N>
@@ -431,6 +434,81 @@ i8_tile(I8Args args)
 #pragma unroll
     for (int i = 0; i < FM; ++i)
         sa[i] = sc[lrow + 16 * i];
+    // the values of this lane's COUNT channels of pair p, for operand i
+    auto values = [&](int p, int i, const float (&sw)[COUNT], const float (&bv)[COUNT], float (&v)[COUNT])
+        __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < COUNT; ++e) {
+            const int32_t sum = acc[i][Cfg::PAIR ? 2 * p + e / 4 : p][e % 4];
+            v[e] = i8_value(sum, sa[i], sw[e], bv[e], has_bias);
+        }
+    };
+    auto scales = [&](int p, float (&sw)[COUNT], float (&bv)[COUNT]) __attribute__((always_inline)) {
+        const int c = lcol + 4 * COUNT * p;
+#pragma unroll
+        for (int e = 0; e < COUNT; ++e) {
+            sw[e] = sc[64 * Cfg::UA + c + e];
+            bv[e] = has_bias ? sc[64 * (Cfg::UA + Cfg::UW) + c + e] : 0.0f;
+        }
+    };
+    E *const out = (E *)args.C + (int64_t)row0 * args.ldc + n0;
+    // Whole lines.  A store of 16 bytes a lane covers 64 bytes of each of 16
+    // rows (16-bit values), or every other 16 bytes of 128 (FP32): partial
+    // lines, which cost the L2 about a third more time.  Lanes r and r + 8 of
+    // a group of 16 swap one of their two 16-byte pieces, so that one store
+    // fills 128 bytes of rows 0..7 and the next those of rows 8..15.
+    constexpr int NQ = OUT == kTF32 ? 1 : 2;  // pairs that make one line
+    if constexpr (Cfg::PAIR && NP % NQ == 0) {
+        if (wn * Cfg::WTN + Cfg::WTN <= cols_left) {
+            const bool low = (lane & 8) == 0;
+            const int srow = wm * Cfg::WTM + (lane & 7);
+#pragma unroll
+            for (int q = 0; q < NP; q += NQ) {
+                float sw[NQ][COUNT], bv[NQ][COUNT];
+#pragma unroll
+                for (int h = 0; h < NQ; ++h)
+                    scales(q + h, sw[h], bv[h]);
+                // column of this lane's piece within the line
+                const int c = OUT == kTF32 ? lcol + 32 * q + (low ? 0 : 4) : lcol + 32 * (low ? q : q + 1);
+#pragma unroll
+                for (int i = 0; i < FM; ++i) {
+                    u32x4 piece[2];
+                    if constexpr (OUT == kTF32) {
+                        float v[COUNT];
+                        values(q, i, sw[0], bv[0], v);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            piece[e / 4][e % 4] = __builtin_bit_cast(uint32_t, v[e]);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float v[COUNT];
+                            values(q + h, i, sw[h], bv[h], v);
+                            Pack<E, 8> o;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                o.v[e] = (E)v[e];
+                            piece[h] = __builtin_bit_cast(u32x4, o);
+                        }
+                    }
+                    u32x4 first, second;  // of rows 0..7 and 8..15
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t mine0 = piece[0][e], mine1 = piece[1][e];
+                        const uint32_t theirs = __builtin_amdgcn_update_dpp(0, low ? mine1 : mine0, 0x128 /* row_ror:8 */,
+                                                                            0xF, 0xF, true);
+                        first[e] = low ? mine0 : theirs;
+                        second[e] = low ? theirs : mine1;
+                    }
+                    if (srow + 16 * i < rows_left)
+                        *(u32x4_any *)(out + (int64_t)(srow + 16 * i) * args.ldc + c) = first;
+                    if (srow + 16 * i + 8 < rows_left)
+                        *(u32x4_any *)(out + (int64_t)(srow + 16 * i + 8) * args.ldc + c) = second;
+                }
+            }
+            return;
+        }
+    }
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
         const int c = lcol + 4 * COUNT * p;
@@ -438,22 +516,14 @@ i8_tile(I8Args args)
         if (left <= 0)
             continue;
         float sw[COUNT], bv[COUNT];
-#pragma unroll
-        for (int e = 0; e < COUNT; ++e) {
-            sw[e] = sc[64 * Cfg::UA + c + e];
-            bv[e] = has_bias ? sc[64 * (Cfg::UA + Cfg::UW) + c + e] : 0.0f;
-        }
+        scales(p, sw, bv);
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
             if (lrow + 16 * i >= rows_left)
                 continue;
             float v[COUNT];
-#pragma unroll
-            for (int e = 0; e < COUNT; ++e) {
-                const int32_t sum = acc[i][Cfg::PAIR ? 2 * p + e / 4 : p][e % 4];
-                v[e] = i8_value(sum, sa[i], sw[e], bv[e], has_bias);
-            }
-            i8_store<OUT, COUNT>((E *)args.C + (int64_t)(row0 + lrow + 16 * i) * args.ldc + n0, c, left, v);
+            values(p, i, sw, bv, v);
+            i8_store<OUT, COUNT>(out + (int64_t)(lrow + 16 * i) * args.ldc, c, left, v);
         }
     }
 }

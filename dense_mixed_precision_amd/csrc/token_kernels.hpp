@@ -505,9 +505,6 @@ struct GatherArgs {
     int32_t row_bytes;
 };
 
-// 16 bytes at any address
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
-
 // Y[p] = X[order[p] / top_k]: one wave per row.
 __global__ void __launch_bounds__(256)
 gather_rows(GatherArgs a)
