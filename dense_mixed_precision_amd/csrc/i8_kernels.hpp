@@ -37,6 +37,7 @@ struct I8Args {
     int32_t N, K;
     int32_t tiles_n;
     int32_t group_m;
+    int32_t stream_c;        // rows of C start on 128-byte lines: stores past the caches
     GroupArgs groups;
 };
 
@@ -456,7 +457,10 @@ i8_tile(I8Args args)
     // rows (16-bit values), or every other 16 bytes of 128 (FP32): partial
     // lines, which cost the L2 about a third more time.  Lanes r and r + 8 of
     // a group of 16 swap one of their two 16-byte pieces, so that one store
-    // fills 128 bytes of rows 0..7 and the next those of rows 8..15.
+    // fills 128 bytes of rows 0..7 and the next those of rows 8..15.  Where
+    // they are lines of C, they stream past the caches and leave those to the
+    // operands (8192x8192x2048 to FP32 170 -> 152 us, to BF16 145 -> 133;
+    // 2048^3 to FP32 17.3 -> 15.7).
     constexpr int NQ = OUT == kTF32 ? 1 : 2;  // pairs that make one line
     if constexpr (Cfg::PAIR && NP % NQ == 0) {
         if (wn * Cfg::WTN + Cfg::WTN <= cols_left) {
@@ -500,10 +504,17 @@ i8_tile(I8Args args)
                         first[e] = low ? mine0 : theirs;
                         second[e] = low ? theirs : mine1;
                     }
-                    if (srow + 16 * i < rows_left)
-                        *(u32x4_any *)(out + (int64_t)(srow + 16 * i) * args.ldc + c) = first;
-                    if (srow + 16 * i + 8 < rows_left)
-                        *(u32x4_any *)(out + (int64_t)(srow + 16 * i + 8) * args.ldc + c) = second;
+                    auto store = [&](int row, const u32x4 &x) __attribute__((always_inline)) {
+                        u32x4_any *const to = (u32x4_any *)(out + (int64_t)row * args.ldc + c);
+                        if (row < rows_left) {
+                            if (args.stream_c)
+                                __builtin_nontemporal_store(x, to);
+                            else
+                                *to = x;
+                        }
+                    };
+                    store(srow + 16 * i, first);
+                    store(srow + 16 * i + 8, second);
                 }
             }
             return;

@@ -177,21 +177,27 @@ int select_i8(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t lda, int6
 // ---------------------------------------------------------------------------
 using grouped_launch = void (*)(const GemmArgs &, const GroupArgs &, dim3, hipStream_t);
 
+// `launch` streams C past the caches; `launch_plain`, which the 256-column
+// tiles come with, does not: there lines that a row of C shares with the next
+// cost up to half more time streamed (us; 32768 rows over 32 experts of
+// 2048x2049 326 plain, 376 streamed; 65536 over 8 of 256x1030 112 and 173;
+// whole lines 278 and 287, 80 and 79).  Smaller tiles make no difference.
 struct GroupedEntry {
     int bm, bn, bk;
-    grouped_launch launch;
+    grouped_launch launch, launch_plain;
 };
 
-template <class Cfg>
+template <class Cfg, bool STREAM>
 void launch_grouped(const GemmArgs &a, const GroupArgs &g, dim3 grid, hipStream_t s)
 {
-    hipLaunchKernelGGL((mpg::gemm_grouped_pipe<Cfg>), grid, dim3(Cfg::NT), 0, s, a, g);
+    hipLaunchKernelGGL((mpg::gemm_grouped_pipe<Cfg, STREAM>), grid, dim3(Cfg::NT), 0, s, a, g);
 }
 
 template <class Cfg>
 constexpr GroupedEntry grouped_entry()
 {
-    return GroupedEntry{Cfg::BM, Cfg::BN, Cfg::BK, &launch_grouped<Cfg>};
+    return GroupedEntry{Cfg::BM, Cfg::BN, Cfg::BK, &launch_grouped<Cfg, true>,
+                        &launch_grouped<Cfg, Cfg::BN != 256>};
 }
 
 // The tiles of one form of the product.  Where the groups split the rows
@@ -232,6 +238,9 @@ const GroupedEntry *grouped_family(int la, int lb, int in)
         return in == kInBF16 ? rows_table<kColMajor, kInBF16>() : rows_table<kColMajor, kInF16>();
     return in == kInBF16 ? rows_table<kRowMajor, kInBF16>() : rows_table<kRowMajor, kInF16>();
 }
+
+// Do the rows of an FP32 C start on 128-byte lines?
+bool whole_lines(const float *C, int64_t ldc) { return aligned(C, 128) && ldc % 32 == 0; }
 
 bool grouped_fits(const GroupedEntry &e, int la, int lb, int64_t lda, int64_t ldb, int64_t ldc)
 {
@@ -510,6 +519,7 @@ int mpgemm_i8_gemm(int out_type, int64_t groups, int64_t M, int64_t N, int64_t K
     a.K = (int32_t)K;
     a.tiles_n = (int32_t)tiles_n;
     a.group_m = 8;
+    a.stream_c = aligned(C, 128) && ldc * size_of(out_type) % 128 == 0;
     a.groups = group_args;
     forget_error();
     e.launch[out_type](a, dim3((unsigned)grid), stream_of(stream));
@@ -744,7 +754,7 @@ int mpgemm_grouped(int in_type, int layout_b, int64_t groups, int64_t R, int64_t
     a.group_m = 8;
     a.splits = 1;
     forget_error();
-    e.launch(a, group_args, dim3((unsigned)grid), stream_of(stream));
+    (whole_lines(C, ldc) ? e.launch : e.launch_plain)(a, group_args, dim3((unsigned)grid), stream_of(stream));
     return launched();
 }
 
@@ -794,7 +804,9 @@ int mpgemm_grouped_wgrad(int in_type, int64_t groups, int64_t R, int64_t M, int6
     a.group_m = 8;
     a.splits = 1;
     forget_error();
-    e.launch(a, GroupArgs{offsets, (int32_t)groups, (int32_t)R, stride_c}, dim3((unsigned)grid), stream_of(stream));
+    const bool lines = whole_lines(C, ldc) && stride_c % 32 == 0;
+    (lines ? e.launch : e.launch_plain)(a, GroupArgs{offsets, (int32_t)groups, (int32_t)R, stride_c},
+                                        dim3((unsigned)grid), stream_of(stream));
     return launched();
 }
 
