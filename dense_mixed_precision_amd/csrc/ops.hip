@@ -99,12 +99,13 @@ constexpr I8Entry i8_entry()
 
 const I8Entry kI8Table[] = {
     i8_entry<I8Cfg<256, 256, 128, 2, 4, 2>>(),
+    i8_entry<I8Cfg<128, 256, 128, 2, 4, 3>>(),
     i8_entry<I8Cfg<128, 128, 128, 2, 4, 3>>(),
     i8_entry<I8Cfg<64, 128, 128, 2, 4, 3>>(),
     i8_entry<I8Cfg<64, 64, 256, 2, 4, 3>>(),
     i8_entry<I8Cfg<16, 64, 256, 1, 4, 4>>(),
 };
-enum : int { kI8Big = 0, kI8Mid = 1, kI8Half = 2, kI8Small = 3, kI8Few = 4 };
+enum : int { kI8Big = 0, kI8Wide = 1, kI8Mid = 2, kI8Half = 3, kI8Small = 4, kI8Few = 5 };
 
 bool i8_fits(const I8Entry &e, int64_t lda, int64_t ldw, int64_t K)
 {
@@ -133,11 +134,25 @@ const narrow_launch kNarrowI8Launch[3] = {&launch_narrow<mpg::kNarrowI8, mpg::kT
                                           &launch_narrow<mpg::kNarrowI8, mpg::kTBF16>,
                                           &launch_narrow<mpg::kNarrowI8, mpg::kTF32>};
 
-// Tiles that `rows` rows in `groups` groups of about the same size make.
+// Tiles that `rows` rows in `groups` groups are likely to make: half a tile
+// more per group than the rows alone, one for each group at least.
 int64_t likely_tiles(int64_t rows, int64_t groups, int64_t bm, int64_t tiles_n)
 {
-    return mul_sat(mul_sat(cdiv(cdiv(rows, groups), bm), groups), tiles_n);
+    const int64_t least = rows < groups ? rows : groups;
+    const int64_t likely = groups <= 1 ? cdiv(rows, bm) : cdiv(rows, bm) + groups / 2;
+    return mul_sat(likely > least ? likely : least, tiles_n);
 }
+
+// 256x256 tiles where they take at most a third of the 128x128 tiles' rounds
+// over the compute units (us; 16-bit, 32768 rows over 32 experts of 2048x2048:
+// 271, 128x256 329, 128x128 443, gradient by the weights 332, 396, 498; 8-bit
+// 4096^3 58, 73, 89).
+bool big_tiles_win(int64_t t256, int64_t t128) { return 3 * cdiv(t256, kNumCu) <= cdiv(t128, kNumCu); }
+
+// A round of 128x256 tiles takes 1.5 to 1.8 times as long as one of 128x128
+// (16-bit, 8192 rows over 32 experts 91, 128x128 124; 8-bit 2048x4096x4096
+// 36, 128x128 46, 256x256 48).
+bool wide_tiles_win(int64_t twide, int64_t t128) { return 8 * cdiv(twide, kNumCu) <= 5 * cdiv(t128, kNumCu); }
 
 // Table entry of an 8-bit product, or -1 for the narrow kernel.  By sweeps of
 // every entry (us, graph-replayed, K and N first where one number stands):
@@ -145,8 +160,7 @@ int64_t likely_tiles(int64_t rows, int64_t groups, int64_t bm, int64_t tiles_n)
 //     16x4096x4096 6.4 against 9.3), but 64x128 tiles for 5 rows and more
 //     a group over at least 512 of them (512 rows over 64 experts of
 //     2048x2048 50.2 against 60.9; 64 rows 48.0 narrow against 59);
-//   256x256 where its rounds of workgroups over the compute units take at
-//     most a third of the 128x128 tiles' (4096^3 64.2 against 88.9);
+//   256x256 and 128x256 by their rounds (above);
 //   128x128 from 192 tiles (512x8192x8192 49.0, 64x128 54.0; 2048^3 15.2
 //     against 16.0; below, 256x8192x8192, 128 tiles, 40.0 against 32.9);
 //   64x128 from 129 tiles (1024x2048x2048 10.5, 64x64 14.5; 128x8192x8192,
@@ -161,8 +175,10 @@ int select_i8(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t lda, int6
     auto fits = [&](int id) { return i8_fits(kI8Table[id], lda, ldw, K); };
     if (per <= 16)
         return per > 4 && groups > 1 && tiles(64, 128) >= 512 && fits(kI8Half) ? kI8Half : -1;
-    if (per > 128 && N > 128 && 3 * cdiv(tiles(256, 256), kNumCu) <= cdiv(tiles(128, 128), kNumCu) && fits(kI8Big))
+    if (per > 128 && N > 128 && big_tiles_win(tiles(256, 256), tiles(128, 128)) && fits(kI8Big))
         return kI8Big;
+    if (per > 64 && N > 128 && wide_tiles_win(tiles(128, 256), tiles(128, 128)) && fits(kI8Wide))
+        return kI8Wide;
     if (per > 64 && tiles(128, 128) >= 192 && fits(kI8Mid))
         return kI8Mid;
     if (tiles(64, 128) > 128 && fits(kI8Half))
@@ -248,15 +264,6 @@ bool grouped_fits(const GroupedEntry &e, int la, int lb, int64_t lda, int64_t ld
            (lb == kRowMajor ? span_fits(e.bk, ldb, e.bn, 2) : span_fits(e.bn, ldb, e.bk, 2)) &&
            span_fits(e.bm, ldc, e.bn, 4);
 }
-
-// 256x256 tiles where they take at most a third of the 128x128 tiles' rounds
-// over the compute units (32768 rows over 32 experts of 2048x2048: 271 us,
-// 128x256 329, 128x128 443; gradient by the weights 332, 396, 498).
-bool big_tiles_win(int64_t t256, int64_t t128) { return 3 * cdiv(t256, kNumCu) <= cdiv(t128, kNumCu); }
-
-// 128x256 tiles take 1.8 times as long as 128x128 (gradient by the weights,
-// 32768 rows over 8 experts of 1024x1024: one round 74 us, two of 128x128 83).
-bool wide_tiles_win(int64_t twide, int64_t t128) { return 9 * cdiv(twide, kNumCu) <= 5 * cdiv(t128, kNumCu); }
 
 // Table entry of a grouped product whose rows the groups split, or -1 for the
 // narrow kernel (column-major B).  By sweeps of every entry (us,
