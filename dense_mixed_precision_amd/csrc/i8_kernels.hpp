@@ -249,35 +249,64 @@ i8_tile(I8Args args)
             off = kOOB;
         dma16(is_a ? rsA : rsW, copy_region + (is_a ? 0 : TA::BYTES) + j * 1024, off, copy_soff);
     };
-    // The vectors of the last tile that straddle K: byte loads, zeros at and
-    // past K, into the slots where the copies wrote zeros.
+    // The vectors of the last tile that straddle K, into the slots where the
+    // copies wrote zeros: the row's last 16 bytes, shifted down so that zeros
+    // stand behind K (a row of less than 16 bytes byte by byte).  Two rows'
+    // loads at a time: the accumulators leave no registers for more.
     auto fill = [&](int buf) __attribute__((always_inline)) {
         int ln = lane;
         asm volatile("" : "+v"(ln));
         const int c_at = klast / 16, nv = klast % 16;
-        const int ko = (num_k - 1) * BKB + 16 * c_at;
-#pragma unroll
-        for (int q = 0; q < NCOPY; ++q) {
+        auto place = [&](int q, int &r, bool &here) __attribute__((always_inline)) {
             const bool is_a = q < TA::PW;
             const int j = (is_a ? q : q - TA::PW) * Cfg::NW + wave;
-            const int r = TA::RPI * j + ln / TA::CH;
+            r = TA::RPI * j + ln / TA::CH;
             const int c = (ln % TA::CH) ^ (is_a ? TA::swz(r) : TW::swz(r));
-            if (c == c_at && r < (is_a ? rows_left : cols_left)) {
-                const int8_t *p = is_a ? Ap + (int64_t)r * args.lda + ko : Wp + (int64_t)r * args.ldw + ko;
-                uint32_t w[4] = {0, 0, 0, 0};
-                for (int e = 0; e < nv; ++e) {
-                    const uint32_t b = (uint32_t)(uint8_t)p[e] << (8 * (e & 3));
-                    if (e < 4)
-                        w[0] |= b;
-                    else if (e < 8)
-                        w[1] |= b;
-                    else if (e < 12)
-                        w[2] |= b;
-                    else
-                        w[3] |= b;
+            here = c == c_at && r < (is_a ? rows_left : cols_left);
+            return j;
+        };
+#pragma unroll
+        for (int q0 = 0; q0 < NCOPY; q0 += 2) {
+            u32x4 v[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int q = q0 + h;
+                if (q >= NCOPY)
+                    break;
+                const bool is_a = q < TA::PW;
+                int r;
+                bool here;
+                place(q, r, here);
+                v[h] = u32x4{0, 0, 0, 0};
+                if (here) {
+                    const int8_t *const row = is_a ? Ap + (int64_t)r * args.lda : Wp + (int64_t)r * args.ldw;
+                    if (K >= 16) {
+                        v[h] = *(const u32x4_any *)(row + K - 16);
+                    } else {
+                        for (int e = 0; e < nv; ++e) {
+                            const uint32_t b = (uint32_t)(uint8_t)row[e] << (8 * (e & 3));
+#pragma unroll
+                            for (int w = 0; w < 4; ++w)
+                                v[h][w] |= e / 4 == w ? b : 0u;
+                        }
+                    }
                 }
-                *(lds_u32x4 *)(lds + buf * Cfg::STAGE_BYTES + (is_a ? 0 : TA::BYTES) + j * 1024 + ln * 16) =
-                    u32x4{w[0], w[1], w[2], w[3]};
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int q = q0 + h;
+                if (q >= NCOPY)
+                    break;
+                const bool is_a = q < TA::PW;
+                int r;
+                bool here;
+                const int j = place(q, r, here);
+                if (here) {
+                    u32x4 x = v[h];
+                    if (K >= 16)
+                        x = __builtin_bit_cast(u32x4, __builtin_bit_cast(unsigned __int128, x) >> (8 * (16 - nv)));
+                    *(lds_u32x4 *)(lds + buf * Cfg::STAGE_BYTES + (is_a ? 0 : TA::BYTES) + j * 1024 + ln * 16) = x;
+                }
             }
         }
     };

@@ -471,6 +471,12 @@ struct TileSrc {
     int64_t ld;
     int64_t row_left;
     int64_t chunk_left;
+#ifdef MPGEMM_GROUPED
+    // Vectors that straddle the end of a row are copied whole.  What they
+    // bring in behind the row (the next row's values) only reaches rows or
+    // columns of C outside the product, which are never stored.
+    bool loose;
+#endif
 };
 
 // Copy number i (0 .. T::PW-1) of this wave for one operand tile: LDS row
@@ -484,7 +490,11 @@ __device__ __forceinline__ void copy_slot(int i, int wave, int lane, i32x4 rs, c
     const int rl = lane / T::CH;
     const int r = T::RPI * j + rl;
     const int c = (lane % T::CH) ^ T::swz(r);
+#ifdef MPGEMM_GROUPED
+    const bool ok = r < src.row_left && (T::K_CONTIG || !src.loose ? 8 * c + 8 : 8 * c + 1) <= src.chunk_left;
+#else
     const bool ok = r < src.row_left && 8 * c + 8 <= src.chunk_left;
+#endif
     const uint32_t voff = (uint32_t)((rl * src.ld + 8 * c) * 2);
     dma16(rs, region + j * 1024, ok ? voff : kOOB, (uint32_t)(T::RPI * j * src.ld * 2));
 }
@@ -693,6 +703,29 @@ gemm_pipe(GemmArgs args_in)
             return t + koff < num_kt ? t + koff : t + koff - num_kt;
     };
 
+#ifdef MPGEMM_GROUPED
+    // An operand stored along M or N, `width` wide, may copy straddling
+    // vectors whole (up to 7 values behind a row) where another stored row
+    // follows: in every K tile but the last, and there if a K tail follows.
+    static_assert(Cfg::STAGGER == 0, "K tiles in order");
+    auto is_loose = [&](int64_t t, int64_t width) __attribute__((always_inline)) {
+        return width >= 8 && (t + 1 < num_kt || ktail > 0);
+    };
+    auto src_a = [&](int64_t t) __attribute__((always_inline)) {
+        const int64_t k0 = t * BK;
+        if constexpr (A_ROW)
+            return TileSrc{args.A + m0 * lda + k0, lda, rows_left, K - k0, false};
+        else
+            return TileSrc{args.A + k0 * lda + m0, lda, K - k0, rows_left, is_loose(t, args.M)};
+    };
+    auto src_b = [&](int64_t t) __attribute__((always_inline)) {
+        const int64_t k0 = t * BK;
+        if constexpr (B_ROW)
+            return TileSrc{args.B + k0 * ldb + n0, ldb, K - k0, cols_left, is_loose(t, args.N)};
+        else
+            return TileSrc{args.B + n0 * ldb + k0, ldb, cols_left, K - k0, false};
+    };
+#else
     // The A and B tiles of K tile t as windows of the stored matrices.
     auto src_a = [&](int64_t t) __attribute__((always_inline)) {
         const int64_t k0 = kmem(t) * BK;
@@ -708,6 +741,7 @@ gemm_pipe(GemmArgs args_in)
         else
             return TileSrc{args.B + n0 * ldb + k0, ldb, cols_left, K - k0};
     };
+#endif
 
     // ---- copies of one K tile into one ring buffer, issued a few at a time
     TileSrc cpa{}, cpb{};
@@ -737,6 +771,17 @@ gemm_pipe(GemmArgs args_in)
     auto fill = [&](int64_t kt, int buf) __attribute__((always_inline)) {
         lds_u8 *const sbase = lds + buf * Cfg::STAGE_BYTES;
         const TileSrc a = src_a(kt), b = src_b(kt);
+#ifdef MPGEMM_GROUPED
+        if (!a.loose && has_partial<TA>(a.chunk_left))
+            fill_tile<TA>(wave, lane, a, sbase);
+        if (!b.loose && has_partial<TB>(b.chunk_left))
+            fill_tile<TB>(wave, lane, b, sbase + Cfg::A_BYTES);
+    };
+    auto needs_fill = [&](int64_t kt) __attribute__((always_inline)) {
+        const TileSrc a = src_a(kt), b = src_b(kt);
+        return (!a.loose && has_partial<TA>(a.chunk_left)) || (!b.loose && has_partial<TB>(b.chunk_left));
+    };
+#else
         if (has_partial<TA>(a.chunk_left))
             fill_tile<TA>(wave, lane, a, sbase);
         if (has_partial<TB>(b.chunk_left))
@@ -745,6 +790,7 @@ gemm_pipe(GemmArgs args_in)
     auto needs_fill = [&](int64_t kt) __attribute__((always_inline)) {
         return has_partial<TA>(src_a(kt).chunk_left) || has_partial<TB>(src_b(kt).chunk_left);
     };
+#endif
 
     // ---- operand reads -----------------------------------------------------
     const OpReader<TA, Cfg::MI> rd_a(wm * Cfg::WTM, lane);

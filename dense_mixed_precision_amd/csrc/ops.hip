@@ -370,26 +370,40 @@ void launch_combine(int o_type, const mpg::CombineArgs &a, dim3 grid, hipStream_
         hipLaunchKernelGGL((mpg::combine_rows<YT, mpg::kTF32>), grid, dim3(256), 0, s, a);
 }
 
+// Rows of up to 256 values: 16 lanes per pair (78743 pairs of 119 values,
+// BF16 and FP32: 15.3 us, with 64 lanes 28.9).
+template <int DT, int YT, int GT>
+void launch_combine_backward(const mpg::CombineBackArgs &a, hipStream_t s)
+{
+    const int64_t pairs = (int64_t)a.T * a.top_k;
+    if (a.H <= 256)
+        hipLaunchKernelGGL((mpg::combine_rows_backward<DT, YT, GT, 16>), dim3((unsigned)cdiv(pairs, 16)), dim3(256), 0,
+                           s, a);
+    else
+        hipLaunchKernelGGL((mpg::combine_rows_backward<DT, YT, GT, 64>), dim3((unsigned)cdiv(pairs, 4)), dim3(256), 0,
+                           s, a);
+}
+
 template <int DT, int YT>
-void launch_combine_backward(int g_type, const mpg::CombineBackArgs &a, dim3 grid, hipStream_t s)
+void launch_combine_backward(int g_type, const mpg::CombineBackArgs &a, hipStream_t s)
 {
     if (g_type == MPGEMM_T_F16)
-        hipLaunchKernelGGL((mpg::combine_rows_backward<DT, YT, mpg::kTF16>), grid, dim3(256), 0, s, a);
+        launch_combine_backward<DT, YT, mpg::kTF16>(a, s);
     else if (g_type == MPGEMM_T_BF16)
-        hipLaunchKernelGGL((mpg::combine_rows_backward<DT, YT, mpg::kTBF16>), grid, dim3(256), 0, s, a);
+        launch_combine_backward<DT, YT, mpg::kTBF16>(a, s);
     else
-        hipLaunchKernelGGL((mpg::combine_rows_backward<DT, YT, mpg::kTF32>), grid, dim3(256), 0, s, a);
+        launch_combine_backward<DT, YT, mpg::kTF32>(a, s);
 }
 
 template <int DT>
-void launch_combine_backward(int y_type, int g_type, const mpg::CombineBackArgs &a, dim3 grid, hipStream_t s)
+void launch_combine_backward(int y_type, int g_type, const mpg::CombineBackArgs &a, hipStream_t s)
 {
     if (y_type == MPGEMM_T_F16)
-        launch_combine_backward<DT, mpg::kTF16>(g_type, a, grid, s);
+        launch_combine_backward<DT, mpg::kTF16>(g_type, a, s);
     else if (y_type == MPGEMM_T_BF16)
-        launch_combine_backward<DT, mpg::kTBF16>(g_type, a, grid, s);
+        launch_combine_backward<DT, mpg::kTBF16>(g_type, a, s);
     else
-        launch_combine_backward<DT, mpg::kTF32>(g_type, a, grid, s);
+        launch_combine_backward<DT, mpg::kTF32>(g_type, a, s);
 }
 
 // Pairs one workgroup sorts alone.
@@ -677,14 +691,13 @@ int mpgemm_combine_rows_backward(int d_type, int y_type, int dy_type,
         return MPGEMM_EALIGN;
     const mpg::CombineBackArgs a{dO, Y, dY, dweights, position, weights, ldo, ldy, lddy,
                                  (int32_t)T, (int32_t)H, (int32_t)R, (int32_t)top_k};
-    const dim3 grid((unsigned)cdiv(T * top_k, 4));
     forget_error();
     if (d_type == MPGEMM_T_F16)
-        launch_combine_backward<mpg::kTF16>(y_type, dy_type, a, grid, stream_of(stream));
+        launch_combine_backward<mpg::kTF16>(y_type, dy_type, a, stream_of(stream));
     else if (d_type == MPGEMM_T_BF16)
-        launch_combine_backward<mpg::kTBF16>(y_type, dy_type, a, grid, stream_of(stream));
+        launch_combine_backward<mpg::kTBF16>(y_type, dy_type, a, stream_of(stream));
     else
-        launch_combine_backward<mpg::kTF32>(y_type, dy_type, a, grid, stream_of(stream));
+        launch_combine_backward<mpg::kTF32>(y_type, dy_type, a, stream_of(stream));
     return launched();
 }
 

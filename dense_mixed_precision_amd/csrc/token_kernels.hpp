@@ -661,9 +661,9 @@ struct CombineBackArgs {
 
 // Of each pair (t, s) with a position p: dY[p] = weights[t][s] * dO[t] and
 // dweights[t][s] = <dO[t], Y[p]>, the products summed in FP32; a pair without
-// one has dweights 0.  One wave per pair; the slots of a token are
-// neighbours, so dO[t] comes from memory once.
-template <int DT, int YT, int GT>
+// one has dweights 0.  LANES lanes per pair (64, or 16 for short rows); the
+// slots of a token are neighbours, so dO[t] comes from memory once.
+template <int DT, int YT, int GT, int LANES>
 __global__ void __launch_bounds__(256)
 combine_rows_backward(CombineBackArgs a)
 {
@@ -671,45 +671,45 @@ combine_rows_backward(CombineBackArgs a)
     typedef typename ElemOf<YT>::type EY;
     typedef typename ElemOf<GT>::type EG;
     constexpr int VN = 8;
-    const int lane = threadIdx.x & 63;
-    const int64_t pair = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x % LANES;
+    const int sub = threadIdx.x / LANES;
+    const int64_t pair = (int64_t)blockIdx.x * (256 / LANES) + (LANES == 64 ? __builtin_amdgcn_readfirstlane(sub) : sub);
     if (pair >= (int64_t)a.T * a.top_k)
         return;
     const int p = a.position[pair];
-    if (p < 0 || p >= a.R) {
-        if (a.dweights && lane == 0)
-            a.dweights[pair] = 0.0f;
-        return;
-    }
-    const float w = a.weights ? a.weights[pair] : 1.0f;
-    const ED *const d = (const ED *)a.dO + (pair / a.top_k) * a.ldo;
-    const EY *const y = (const EY *)a.Y + (int64_t)p * a.ldy;
-    EG *const g = (EG *)a.dY + (int64_t)p * a.lddy;
-    const int nv = a.H / VN;
+    const bool there = p >= 0 && p < a.R;
     float dot = 0.0f;
-    for (int i = lane; i < nv; i += 64) {
-        const Pack<ED, VN> dv = *(const Pack<ED, VN> *)(d + (int64_t)i * VN);
-        Pack<EG, VN> gv;
-        if (a.dweights) {
-            const Pack<EY, VN> yv = *(const Pack<EY, VN> *)(y + (int64_t)i * VN);
+    if (there) {
+        const float w = a.weights ? a.weights[pair] : 1.0f;
+        const ED *const d = (const ED *)a.dO + (pair / a.top_k) * a.ldo;
+        const EY *const y = (const EY *)a.Y + (int64_t)p * a.ldy;
+        EG *const g = (EG *)a.dY + (int64_t)p * a.lddy;
+        const int nv = a.H / VN;
+        for (int i = lane; i < nv; i += LANES) {
+            const Pack<ED, VN> dv = *(const Pack<ED, VN> *)(d + (int64_t)i * VN);
+            Pack<EG, VN> gv;
+            if (a.dweights) {
+                const Pack<EY, VN> yv = *(const Pack<EY, VN> *)(y + (int64_t)i * VN);
+#pragma unroll
+                for (int e = 0; e < VN; ++e)
+                    dot = __builtin_fmaf((float)dv.v[e], (float)yv.v[e], dot);
+            }
 #pragma unroll
             for (int e = 0; e < VN; ++e)
-                dot = __builtin_fmaf((float)dv.v[e], (float)yv.v[e], dot);
+                gv.v[e] = (EG)(w * (float)dv.v[e]);
+            *(Pack<EG, VN> *)(g + (int64_t)i * VN) = gv;
         }
-#pragma unroll
-        for (int e = 0; e < VN; ++e)
-            gv.v[e] = (EG)(w * (float)dv.v[e]);
-        *(Pack<EG, VN> *)(g + (int64_t)i * VN) = gv;
-    }
-    for (int i = nv * VN + lane; i < a.H; i += 64) {
-        const float dv = (float)d[i];
-        if (a.dweights)
-            dot = __builtin_fmaf(dv, (float)y[i], dot);
-        g[i] = (EG)(w * dv);
+        for (int i = nv * VN + lane; i < a.H; i += LANES) {
+            const float dv = (float)d[i];
+            if (a.dweights)
+                dot = __builtin_fmaf(dv, (float)y[i], dot);
+            g[i] = (EG)(w * dv);
+        }
     }
     if (a.dweights) {
+        // (lanes of one pair are alike in `there`, and only they add)
 #pragma unroll
-        for (int s = 32; s > 0; s /= 2)
+        for (int s = LANES / 2; s > 0; s /= 2)
             dot += __shfl_xor(dot, s);
         if (lane == 0)
             a.dweights[pair] = dot;

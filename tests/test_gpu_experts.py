@@ -5,7 +5,8 @@ definitions in 64 bits.
 Bounds (u = 2^-24, h the output type's half step): a weighted sum of k rows is
 k fused steps in FP32, k*u of the sum of magnitudes, and h of the result.  A
 dot product over H values takes at most ceil(H/64) + 16 FP32 additions in a
-chain.  A grouped product is an FP32 running sum of K products: (K + 2)*u of
+chain (64 lanes: 8 per whole 512 values, one more and 6 across lanes; 16 lanes
+up to H = 256: 16, one more where H is no multiple of 8, and 4 across).  A grouped product is an FP32 running sum of K products: (K + 2)*u of
 the sum of magnitudes covers any order and the epilogue's alpha and beta."""
 import pytest
 import torch
@@ -200,7 +201,7 @@ def test_combine_no_slots_no_rows_wrong_positions():
                                       (torch.bfloat16, torch.bfloat16, torch.float32),
                                       (torch.float32, torch.float16, torch.bfloat16)])
 @pytest.mark.parametrize("T,k,E,H,gap,shift", [(1, 1, 1, 1, 0, 0), (6, 2, 3, 7, 1, 1), (17, 8, 64, 256, 0, 0),
-                                               (5, 3, 4, 2051, 2, 1)])
+                                               (9, 5, 4, 119, 0, 0), (7, 3, 4, 264, 0, 0), (5, 3, 4, 2051, 2, 1)])
 def test_combine_rows_backward(dt, yt, gt, T, k, E, H, gap, shift):
     g = torch.Generator().manual_seed(T + H)
     ids = make_ids(T, k, E, T + H, drop=0.25)
@@ -328,6 +329,40 @@ def test_grouped_every_tile_size(dtype, col):
     check_grouped([1, 700, 0, 1299, 490], 2500, 1100, 77, dtype, col)
     check_grouped([1, 4000, 0, 5, 4901], 9000, 1100, 69, dtype, col, beta=0.5)
     check_grouped([1, 9, 0, 16, 17], 50, 300, 1003, dtype, col, alpha=0.5, beta=2.0, gap=1, shift=1)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("K", [8, 24, 64, 100, 136])
+@pytest.mark.parametrize("N", [5, 8, 13, 130, 257])
+def test_grouped_edges_of_stored_rows(dtype, K, N):
+    """Odd widths of operands stored along M and N, tightly packed at the end
+    of their buffers, with K tiles that end at and beside the last row: the
+    values behind a row are NaN where the sentinels are, and none of them may
+    reach C."""
+    dev = device()
+    g = torch.Generator().manual_seed(K * N)
+    a = torch.randn(K, N, generator=g).to(dtype)     # stored rows of the wgrad's A: K tokens x N
+    b = torch.randn(K, 19, generator=g).to(dtype)
+    flat = torch.full((K * N + 64,), float("nan"), dtype=dtype, device=dev)
+    flat[:K * N] = a.reshape(-1).to(dev)
+    A = flat[:K * N].view(K, N)
+    out = torch.empty(2, N, 19, device=dev)
+    sizes = [K - 5, 5]
+    mp.gemm_grouped_wgrad(A.t(), b.to(dev), out, offsets_of(sizes))
+    out2 = torch.empty(2, 19, N, device=dev)
+    mp.gemm_grouped_wgrad(b.to(dev).t(), A, out2, offsets_of(sizes))
+    x = torch.randn(70, K, generator=g).to(dtype)
+    out3 = torch.empty(70, N, device=dev)
+    mp.gemm_grouped(x.to(dev), A.unsqueeze(0), out3, offsets_of([70]))
+    torch.cuda.synchronize()
+    lo = 0
+    for e, n in enumerate(sizes):
+        u, v = a[lo:lo + n].double(), b[lo:lo + n].double()
+        bound = (n + 2) * U32 * (u.abs().t() @ v.abs()) + 1e-40
+        assert_within(out[e], u.t() @ v, bound, "wgrad")
+        assert_within(out2[e], v.t() @ u, bound.t(), "wgrad, operands exchanged")
+        lo += n
+    assert_within(out3, x.double() @ a.double(), (K + 2) * U32 * (x.double().abs() @ a.double().abs()), "rows")
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])

@@ -230,6 +230,14 @@ def test_i8_alignments(dtype, gap, shift):
     check_i8(70, 83, 300, dtype, gap=gap, shift=shift, seed=gap + 8 * shift)
 
 
+@pytest.mark.parametrize("K", [1, 15, 16, 17, 31, 54, 59, 127, 128, 129, 143, 255, 257, 271])
+@pytest.mark.parametrize("M,N", [(3, 20), (40, 50), (100, 520), (600, 2000)])
+def test_i8_ends_of_rows(M, N, K):
+    """Rows whose last vector straddles K, in every kernel, tightly packed."""
+    check_i8(M, N, K, torch.float32, seed=K)
+    check_i8(M, N, K, torch.bfloat16, gap=5, shift=1, bias=False, seed=K)
+
+
 @pytest.mark.parametrize("M,N,K", [(5, 9, 0), (0, 9, 5), (5, 0, 5)])
 def test_i8_empty(M, N, K):
     check_i8(M, N, K, torch.float32)
