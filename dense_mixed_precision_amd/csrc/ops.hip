@@ -101,11 +101,12 @@ const I8Entry kI8Table[] = {
     i8_entry<I8Cfg<256, 256, 128, 2, 4, 2>>(),
     i8_entry<I8Cfg<128, 256, 128, 2, 4, 3>>(),
     i8_entry<I8Cfg<128, 128, 128, 2, 4, 3>>(),
+    i8_entry<I8Cfg<128, 128, 128, 2, 4, 2>>(),  // 66 KiB of LDS: two workgroups per compute unit
     i8_entry<I8Cfg<64, 128, 128, 2, 4, 3>>(),
     i8_entry<I8Cfg<64, 64, 256, 2, 4, 3>>(),
     i8_entry<I8Cfg<16, 64, 256, 1, 4, 4>>(),
 };
-enum : int { kI8Big = 0, kI8Wide = 1, kI8Mid = 2, kI8Half = 3, kI8Small = 4, kI8Few = 5 };
+enum : int { kI8Big = 0, kI8Wide = 1, kI8Mid = 2, kI8Two = 3, kI8Half = 4, kI8Small = 5, kI8Few = 6 };
 
 bool i8_fits(const I8Entry &e, int64_t lda, int64_t ldw, int64_t K)
 {
@@ -162,7 +163,11 @@ bool wide_tiles_win(int64_t twide, int64_t t128) { return 8 * cdiv(twide, kNumCu
 //     2048x2048 50.2 against 60.9; 64 rows 48.0 narrow against 59);
 //   256x256 and 128x256 by their rounds (above);
 //   128x128 from 192 tiles (512x8192x8192 49.0, 64x128 54.0; 2048^3 15.2
-//     against 16.0; below, 256x8192x8192, 128 tiles, 40.0 against 32.9);
+//     against 16.0; below, 256x8192x8192, 128 tiles, 40.0 against 32.9), with
+//     two ring stages and two workgroups per compute unit where there are
+//     more tiles than units, or at short K (16384 rows over 32 experts of
+//     2048x2048 108 against 127 with three; 6560 over 82 of 59x1379 20 against
+//     29; 2048^3 16.0 against 15.3);
 //   64x128 from 129 tiles (1024x2048x2048 10.5, 64x64 14.5; 128x8192x8192,
 //     128 tiles, 32.5 against 22.6);
 //   64x64 from 128 tiles above 32 rows (128x8192x8192 22.6, 16x64 39.4;
@@ -180,7 +185,7 @@ int select_i8(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t lda, int6
     if (per > 64 && N > 128 && wide_tiles_win(tiles(128, 256), tiles(128, 128)) && fits(kI8Wide))
         return kI8Wide;
     if (per > 64 && tiles(128, 128) >= 192 && fits(kI8Mid))
-        return kI8Mid;
+        return tiles(128, 128) > kNumCu || K <= 512 ? kI8Two : kI8Mid;
     if (tiles(64, 128) > 128 && fits(kI8Half))
         return kI8Half;
     if (per > 32 && tiles(64, 64) >= 128 && fits(kI8Small))
@@ -193,11 +198,13 @@ int select_i8(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t lda, int6
 // ---------------------------------------------------------------------------
 using grouped_launch = void (*)(const GemmArgs &, const GroupArgs &, dim3, hipStream_t);
 
-// `launch` streams C past the caches; `launch_plain`, which the 256-column
-// tiles come with, does not: there lines that a row of C shares with the next
-// cost up to half more time streamed (us; 32768 rows over 32 experts of
-// 2048x2049 326 plain, 376 streamed; 65536 over 8 of 256x1030 112 and 173;
-// whole lines 278 and 287, 80 and 79).  Smaller tiles make no difference.
+// `launch` streams C past the caches; `launch_plain` does not (the same where
+// an entry has one form only).  Lines that a row of C shares with the next
+// cost up to half more time streamed where C is much of the work: 256-column
+// tiles (us; 32768 rows over 32 experts of 2048x2049 326 plain, 376 streamed;
+// 65536 over 8 of 256x1030 112 and 173; whole lines 278 and 287, 80 and 79) and
+// 128x128 ones two to a compute unit (both gradients of 9 rows over 101
+// experts of 1888x1381 314 and 545).
 struct GroupedEntry {
     int bm, bn, bk;
     grouped_launch launch, launch_plain;
@@ -209,25 +216,27 @@ void launch_grouped(const GemmArgs &a, const GroupArgs &g, dim3 grid, hipStream_
     hipLaunchKernelGGL((mpg::gemm_grouped_pipe<Cfg, STREAM>), grid, dim3(Cfg::NT), 0, s, a, g);
 }
 
-template <class Cfg>
+template <class Cfg, bool BOTH = false>
 constexpr GroupedEntry grouped_entry()
 {
-    return GroupedEntry{Cfg::BM, Cfg::BN, Cfg::BK, &launch_grouped<Cfg, true>,
-                        &launch_grouped<Cfg, Cfg::BN != 256>};
+    return GroupedEntry{Cfg::BM, Cfg::BN, Cfg::BK, &launch_grouped<Cfg, true>, &launch_grouped<Cfg, !BOTH>};
 }
 
 // The tiles of one form of the product.  Where the groups split the rows
-// (A row-major): 256x256, 128x256, 128x128, 64x128 and 32x64; where they split
-// K (A column-major): 256x256, 128x256, 128x128 and 64x64.
-enum : int { kGroupedBig = 0, kGroupedWide = 1, kGroupedMid = 2, kGroupedHalf = 3, kGroupedFew = 4, kGroupedSmall = 3 };
+// (A row-major): 256x256, 128x256, 128x128 with two ring stages (64 KiB of LDS:
+// two workgroups per compute unit) or three, 64x128 and 32x64; where they split
+// K (A column-major): 256x256, 128x256, 128x128 with two stages and 64x64.
+enum : int { kGroupedBig = 0, kGroupedWide = 1, kGroupedTwo = 2, kGroupedMid = 3, kGroupedHalf = 4, kGroupedFew = 5,
+             kWgradSmall = 3 };
 
 template <int LB, int IN>
 const GroupedEntry *rows_table()
 {
     static constexpr GroupedEntry table[] = {
-        grouped_entry<PipeCfg<256, 256, 64, 2, 4, 2, kRowMajor, LB, IN, 1, 16>>(),
-        grouped_entry<PipeCfg<128, 256, 64, 2, 4, 3, kRowMajor, LB, IN, 1, 16>>(),
-        grouped_entry<PipeCfg<128, 128, 128, 2, 4, 2, kRowMajor, LB, IN, 1, 32>>(),
+        grouped_entry<PipeCfg<256, 256, 64, 2, 4, 2, kRowMajor, LB, IN, 1, 16>, true>(),
+        grouped_entry<PipeCfg<128, 256, 64, 2, 4, 3, kRowMajor, LB, IN, 1, 16>, true>(),
+        grouped_entry<PipeCfg<128, 128, 64, 2, 4, 2, kRowMajor, LB, IN>, true>(),
+        grouped_entry<PipeCfg<128, 128, 64, 2, 4, 3, kRowMajor, LB, IN>>(),
         grouped_entry<PipeCfg<64, 128, 64, 2, 4, 3, kRowMajor, LB, IN, 1, 16>>(),
         grouped_entry<PipeCfg<32, 64, 128, 2, 4, 3, kRowMajor, LB, IN, 1, 16>>(),
     };
@@ -238,9 +247,9 @@ template <int IN>
 const GroupedEntry *wgrad_table()
 {
     static constexpr GroupedEntry table[] = {
-        grouped_entry<PipeCfg<256, 256, 64, 2, 4, 2, kColMajor, kRowMajor, IN, 1, 16>>(),
-        grouped_entry<PipeCfg<128, 256, 64, 2, 4, 3, kColMajor, kRowMajor, IN, 1, 16>>(),
-        grouped_entry<PipeCfg<128, 128, 128, 2, 4, 2, kColMajor, kRowMajor, IN, 1, 32>>(),
+        grouped_entry<PipeCfg<256, 256, 64, 2, 4, 2, kColMajor, kRowMajor, IN, 1, 16>, true>(),
+        grouped_entry<PipeCfg<128, 256, 64, 2, 4, 3, kColMajor, kRowMajor, IN, 1, 16>, true>(),
+        grouped_entry<PipeCfg<128, 128, 64, 2, 4, 2, kColMajor, kRowMajor, IN>, true>(),
         grouped_entry<PipeCfg<64, 64, 64, 2, 2, 2, kColMajor, kRowMajor, IN>>(),
     };
     return table;
@@ -273,13 +282,16 @@ bool grouped_fits(const GroupedEntry &e, int la, int lb, int64_t lda, int64_t ld
 //     experts 95, 32x64 106) or few tiles, else 32x64 (8 per over 64 experts
 //     108 against 123);
 //   128x128 above 64 per from 128 tiles (3000 rows, 13 experts of 617x800,
-//     182 tiles: 12.6, 64x128 15.0);
+//     182 tiles: 12.1, 64x128 15.0), two workgroups per compute unit where
+//     there are more tiles than units, or at short K (18000 rows, 13 experts
+//     45 against 52 with three stages; 6560 over 82 of 59x1379 17.5 against
+//     24; 4096 over 32 89 against 80);
 //   64x128 from 192 tiles above 32 per (64 per: 67, 32x64 77; 54 against 78
 //     with B row-major), or at any per with B row-major (32 per: 52 against
 //     58; B column-major 65 against 58);
 //   else 32x64 (300 rows, 13 experts of 617x800: 6.8, 64x128 9.0).
-int select_grouped(const GroupedEntry *table, int lb, int64_t groups, int64_t R, int64_t N, int64_t lda, int64_t ldb,
-                   int64_t ldc)
+int select_grouped(const GroupedEntry *table, int lb, int64_t groups, int64_t R, int64_t N, int64_t K, int64_t lda,
+                   int64_t ldb, int64_t ldc)
 {
     const int64_t per = cdiv(R, groups);
     auto tiles = [&](int64_t bm, int64_t bn) { return likely_tiles(R, groups, bm, cdiv(N, bn)); };
@@ -293,25 +305,29 @@ int select_grouped(const GroupedEntry *table, int lb, int64_t groups, int64_t R,
             return kGroupedWide;
     }
     if (per > 64 && tiles(128, 128) >= kNumCu / 2 && fits(kGroupedMid))
-        return kGroupedMid;
+        return tiles(128, 128) > kNumCu || K <= 256 ? kGroupedTwo : kGroupedMid;
     if ((per > 32 || lb == kRowMajor) && tiles(64, 128) >= 192 && fits(kGroupedHalf))
         return kGroupedHalf;
     return kGroupedFew;
 }
 
 // Table entry of a gradient by the weights (M x N per group; the groups split
-// K).  Below 128 tiles of 128x128, 64x64.
-int select_wgrad(const GroupedEntry *table, int64_t groups, int64_t M, int64_t N, int64_t lda, int64_t ldb, int64_t ldc)
+// K).  Up to 128 rows a group it is the writing of C: 128x128 with two
+// workgroups per compute unit, one writing while the other multiplies (512
+// rows over 64 experts of 2048x2048 164, 256x256 195; 4096 over 32 112 and
+// 115; 32768 over 32 412 and 325).  Below 128 tiles of 128x128, 64x64.
+int select_wgrad(const GroupedEntry *table, int64_t groups, int64_t R, int64_t M, int64_t N, int64_t lda, int64_t ldb,
+                 int64_t ldc)
 {
     auto tiles = [&](int64_t bm, int64_t bn) { return mul_sat(mul_sat(cdiv(M, bm), cdiv(N, bn)), groups); };
     auto fits = [&](int id) { return grouped_fits(table[id], kColMajor, kRowMajor, lda, ldb, ldc); };
-    if (M > 128 && N > 128 && big_tiles_win(tiles(256, 256), tiles(128, 128)) && fits(kGroupedBig))
-        return kGroupedBig;
-    if (N > 128 && wide_tiles_win(tiles(128, 256), tiles(128, 128)) && fits(kGroupedWide))
-        return kGroupedWide;
-    if (tiles(128, 128) >= kNumCu / 2 && fits(kGroupedMid))
-        return kGroupedMid;
-    return kGroupedSmall;
+    if (cdiv(R, groups) > 128) {
+        if (M > 128 && N > 128 && big_tiles_win(tiles(256, 256), tiles(128, 128)) && fits(kGroupedBig))
+            return kGroupedBig;
+        if (N > 128 && wide_tiles_win(tiles(128, 256), tiles(128, 128)) && fits(kGroupedWide))
+            return kGroupedWide;
+    }
+    return tiles(128, 128) >= kNumCu / 2 && fits(kGroupedTwo) ? kGroupedTwo : kWgradSmall;
 }
 
 // ---------------------------------------------------------------------------
@@ -724,7 +740,7 @@ int mpgemm_grouped(int in_type, int layout_b, int64_t groups, int64_t R, int64_t
         return MPGEMM_EALIGN;
     const GroupArgs group_args{offsets, (int32_t)groups, (int32_t)R, stride_b};
     const GroupedEntry *const table = grouped_family(kRowMajor, layout_b, in_type);
-    const int id = select_grouped(table, layout_b, groups, R, N, lda, ldb, ldc);
+    const int id = select_grouped(table, layout_b, groups, R, N, K, lda, ldb, ldc);
     if (id < 0 && span_fits(16, lda, K, 2) && span_fits(16, ldb, K, 2)) {
         const int64_t tiles_n = cdiv(N, 16);
         const int64_t grid = mul_sat(row_tiles(R, groups, 16), tiles_n);
@@ -800,7 +816,7 @@ int mpgemm_grouped_wgrad(int in_type, int64_t groups, int64_t R, int64_t M, int6
     if (!aligned(C, 4) || !aligned(offsets, 4) || (reads && (!aligned(A, 2) || !aligned(B, 2))))
         return MPGEMM_EALIGN;
     const GroupedEntry *const table = grouped_family(kColMajor, kRowMajor, in_type);
-    const GroupedEntry &e = table[select_wgrad(table, groups, M, N, lda, ldb, ldc)];
+    const GroupedEntry &e = table[select_wgrad(table, groups, R, M, N, lda, ldb, ldc)];
     if (!grouped_fits(e, kColMajor, kRowMajor, lda, ldb, ldc))
         return MPGEMM_ELD;
     const int64_t tiles_m = cdiv(M, e.bm), tiles_n = cdiv(N, e.bn);
