@@ -138,14 +138,15 @@ def _type(t, name, types=(MPGEMM_T_F16, MPGEMM_T_BF16, MPGEMM_T_F32)):
 
 
 def _rows(t, name, dtype):
-    """Leading dimension of a row-major 2-D GPU tensor."""
+    """(rows, columns, leading dimension) of a row-major 2-D GPU tensor."""
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.dim() == 2:
         # the ordinary case at once; the rest, and what is refused, below
         ld, step = t.stride()
         rows, cols = t.shape
         if step == 1 and rows > 1 and ld >= cols > 0:
-            return ld
-    return _check_tensor(t, name, dtype)[1]
+            return rows, cols, ld
+    ld = _check_tensor(t, name, dtype)[1]
+    return t.shape[0], t.shape[1], ld
 
 
 def _flat(t, name, dtype, shape):
@@ -183,18 +184,18 @@ def _matrices(t, name, dtype):
 
 
 def _on(stream, *tensors):
-    """(device, stream handle) of a call: every tensor on one GPU, the launch
-    on that GPU's current stream or the one given."""
-    device = tensors[0].device
+    """(device index, stream handle) of a call: every tensor on one GPU, the
+    launch on that GPU's current stream or the one given."""
+    device = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors are on {device} and {t.device}: one GPU is needed")
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors are on {tensors[0].device} and {t.device}: one GPU is needed")
     if stream is None:
         # the handle alone: a Stream object costs as much as a small launch
-        return device, torch._C._cuda_getCurrentRawStream(device.index)
+        return device, torch._C._cuda_getCurrentRawStream(device)
     if hasattr(stream, "cuda_stream"):
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        if stream.device.index != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {tensors[0].device}")
         return device, stream.cuda_stream
     return device, int(stream)
 
@@ -202,10 +203,11 @@ def _on(stream, *tensors):
 def _new(on, stream, *shapes):
     """Uninitialised int32 tensors that belong to the launch's stream: memory
     that another stream freed may still be in use there."""
+    device = torch.device("cuda", on[0])
     if stream is None:
-        return [torch.empty(shape, dtype=torch.int32, device=on[0]) for shape in shapes]
-    with torch.cuda.stream(torch.cuda.ExternalStream(on[1], device=on[0])):
-        return [torch.empty(shape, dtype=torch.int32, device=on[0]) for shape in shapes]
+        return [torch.empty(shape, dtype=torch.int32, device=device) for shape in shapes]
+    with torch.cuda.stream(torch.cuda.ExternalStream(on[1], device=device)):
+        return [torch.empty(shape, dtype=torch.int32, device=device) for shape in shapes]
 
 
 def _workspace(on, stream, given, need):
@@ -224,7 +226,7 @@ def _workspace(on, stream, given, need):
 def _call(fn, on, *args):
     """fn(*args, stream) with the tensors' GPU current; raises on an error."""
     device, handle = on
-    if torch._C._cuda_getDevice() == device.index:
+    if torch._C._cuda_getDevice() == device:
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(device):
@@ -247,11 +249,9 @@ def quantize_rows(X, Q, scale, order=None, top_k: int = 1, workspace=None, strea
     if torch is None:
         _with_torch()
     xt = _type(X, "X")
-    ldx = _rows(X, "X", X.dtype)
-    ldq = _rows(Q, "Q", torch.int8)
-    T, H = X.shape
-    R = Q.shape[0]
-    if Q.shape[1] != H or (order is None and R != T):
+    T, H, ldx = _rows(X, "X", X.dtype)
+    R, H2, ldq = _rows(Q, "Q", torch.int8)
+    if H2 != H or (order is None and R != T):
         raise ValueError(f"shape mismatch: X {tuple(X.shape)}, Q {tuple(Q.shape)}")
     sp = _flat(scale, "scale", torch.float32, (R,))
     op = 0 if order is None else _flat(order, "order", torch.int32, (R,))
@@ -276,9 +276,8 @@ def gemm_i8(A, B, C, scale_a, scale_b, bias=None, offsets=None, stream=None):
     if torch is None:
         _with_torch()
     ot = _type(C, "C")
-    lda = _rows(A, "A", torch.int8)
-    ldc = _rows(C, "C", C.dtype)
-    M, K = A.shape
+    M, K, lda = _rows(A, "A", torch.int8)
+    M2, N2, ldc = _rows(C, "C", C.dtype)
     if offsets is None:
         if not isinstance(B, torch.Tensor) or B.dim() != 2:
             raise ValueError("B must be 2-D (3-D with offsets)")
@@ -294,7 +293,7 @@ def gemm_i8(A, B, C, scale_a, scale_b, bias=None, offsets=None, stream=None):
             if B.stride(1) != 1 and N == 1:
                 raise ValueError("B must be column-major (unit stride along K)")
             ldw = K2
-    if K2 != K or tuple(C.shape) != (M, N):
+    if K2 != K or M2 != M or N2 != N:
         raise ValueError(f"shape mismatch: A {tuple(A.shape)}, B {tuple(B.shape)}, C {tuple(C.shape)}")
     wide = (N,) if offsets is None else (G, N)
     sa = _flat(scale_a, "scale_a", torch.float32, (M,))
@@ -355,12 +354,12 @@ def gather_rows(X, order, Y, top_k: int = 1, workspace=None, stream=None):
     if torch is None:
         _with_torch()
     ty = _type(X, "X")
-    ldx, ldy = _rows(X, "X", X.dtype), _rows(Y, "Y", X.dtype)
-    if X.shape[1] != Y.shape[1]:
+    T, H, ldx = _rows(X, "X", X.dtype)
+    R, H2, ldy = _rows(Y, "Y", X.dtype)
+    if H2 != H:
         raise ValueError(f"shape mismatch: X {tuple(X.shape)}, Y {tuple(Y.shape)}")
-    op = _flat(order, "order", torch.int32, (Y.shape[0],))
+    op = _flat(order, "order", torch.int32, (R,))
     lib, on = load_ops(), _on(stream, Y, X, order, workspace)
-    T, H, R = X.shape[0], X.shape[1], Y.shape[0]
     wp, wb, _ws = _workspace(on, stream, workspace, lib.mpgemm_rows_workspace(ty, T, H, R, int(top_k)))
     _call(lib.mpgemm_gather_rows, on, ty, T, H, X.data_ptr(), ldx, op, R, int(top_k), Y.data_ptr(), ldy, wp, wb)
     return Y
@@ -382,14 +381,14 @@ def combine_rows(Y, position, out, weights=None, stream=None):
     if torch is None:
         _with_torch()
     yt, ot = _type(Y, "Y"), _type(out, "out")
-    ldy, ldo = _rows(Y, "Y", Y.dtype), _rows(out, "out", out.dtype)
-    T, H = out.shape
-    if Y.shape[1] != H:
+    R, H2, ldy = _rows(Y, "Y", Y.dtype)
+    T, H, ldo = _rows(out, "out", out.dtype)
+    if H2 != H:
         raise ValueError(f"shape mismatch: Y {tuple(Y.shape)}, out {tuple(out.shape)}")
     pp = _flat(position, "position", torch.int32, None)
     k = _slots(position, T)
     wp = 0 if weights is None else _flat(weights, "weights", torch.float32, (T, k))
-    _call(load_ops().mpgemm_combine_rows, _on(stream, out, Y, position, weights), yt, ot, T, k, H, Y.shape[0],
+    _call(load_ops().mpgemm_combine_rows, _on(stream, out, Y, position, weights), yt, ot, T, k, H, R,
           Y.data_ptr(), ldy, pp, wp, out.data_ptr(), ldo)
     return out
 
@@ -406,23 +405,24 @@ def combine_rows_backward(dout, Y, position, weights, dY, dweights=None, stream=
     if torch is None:
         _with_torch()
     dt, gt = _type(dout, "dout"), _type(dY, "dY")
-    ldo, ldg = _rows(dout, "dout", dout.dtype), _rows(dY, "dY", dY.dtype)
-    T, H = dout.shape
+    T, H, ldo = _rows(dout, "dout", dout.dtype)
+    R, H2, ldg = _rows(dY, "dY", dY.dtype)
     yt, ldy, yp = dt, ldo, 0
     if Y is not None:
-        yt, ldy, yp = _type(Y, "Y"), _rows(Y, "Y", Y.dtype), Y.data_ptr()
+        yt, yp = _type(Y, "Y"), Y.data_ptr()
+        ldy = _rows(Y, "Y", Y.dtype)[2]
         if Y.shape != dY.shape:
             raise ValueError(f"shape mismatch: Y {tuple(Y.shape)}, dY {tuple(dY.shape)}")
     elif dweights is not None:
         raise ValueError("dweights needs Y")
-    if dY.shape[1] != H:
+    if H2 != H:
         raise ValueError(f"shape mismatch: dout {tuple(dout.shape)}, dY {tuple(dY.shape)}")
     pp = _flat(position, "position", torch.int32, None)
     k = _slots(position, T)
     wp = 0 if weights is None else _flat(weights, "weights", torch.float32, (T, k))
     gp = 0 if dweights is None else _flat(dweights, "dweights", torch.float32, (T, k))
     _call(load_ops().mpgemm_combine_rows_backward, _on(stream, dY, dout, Y, position, weights, dweights), dt, yt,
-          gt, T, k, H, dY.shape[0], dout.data_ptr(), ldo, yp, ldy, pp, wp, dY.data_ptr(), ldg, gp)
+          gt, T, k, H, R, dout.data_ptr(), ldo, yp, ldy, pp, wp, dY.data_ptr(), ldg, gp)
     return dY, dweights
 
 
@@ -437,10 +437,10 @@ def gemm_grouped(A, B, C, offsets, alpha: float = 1.0, beta: float = 0.0, stream
     if torch is None:
         _with_torch()
     it = _type(A, "A", (MPGEMM_T_F16, MPGEMM_T_BF16))
-    lda, ldc = _rows(A, "A", A.dtype), _rows(C, "C", torch.float32)
+    R, K, lda = _rows(A, "A", A.dtype)
+    R2, N2, ldc = _rows(C, "C", torch.float32)
     G, K2, N, layout, ldb, stride = _matrices(B, "B", A.dtype)
-    R, K = A.shape
-    if K2 != K or tuple(C.shape) != (R, N):
+    if K2 != K or R2 != R or N2 != N:
         raise ValueError(f"shape mismatch: A {tuple(A.shape)}, B {tuple(B.shape)}, C {tuple(C.shape)}")
     op = _flat(offsets, "offsets", torch.int32, (G + 1,))
     _call(load_ops().mpgemm_grouped, _on(stream, C, A, B, offsets), it, layout, G, R, N, K, A.data_ptr(), lda,
@@ -460,12 +460,12 @@ def gemm_grouped_wgrad(A, B, C, offsets, alpha: float = 1.0, beta: float = 0.0, 
     it = _type(A, "A", (MPGEMM_T_F16, MPGEMM_T_BF16))
     if A.dim() != 2:
         raise ValueError("A must be 2-D")
-    lda, ldb = _rows(A.t(), "A (transposed)", A.dtype), _rows(B, "B", A.dtype)
+    R2, M2, lda = _rows(A.t(), "A (transposed)", A.dtype)
+    R, N2, ldb = _rows(B, "B", A.dtype)
     G, M, N, layout, ldc, stride = _matrices(C, "C", torch.float32)
     if layout != MPGEMM_ROW_MAJOR:
         raise ValueError("C must be row-major")
-    R = B.shape[0]
-    if tuple(A.shape) != (M, R) or B.shape[1] != N:
+    if M2 != M or R2 != R or N2 != N:
         raise ValueError(f"shape mismatch: A {tuple(A.shape)}, B {tuple(B.shape)}, C {tuple(C.shape)}")
     op = _flat(offsets, "offsets", torch.int32, (G + 1,))
     _call(load_ops().mpgemm_grouped_wgrad, _on(stream, C, A, B, offsets), it, G, R, M, N, A.data_ptr(), lda,
