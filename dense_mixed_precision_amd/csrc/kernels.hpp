@@ -229,6 +229,7 @@ gemm_direct(GemmArgs args)
                  lane);
 }
 
+#ifndef MPGEMM_GROUPED
 // Split-K reduction: C <- alpha * sum_{s<splits} ws[s] + beta*C (+ bias[j]),
 // the partials summed in ascending s (run-to-run deterministic).  ws holds
 // `splits` row-major M x N partial products, rows of N.  Grid-stride over
@@ -270,6 +271,7 @@ scale_c(float *C, int64_t M, int64_t N, int64_t ldc, float beta, const float *bi
         }
     }
 }
+#endif
 
 // ---------------------------------------------------------------------------
 // Pipelined kernel: global -> LDS with buffer_load ... lds

@@ -3,11 +3,15 @@
 // i8_kernels.hpp.
 //
 // At most 16 token rows per tile make the product a stream over the weights
-// (N x K, K-contiguous): 16 channels per workgroup, its 8 waves splitting K,
+// (N x K, K-contiguous): 16 channels per workgroup, its waves splitting K,
 // the weights straight from memory into operand registers with DEPTH loads in
 // flight, the tokens beside them (a few rows, from the L2).  Nothing of a weight row is
 // used twice, so an LDS ring would only add a copy and a barrier per K tile.
-// The 8 partial tiles are summed in LDS in wave order.
+// The waves' partial tiles are summed in LDS in wave order.
+//
+// Bound: HBM.  8x8192x8192 codes 14.4 us, 4.65 TB/s; 64 BF16 rows over 64
+// experts of 2048x2048, of which they reach about 41, 58 us, 5.9 TB/s (1 GiB
+// copies at 5.2).
 //
 // The same bytes serve 8-bit codes (v_mfma_i32_16x16x64_i8, 16 codes per lane)
 // and 16-bit values (v_mfma_f32_16x16x32_{f16,bf16}, 8 per lane); the weights
@@ -42,14 +46,14 @@ struct NarrowAcc<kNarrowI8> {
     static constexpr int ES = 1;
 };
 
-template <int IN, int OUT, int DEPTH, int WAVES, int NB = 1, int POLICY = 0>
+template <int IN, int OUT, int DEPTH, int WAVES>
 __global__ void __launch_bounds__(64 * WAVES)
 narrow_rows(NarrowArgs args)
 {
     typedef typename NarrowAcc<IN>::type Acc;
     typedef typename ElemOf<OUT>::type E;
     constexpr int ES = NarrowAcc<IN>::ES;
-    __shared__ Acc part[WAVES][NB][64];
+    __shared__ Acc part[WAVES][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     GroupTile gt;
@@ -57,7 +61,7 @@ narrow_rows(NarrowArgs args)
         return;
     const int row0 = gt.start + gt.tm * 16;
     const int rows = min(gt.rows - gt.tm * 16, 16);
-    const int n0 = gt.tn * 16 * NB;
+    const int n0 = gt.tn * 16;
     const int cols = args.N - n0;
     const int KB = (IN != kNarrowI8 && args.alpha == 0.0f) ? 0 : args.KB;
     const int r = lane & 15;          // token of the second operand, channel of the first
@@ -68,10 +72,7 @@ narrow_rows(NarrowArgs args)
     const __amdgpu_buffer_rsrc_t rsA = make_rsrc(Ap), rsW = make_rsrc(Wp);
     // 32-bit offsets: the host checks that 16 rows span less than 2 GiB
     const uint32_t offA = (uint32_t)(r * (int)args.lda + kq);
-    uint32_t offW[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-        offW[b] = 16 * b + r < cols ? (uint32_t)((16 * b + r) * (int)args.ldw + kq) : kOOB;
+    const uint32_t offW = r < cols ? (uint32_t)(r * (int)args.ldw + kq) : kOOB;
 
     // this wave's 64-byte steps of the whole vectors; the last KB % 16 bytes
     // are a step of their own
@@ -79,26 +80,20 @@ narrow_rows(NarrowArgs args)
     const int steps = (whole + 63) / 64;
     const int per = (steps + WAVES - 1) / WAVES;
     const int s0 = min(wave * per, steps), s1 = min(s0 + per, steps);
-    u32x4 ra[DEPTH], rw[DEPTH][NB];
+    u32x4 ra[DEPTH], rw[DEPTH];
     auto issue = [&](int d, int s) __attribute__((always_inline)) {
         const bool k_ok = 64 * s + kq < whole;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-            rw[d][b] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsW, k_ok ? offW[b] : kOOB, 64 * s,
-                                                                                       POLICY));
+        rw[d] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsW, k_ok ? offW : kOOB, 64 * s, 0));
         ra[d] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsA, (a_ok && k_ok) ? offA + 64 * s : kOOB,
                                                                                 0, 0));
     };
-    Acc acc[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-        acc[b] = Acc{0};
-    auto multiply = [&](int b, const u32x4 &w, const u32x4 &a) __attribute__((always_inline)) {
+    Acc acc = Acc{0};
+    auto multiply = [&](const u32x4 &w, const u32x4 &a) __attribute__((always_inline)) {
         if constexpr (IN == kNarrowI8)
-            acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4v, w), __builtin_bit_cast(i32x4v, a),
-                                                           acc[b], 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4v, w), __builtin_bit_cast(i32x4v, a),
+                                                        acc, 0, 0, 0);
         else
-            acc[b] = mfma16<IN>(__builtin_bit_cast(half8, w), __builtin_bit_cast(half8, a), acc[b]);
+            acc = mfma16<IN>(__builtin_bit_cast(half8, w), __builtin_bit_cast(half8, a), acc);
     };
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d)
@@ -108,9 +103,7 @@ narrow_rows(NarrowArgs args)
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) {
             if (s + d < s1) {
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-                    multiply(b, rw[d][b], ra[d]);
+                multiply(rw[d], ra[d]);
                 if (s + d + DEPTH < s1)
                     issue(d, s + d + DEPTH);
             }
@@ -135,25 +128,19 @@ narrow_rows(NarrowArgs args)
             }
             return u32x4{v[0], v[1], v[2], v[3]};
         };
-        const u32x4 a = tail(rsA, a_ok ? offA : kOOB);
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-            multiply(b, tail(rsW, offW[b]), a);
+        multiply(tail(rsW, offW), tail(rsA, a_ok ? offA : kOOB));
     }
 
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-        part[wave][b][lane] = acc[b];
+    part[wave][lane] = acc;
     __syncthreads();
-    if (wave >= NB)
+    if (wave != 0)
         return;
-    // wave b finishes channel block b
-    Acc sum = part[0][wave][lane];
+    Acc sum = part[0][lane];
 #pragma unroll
     for (int w = 1; w < WAVES; ++w)
-        sum += part[w][wave][lane];
+        sum += part[w][lane];
 
-    const int c = 16 * wave + 4 * (lane >> 4);
+    const int c = 4 * (lane >> 4);
     const int left = cols - c;
     if (!a_ok || left <= 0)
         return;
