@@ -10,8 +10,8 @@
 // Measured (us; BF16, 32 experts of 2048x2048): 32768 rows of equal shares 271
 // (B column-major) and 282 (row-major), gradient by the weights 325, against 216
 // at the rate of a large library product: FP32 tiles of 256 KiB are written at
-// the end of each round of tiles.  With unequal shares 313, 330 and 345: the
-// compute units hold waves 83 to 85% of the time.
+// the end of each round of tiles.  With unequal shares 313, 330 and about
+// 340: the compute units hold waves 83% (rows) and 93% (weights) of the time.
 //
 // Offsets are read as untrusted data: each range is clamped to [0, rows], so
 // whatever they hold no workgroup leaves the operands.
