@@ -31,6 +31,7 @@ using mpg::PipeCfg;
 
 constexpr int kNumCu = 256;
 constexpr int64_t kMax32 = 0x7FFFFFFF;
+constexpr int64_t kMaxWidth = (int64_t)1 << 28;  // values of a token's row: a row spans at most 1 GiB
 constexpr int64_t kMaxSpan = 0x7FFFFFF0;  // bytes a 32-bit buffer offset may reach
 
 int64_t at_least_one(int64_t v) { return v > 1 ? v : 1; }
@@ -50,6 +51,19 @@ bool aligned(const void *p, int64_t bytes) { return (reinterpret_cast<uintptr_t>
 
 bool is_type(int t) { return t == MPGEMM_T_F16 || t == MPGEMM_T_BF16 || t == MPGEMM_T_F32; }
 int64_t size_of(int t) { return t == MPGEMM_T_F32 ? 4 : 2; }
+
+// A launch holds fewer than 2^32 threads in one dimension: at most this many
+// workgroups of up to 512.
+constexpr int64_t kMaxGrid = (int64_t)1 << 22;
+
+// `blocks` workgroups (fewer than 2^31) over x and y; the last ones may have
+// nothing to do.
+dim3 row_grid(int64_t blocks, int64_t z = 1)
+{
+    if (blocks <= kMaxGrid)
+        return dim3((unsigned)blocks, 1, (unsigned)z);
+    return dim3((unsigned)kMaxGrid, (unsigned)cdiv(blocks, kMaxGrid), (unsigned)z);
+}
 
 hipStream_t stream_of(void *s) { return reinterpret_cast<hipStream_t>(s); }
 
@@ -361,18 +375,18 @@ void launch_quantize(mpg::QuantArgs a, int32_t *inverse, hipStream_t s)
     constexpr int64_t kWaveRow = 64 * 8 * (XT == mpg::kTF32 ? 4 : 8);
     if (inverse) {
         launch_fill(inverse, (int64_t)a.T * a.top_k, s);
-        hipLaunchKernelGGL((mpg::quantize_invert<XT>), dim3((unsigned)cdiv(a.R, 256)), dim3(256), 0, s, a, inverse);
+        hipLaunchKernelGGL((mpg::quantize_invert<XT>), row_grid(cdiv(a.R, 256)), dim3(256), 0, s, a, inverse);
         a.inverse = inverse;
         if (a.H <= kWaveRow)
-            hipLaunchKernelGGL((mpg::quantize_rows<XT, 64, 8, true>), dim3((unsigned)cdiv(a.T, 4)), dim3(256), 0, s, a);
+            hipLaunchKernelGGL((mpg::quantize_rows<XT, 64, 8, true>), row_grid(cdiv(a.T, 4)), dim3(256), 0, s, a);
         else
-            hipLaunchKernelGGL((mpg::quantize_rows<XT, 256, 4, true>), dim3((unsigned)a.T), dim3(256), 0, s, a);
+            hipLaunchKernelGGL((mpg::quantize_rows<XT, 256, 4, true>), row_grid(a.T), dim3(256), 0, s, a);
         return;
     }
     if (a.R >= 8 * kNumCu && a.H <= kWaveRow)
-        hipLaunchKernelGGL((mpg::quantize_rows<XT, 64, 8>), dim3((unsigned)cdiv(a.R, 4)), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((mpg::quantize_rows<XT, 64, 8>), row_grid(cdiv(a.R, 4)), dim3(256), 0, s, a);
     else
-        hipLaunchKernelGGL((mpg::quantize_rows<XT, 256, 4>), dim3((unsigned)a.R), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((mpg::quantize_rows<XT, 256, 4>), row_grid(a.R), dim3(256), 0, s, a);
 }
 
 template <int YT>
@@ -393,11 +407,9 @@ void launch_combine_backward(const mpg::CombineBackArgs &a, hipStream_t s)
 {
     const int64_t pairs = (int64_t)a.T * a.top_k;
     if (a.H <= 256)
-        hipLaunchKernelGGL((mpg::combine_rows_backward<DT, YT, GT, 16>), dim3((unsigned)cdiv(pairs, 16)), dim3(256), 0,
-                           s, a);
+        hipLaunchKernelGGL((mpg::combine_rows_backward<DT, YT, GT, 16>), row_grid(cdiv(pairs, 16)), dim3(256), 0, s, a);
     else
-        hipLaunchKernelGGL((mpg::combine_rows_backward<DT, YT, GT, 64>), dim3((unsigned)cdiv(pairs, 4)), dim3(256), 0,
-                           s, a);
+        hipLaunchKernelGGL((mpg::combine_rows_backward<DT, YT, GT, 64>), row_grid(cdiv(pairs, 4)), dim3(256), 0, s, a);
 }
 
 template <int DT, int YT>
@@ -464,7 +476,7 @@ int mpgemm_quantize_rows(int x_type, int64_t T, int64_t H, const void *X, int64_
 {
     if (!is_type(x_type))
         return MPGEMM_ETYPE;
-    if (T < 0 || H < 0 || R < 0 || T > kMax32 || H > kMax32 || R > kMax32)
+    if (T < 0 || H < 0 || R < 0 || T > kMax32 || H > kMaxWidth || R > kMax32)
         return MPGEMM_EDIM;
     if (order ? (top_k < 1 || top_k > kMax32) : R != T)
         return MPGEMM_EDIM;
@@ -516,7 +528,7 @@ int mpgemm_i8_gemm(int out_type, int64_t groups, int64_t M, int64_t N, int64_t K
     if (id < 0) {
         const int64_t tiles_n = cdiv(N, 16);
         const int64_t grid = mul_sat(row_tiles(M, offsets ? groups : 1, 16), tiles_n);
-        if (grid > kMax32 / 64)
+        if (grid > kMaxGrid)
             return MPGEMM_EDIM;
         mpg::NarrowArgs a{};
         a.A = reinterpret_cast<const uint8_t *>(A);
@@ -540,7 +552,7 @@ int mpgemm_i8_gemm(int out_type, int64_t groups, int64_t M, int64_t N, int64_t K
     const I8Entry &e = kI8Table[id];
     const int64_t tiles_n = cdiv(N, e.bn);
     const int64_t grid = mul_sat(row_tiles(M, offsets ? groups : 1, e.bm), tiles_n);
-    if (grid > kMax32 / 64)
+    if (grid > kMaxGrid)
         return MPGEMM_EDIM;
     I8Args a{};
     a.A = A;
@@ -617,7 +629,7 @@ int64_t mpgemm_rows_workspace(int type, int64_t T, int64_t H, int64_t R, int64_t
 {
     if (!is_type(type))
         return MPGEMM_ETYPE;
-    if (T < 0 || H < 0 || R < 0 || top_k < 1 || T > kMax32 || H > kMax32 || R > kMax32 || top_k > kMax32)
+    if (T < 0 || H < 0 || R < 0 || top_k < 1 || T > kMax32 || H > kMaxWidth || R > kMax32 || top_k > kMax32)
         return MPGEMM_EDIM;
     return inverse_bytes(T, R, top_k, H * size_of(type));
 }
@@ -629,7 +641,7 @@ int mpgemm_gather_rows(int type, int64_t T, int64_t H, const void *X, int64_t ld
     if (!is_type(type))
         return MPGEMM_ETYPE;
     const int64_t es = size_of(type);
-    if (T < 0 || H < 0 || R < 0 || T > kMax32 || H > kMax32 / 4 || R > kMax32 || top_k < 1 || top_k > kMax32)
+    if (T < 0 || H < 0 || R < 0 || T > kMax32 || H > kMaxWidth || R > kMax32 || top_k < 1 || top_k > kMax32)
         return MPGEMM_EDIM;
     if (ldx < at_least_one(H) || ldy < at_least_one(H) || ldx > INT64_MAX / 4 || ldy > INT64_MAX / 4)
         return MPGEMM_ELD;
@@ -646,11 +658,10 @@ int mpgemm_gather_rows(int type, int64_t T, int64_t H, const void *X, int64_t ld
     if (need > 0 && workspace != nullptr && workspace_bytes >= need) {
         int32_t *const inverse = static_cast<int32_t *>(workspace);
         launch_fill(inverse, T * top_k, stream_of(stream));
-        hipLaunchKernelGGL(mpg::gather_invert, dim3((unsigned)cdiv(R, 256)), dim3(256), 0, stream_of(stream), a,
-                           inverse);
-        hipLaunchKernelGGL(mpg::gather_tokens, dim3((unsigned)cdiv(T, 4)), dim3(256), 0, stream_of(stream), a, inverse);
+        hipLaunchKernelGGL(mpg::gather_invert, row_grid(cdiv(R, 256)), dim3(256), 0, stream_of(stream), a, inverse);
+        hipLaunchKernelGGL(mpg::gather_tokens, row_grid(cdiv(T, 4)), dim3(256), 0, stream_of(stream), a, inverse);
     } else {
-        hipLaunchKernelGGL(mpg::gather_rows, dim3((unsigned)cdiv(R, 4)), dim3(256), 0, stream_of(stream), a);
+        hipLaunchKernelGGL(mpg::gather_rows, row_grid(cdiv(R, 4)), dim3(256), 0, stream_of(stream), a);
     }
     return launched();
 }
@@ -661,7 +672,7 @@ int mpgemm_combine_rows(int y_type, int o_type, int64_t T, int64_t top_k, int64_
 {
     if (!is_type(y_type) || !is_type(o_type))
         return MPGEMM_ETYPE;
-    if (T < 0 || H < 0 || R < 0 || top_k < 0 || T > kMax32 || H > kMax32 - 4096 || R > kMax32 || top_k > kMax32)
+    if (T < 0 || H < 0 || R < 0 || top_k < 0 || T > kMax32 || H > kMaxWidth || R > kMax32 || top_k > kMax32)
         return MPGEMM_EDIM;
     if (ldy < at_least_one(H) || ldo < at_least_one(H))
         return MPGEMM_ELD;
@@ -672,8 +683,8 @@ int mpgemm_combine_rows(int y_type, int o_type, int64_t T, int64_t top_k, int64_
     if (!aligned(Y, size_of(y_type)) || !aligned(O, size_of(o_type)) || !aligned(position, 4) || !aligned(weights, 4))
         return MPGEMM_EALIGN;
     const mpg::CombineArgs a{Y, O, position, weights, ldy, ldo, (int32_t)T, (int32_t)H, (int32_t)R, (int32_t)top_k};
-    const int64_t gy = cdiv(H, y_type == MPGEMM_T_F32 ? 1024 : 2048);
-    const dim3 grid((unsigned)T, (unsigned)(gy < 65535 ? gy : 65535));
+    const int64_t gz = cdiv(H, y_type == MPGEMM_T_F32 ? 1024 : 2048);
+    const dim3 grid = row_grid(T, gz < 65535 ? gz : 65535);
     forget_error();
     if (y_type == MPGEMM_T_F16)
         launch_combine<mpg::kTF16>(o_type, a, grid, stream_of(stream));
@@ -692,7 +703,7 @@ int mpgemm_combine_rows_backward(int d_type, int y_type, int dy_type,
 {
     if (!is_type(d_type) || !is_type(y_type) || !is_type(dy_type))
         return MPGEMM_ETYPE;
-    if (T < 0 || H < 0 || R < 0 || top_k < 0 || T > kMax32 || H > kMax32 || R > kMax32 || top_k > kMax32 ||
+    if (T < 0 || H < 0 || R < 0 || top_k < 0 || T > kMax32 || H > kMaxWidth || R > kMax32 || top_k > kMax32 ||
         mul_sat(T, top_k) > kMax32)
         return MPGEMM_EDIM;
     if (ldo < at_least_one(H) || lddy < at_least_one(H) || (dweights && ldy < at_least_one(H)))
@@ -744,7 +755,7 @@ int mpgemm_grouped(int in_type, int layout_b, int64_t groups, int64_t R, int64_t
     if (id < 0 && span_fits(16, lda, K, 2) && span_fits(16, ldb, K, 2)) {
         const int64_t tiles_n = cdiv(N, 16);
         const int64_t grid = mul_sat(row_tiles(R, groups, 16), tiles_n);
-        if (grid > kMax32 / 64)
+        if (grid > kMaxGrid)
             return MPGEMM_EDIM;
         mpg::NarrowArgs a{};
         a.A = reinterpret_cast<const uint8_t *>(A);
@@ -772,7 +783,7 @@ int mpgemm_grouped(int in_type, int layout_b, int64_t groups, int64_t R, int64_t
         return MPGEMM_ELD;
     const int64_t tiles_n = cdiv(N, e.bn);
     const int64_t grid = mul_sat(row_tiles(R, groups, e.bm), tiles_n);
-    if (grid > kMax32 / 64)
+    if (grid > kMaxGrid)
         return MPGEMM_EDIM;
     GemmArgs a{};
     a.A = A;
@@ -821,7 +832,7 @@ int mpgemm_grouped_wgrad(int in_type, int64_t groups, int64_t R, int64_t M, int6
         return MPGEMM_ELD;
     const int64_t tiles_m = cdiv(M, e.bm), tiles_n = cdiv(N, e.bn);
     const int64_t grid = mul_sat(mul_sat(tiles_m, tiles_n), groups);
-    if (grid > kMax32 / 64)
+    if (grid > kMaxGrid)
         return MPGEMM_EDIM;
     GemmArgs a{};
     a.A = A;

@@ -29,6 +29,10 @@ __device__ __forceinline__ void invert_one(const int32_t *order, int32_t *invers
         redo(pair, old);
 }
 
+// Workgroup number of a launch over x and y (see row_grid): one dimension holds
+// fewer than 2^32 threads.
+__device__ __forceinline__ int64_t wg_number() { return blockIdx.x + (int64_t)blockIdx.y * gridDim.x; }
+
 // Rows are read and written in vectors of 16 bytes at any element alignment.
 template <class E>
 struct VecOf {
@@ -132,7 +136,7 @@ quantize_rows(QuantArgs args)
     typedef typename VecOf<E>::type V;
     __shared__ uint32_t part[4];
     const int tid = threadIdx.x % NT;
-    const int64_t row = (int64_t)blockIdx.x * (256 / NT) +
+    const int64_t row = wg_number() * (256 / NT) +
                         (NT == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : 0);
     if (row >= (TOKENS ? args.T : args.R))
         return;
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(256)
 quantize_invert(QuantArgs args, int32_t *inverse)
 {
     typedef typename ElemOf<XT>::type E;
-    const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t p = wg_number() * 256 + threadIdx.x;
     if (p >= args.R)
         return;
     invert_one(args.order, inverse, p, (int64_t)args.T * args.top_k, [&](int pair, int old) {
@@ -515,7 +519,7 @@ __global__ void __launch_bounds__(256)
 gather_rows(GatherArgs a)
 {
     const int lane = threadIdx.x & 63;
-    const int64_t p = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t p = wg_number() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (p >= a.R)
         return;
     const int pair = a.order[p];
@@ -544,7 +548,7 @@ gather_rows(GatherArgs a)
 __global__ void __launch_bounds__(256)
 gather_invert(GatherArgs a, int32_t *inverse)
 {
-    const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t p = wg_number() * 256 + threadIdx.x;
     if (p >= a.R)
         return;
     invert_one(a.order, inverse, p, (int64_t)a.T * a.top_k, [&](int pair, int old) {
@@ -563,7 +567,7 @@ __global__ void __launch_bounds__(256)
 gather_tokens(GatherArgs a, const int32_t *inverse)
 {
     const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t = wg_number() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (t >= a.T)
         return;
     const uint8_t *const x = a.X + t * a.ldx;
@@ -615,9 +619,11 @@ combine_rows(CombineArgs a)
     typedef typename ElemOf<OT>::type EO;
     constexpr int VN = VecOf<EY>::N;
     typedef typename VecOf<EY>::type V;
-    const int64_t t = blockIdx.x;
+    const int64_t t = wg_number();
+    if (t >= a.T)
+        return;
     const int32_t *const at = a.position + t * a.top_k;
-    for (int64_t c = (int64_t)VN * (blockIdx.y * 256 + threadIdx.x); c < a.H; c += (int64_t)VN * 256 * gridDim.y) {
+    for (int64_t c = (int64_t)VN * (blockIdx.z * 256 + threadIdx.x); c < a.H; c += (int64_t)VN * 256 * gridDim.z) {
         const int left = (int)(a.H - c);
         float acc[VN];
 #pragma unroll
@@ -682,7 +688,7 @@ combine_rows_backward(CombineBackArgs a)
     constexpr int VN = 8;
     const int lane = threadIdx.x % LANES;
     const int sub = threadIdx.x / LANES;
-    const int64_t pair = (int64_t)blockIdx.x * (256 / LANES) + (LANES == 64 ? __builtin_amdgcn_readfirstlane(sub) : sub);
+    const int64_t pair = wg_number() * (256 / LANES) + (LANES == 64 ? __builtin_amdgcn_readfirstlane(sub) : sub);
     if (pair >= (int64_t)a.T * a.top_k)
         return;
     const int p = a.position[pair];

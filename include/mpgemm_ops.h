@@ -19,8 +19,10 @@
  * allocated, kept or synchronized, 0 or a negative MPGEMM_E* code (argument
  * errors before any HIP call).  Every call may be recorded into a HIP graph.
  * Results are the same from run to run.  Outputs must not overlap inputs or
- * each other.  Any size >= 0 is accepted within the limits named below, and
- * any element alignment.
+ * each other.  Any size >= 0 is accepted within the limits named below
+ * (MPGEMM_EDIM beyond them), and any element alignment.  A token's row has at
+ * most 2^28 values; a product has at most 2^22 tiles, of at least 16x16 values
+ * each and of up to 256x256 where the rows are many.
  *
  * Experts.  T tokens with top_k slots each make T*top_k pairs, pair
  * t*top_k + s for slot s of token t.  Sorted by expert they take positions

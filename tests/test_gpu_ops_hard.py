@@ -215,6 +215,34 @@ def test_callers_workspaces():
 
 # ---- offsets beyond 32 bits -------------------------------------------------
 
+def test_more_rows_than_one_dimension_of_a_launch_holds():
+    """2^24 + 5 rows: combine takes a workgroup of 256 for each, over 2^32
+    threads, the others a wave."""
+    dev = device()
+    n = (1 << 24) + 5
+    x = torch.arange(n, device=dev, dtype=torch.int32).bitwise_and_(127).add_(1).to(torch.float16).view(n, 1)
+    q, s = torch.zeros(n, 1, dtype=torch.int8, device=dev), torch.zeros(n, device=dev)
+    mp.quantize_rows(x, q, s)
+    # (in 64 bits: torch divides FP32 by a number through its reciprocal)
+    assert (q == 127).all() and torch.equal(s, (x.double() / 127.0).float().view(-1))
+    position = torch.arange(n - 1, -1, -1, device=dev, dtype=torch.int32).view(n, 1)
+    out = torch.zeros(n, 1, device=dev)
+    mp.combine_rows(x, position, out)
+    assert torch.equal(out, x.float().flip(0))
+    dy, dw = torch.zeros(n, 1, dtype=torch.float16, device=dev), torch.zeros(n, 1, device=dev)
+    mp.combine_rows_backward(out, x, position, None, dy, dw)
+    assert torch.equal(dy, x) and torch.equal(dw, out * out)
+    y = torch.zeros(n, 1, dtype=torch.float16, device=dev)
+    mp.gather_rows(x, position.view(-1), y)
+    assert torch.equal(y, x.flip(0))
+    ids = torch.arange(n, device=dev, dtype=torch.int32).remainder_(3)
+    order, back, offsets = mp.route(ids, 3)
+    assert offsets.tolist() == [0, (n + 2) // 3, (n + 2) // 3 + (n + 1) // 3, n]
+    at = torch.arange(n, device=dev, dtype=torch.int32)
+    assert torch.equal(back[order.long()], at) and torch.equal(ids[order.long()], torch.sort(ids).values)
+    assert (order[1:offsets[1]] > order[:offsets[1] - 1]).all()
+
+
 def test_rows_beyond_32_bits():
     """Rows at more than 2^32 bytes, and 2^31 elements, into each operand."""
     dev = device()

@@ -51,6 +51,7 @@ QUANT = dict(x_type=0, T=4, H=8, X=P, ldx=8, order=0, R=4, top_k=1, Q=P, ldq=8, 
     (dict(x_type=3), mp.MPGEMM_ETYPE), (dict(x_type=-1), mp.MPGEMM_ETYPE),
     (dict(T=-1), mp.MPGEMM_EDIM), (dict(H=-1), mp.MPGEMM_EDIM), (dict(R=3), mp.MPGEMM_EDIM),
     (dict(T=1 << 31, R=1 << 31), mp.MPGEMM_EDIM), (dict(order=P, top_k=0), mp.MPGEMM_EDIM),
+    (dict(H=(1 << 28) + 1, ldx=1 << 30, ldq=1 << 30), mp.MPGEMM_EDIM),
     (dict(ldx=7), mp.MPGEMM_ELD), (dict(ldq=7), mp.MPGEMM_ELD), (dict(H=0, ldx=0), mp.MPGEMM_ELD),
     (dict(X=0), mp.MPGEMM_ENULL), (dict(Q=0), mp.MPGEMM_ENULL), (dict(scale=0), mp.MPGEMM_ENULL),
     (dict(X=P + 1), mp.MPGEMM_EALIGN), (dict(x_type=2, X=P + 2), mp.MPGEMM_EALIGN),
@@ -133,7 +134,7 @@ def test_gather_codes(change, expect):
     (1, 64, 2048, 256, 4, 0),                       # few rows
     (1, 16384, 2048, 16384, 8, 0),                  # most pairs have no row
     (3, 1, 1, 1, 1, mp.MPGEMM_ETYPE), (0, -1, 1, 1, 1, mp.MPGEMM_EDIM), (0, 1, 1, 1, 0, mp.MPGEMM_EDIM),
-    (2, (1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 1, 0),
+    (2, (1 << 31) - 1, 1 << 28, (1 << 31) - 1, (1 << 31) - 1, 0), (0, 1, (1 << 28) + 1, 1, 1, mp.MPGEMM_EDIM),
 ])
 def test_rows_workspace(type_, T, H, R, top_k, expect):
     assert mp.mpgemm_rows_workspace(type_, T, H, R, top_k) == expect
