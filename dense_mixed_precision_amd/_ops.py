@@ -262,6 +262,25 @@ def quantize_rows(X, Q, scale, order=None, top_k: int = 1, workspace=None, strea
     return Q, scale
 
 
+def _codes(B, grouped):
+    """(groups, K, N, leading dimension, group stride) of gemm_i8's B."""
+    if not isinstance(B, torch.Tensor) or B.dim() != (3 if grouped else 2):
+        raise ValueError("B must be 2-D, or 3-D with offsets")
+    if not grouped:
+        K, N = B.shape
+        step, ld = B.stride()
+        if step == 1 and ld >= K > 1 and N > 1 and B.dtype is torch.int8 and B.is_cuda:
+            return 1, K, N, ld, 0  # the ordinary case; the rest below
+        B = B.unsqueeze(0)
+    G, K, N, layout, ld, stride = _matrices(B, "B", torch.int8)
+    if layout != MPGEMM_COL_MAJOR:
+        # one value along a dimension: the bytes lie the same in both orders
+        if (K > 1 and N > 1) or (K > 1 and N == 1 and B.stride(1) != 1):
+            raise ValueError("B must be column-major (unit stride along K)")
+        ld = K if K > 1 else B.stride(2) if N > 1 else 1
+    return G, K, N, ld, stride
+
+
 def gemm_i8(A, B, C, scale_a, scale_b, bias=None, offsets=None, stream=None):
     """C <- (A @ B) * scale_a[:, None] * scale_b (+ bias), A and B 8-bit codes,
     the sum exact.  Returns C.
@@ -278,21 +297,7 @@ def gemm_i8(A, B, C, scale_a, scale_b, bias=None, offsets=None, stream=None):
     ot = _type(C, "C")
     M, K, lda = _rows(A, "A", torch.int8)
     M2, N2, ldc = _rows(C, "C", C.dtype)
-    if offsets is None:
-        if not isinstance(B, torch.Tensor) or B.dim() != 2:
-            raise ValueError("B must be 2-D (3-D with offsets)")
-        B = B.unsqueeze(0)
-    G, K2, N, layout, ldw, stride = _matrices(B, "B", torch.int8)
-    if layout != MPGEMM_COL_MAJOR:
-        # one value along a dimension: the bytes lie the same in both orders
-        if K2 > 1 and N > 1:
-            raise ValueError("B must be column-major (unit stride along K)")
-        if K2 <= 1:
-            ldw = B.stride(2) if N > 1 else 1
-        else:  # N <= 1
-            if B.stride(1) != 1 and N == 1:
-                raise ValueError("B must be column-major (unit stride along K)")
-            ldw = K2
+    G, K2, N, ldw, stride = _codes(B, offsets is not None)
     if K2 != K or M2 != M or N2 != N:
         raise ValueError(f"shape mismatch: A {tuple(A.shape)}, B {tuple(B.shape)}, C {tuple(C.shape)}")
     wide = (N,) if offsets is None else (G, N)
@@ -350,7 +355,8 @@ def gather_rows(X, order, Y, top_k: int = 1, workspace=None, stream=None):
     X (T x H) and Y (R x H): float16, bfloat16 or float32, the same, row-major.
     order: int32, R values from :func:`route`; rows whose order is -1 keep
     what they hold.  ``workspace``: a contiguous int32 tensor of
-    mpgemm_rows_workspace bytes, allocated when None and of use.  The gradient by X is ``combine_rows(dY, position, dX)``."""
+    mpgemm_rows_workspace bytes, allocated when None and of use.  The gradient
+    by X is ``combine_rows(dY, position, dX)``."""
     if torch is None:
         _with_torch()
     ty = _type(X, "X")

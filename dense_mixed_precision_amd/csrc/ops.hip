@@ -169,13 +169,20 @@ bool big_tiles_win(int64_t t256, int64_t t128) { return 3 * cdiv(t256, kNumCu) <
 // 36, 128x128 46, 256x256 48).
 bool wide_tiles_win(int64_t twide, int64_t t128) { return 8 * cdiv(twide, kNumCu) <= 5 * cdiv(t128, kNumCu); }
 
+// The narrow kernel's workgroups split K over their waves, which fills more of
+// the chip than the tiles where C is small: up to this many of its 16x16 tiles
+// (8 bits 67x46x7908 6.9 us against 15.5 with 16x64 tiles, 256x256x4096 6.5
+// and 9.1, 24x4096x4096, 512 tiles, 9.9 and 12.1, 219x646x5295, 574, 40 and 19;
+// 16 bits, 500 rows over 4 groups of 128x4096 10.2 and 17.5 with 32x64, 80 rows
+// over 2 of 2048x1024, 768, 9.1 and 7.2).
+constexpr int64_t kNarrowFewTiles = 512;
+
 // Table entry of an 8-bit product, or -1 for the narrow kernel.  By sweeps of
-// every entry (us, graph-replayed, K and N first where one number stands):
+// every entry (us, graph-replayed, M, N, K in order), besides the rules above:
 //   up to 16 rows a group: narrow (8x8192x8192 15.1, 16x64 tiles 15.8;
 //     16x4096x4096 6.4 against 9.3), but 64x128 tiles for 5 rows and more
 //     a group over at least 512 of them (512 rows over 64 experts of
 //     2048x2048 50.2 against 60.9; 64 rows 48.0 narrow against 59);
-//   256x256 and 128x256 by their rounds (above);
 //   128x128 from 192 tiles (512x8192x8192 49.0, 64x128 54.0; 2048^3 15.2
 //     against 16.0; below, 256x8192x8192, 128 tiles, 40.0 against 32.9), with
 //     two ring stages and two workgroups per compute unit where there are
@@ -192,6 +199,8 @@ int select_i8(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t lda, int6
     const int64_t per = cdiv(M, groups);
     auto tiles = [&](int64_t bm, int64_t bn) { return likely_tiles(M, groups, bm, cdiv(N, bn)); };
     auto fits = [&](int id) { return i8_fits(kI8Table[id], lda, ldw, K); };
+    if (tiles(16, 16) <= kNarrowFewTiles)
+        return -1;
     if (per <= 16)
         return per > 4 && groups > 1 && tiles(64, 128) >= 512 && fits(kI8Half) ? kI8Half : -1;
     if (per > 128 && N > 128 && big_tiles_win(tiles(256, 256), tiles(128, 128)) && fits(kI8Big))
@@ -310,7 +319,7 @@ int select_grouped(const GroupedEntry *table, int lb, int64_t groups, int64_t R,
     const int64_t per = cdiv(R, groups);
     auto tiles = [&](int64_t bm, int64_t bn) { return likely_tiles(R, groups, bm, cdiv(N, bn)); };
     auto fits = [&](int id) { return grouped_fits(table[id], kRowMajor, lb, lda, ldb, ldc); };
-    if (per <= 16 && lb == kColMajor && (per <= 4 || tiles(32, 64) < 512))
+    if (lb == kColMajor && (tiles(16, 16) <= kNarrowFewTiles || (per <= 16 && (per <= 4 || tiles(32, 64) < 512))))
         return -1;
     if (per > 64 && N > 128) {
         if (per > 128 && big_tiles_win(tiles(256, 256), tiles(128, 128)) && fits(kGroupedBig))

@@ -243,6 +243,33 @@ def test_i8_empty(M, N, K):
     check_i8(M, N, K, torch.float32)
 
 
+def test_i8_views_of_weights():
+    """Weights as a user may hold them: one row, one column, one value, a slice
+    of wider rows, and what is refused."""
+    dev = device()
+    g = torch.Generator().manual_seed(6)
+    big = torch.randint(-9, 10, (40, 64), generator=g, dtype=torch.int8).to(dev)
+    a = torch.randint(-9, 10, (7, 64), generator=g, dtype=torch.int8).to(dev)
+
+    def run(a, w):  # w: K x N view
+        out = torch.empty(a.shape[0], w.shape[1], device=dev)
+        one = torch.ones(64, device=dev)
+        mp.gemm_i8(a, w, out, one[:a.shape[0]], one[:w.shape[1]])
+        assert torch.equal(out.double().cpu(), a.double().cpu() @ w.double().cpu())
+
+    run(a, big.t())
+    run(a, big[:1].t())
+    run(a, big[3].view(64, 1))
+    run(a[:, :1].contiguous(), big[:, :1].t())
+    run(a[:, :1].contiguous(), big[:1, :1])
+    run(a[:, :33].contiguous(), big[5:25, 10:43].t())
+    run(a[:, :33], big[5:25, 10:43].t())
+    run(a[:, :0].contiguous(), big[:, :0].t())
+    for bad in (big.t().contiguous(), big[:, ::2].t(), big.float().t(), big[:, :1].expand(40, 64).t(), big.cpu().t(), None):
+        with pytest.raises((ValueError, TypeError)):
+            mp.gemm_i8(a, bad, torch.empty(7, 40, device=dev), torch.ones(7, device=dev), torch.ones(40, device=dev))
+
+
 def test_i8_largest_sum():
     """Every code -128 at the largest K: the sum is 131071 * 2^14."""
     check_i8(3, 18, mp.MPGEMM_I8_MAX_K, torch.float32, extremes=True, bias=False)
