@@ -166,8 +166,13 @@ bool big_tiles_win(int64_t t256, int64_t t128) { return 3 * cdiv(t256, kNumCu) <
 
 // A round of 128x256 tiles takes 1.5 to 1.8 times as long as one of 128x128
 // (16-bit, 8192 rows over 32 experts 91, 128x128 124; 8-bit 2048x4096x4096
-// 36, 128x128 46, 256x256 48).
-bool wide_tiles_win(int64_t twide, int64_t t128) { return 8 * cdiv(twide, kNumCu) <= 5 * cdiv(t128, kNumCu); }
+// 36, 128x128 46, 256x256 48).  At short K it is the writing of C, where two
+// 128x128 tiles a unit do better (K = 512, 6560 rows over 82 experts of 1379:
+// 16-bit 31 against 39, 8-bit 27 against 30).
+bool wide_tiles_win(int64_t twide, int64_t t128, int64_t K)
+{
+    return K > 512 && 8 * cdiv(twide, kNumCu) <= 5 * cdiv(t128, kNumCu);
+}
 
 // The narrow kernel's workgroups split K over their waves, which fills more of
 // the chip than the tiles where C is small: up to this many of its 16x16 tiles
@@ -205,7 +210,7 @@ int select_i8(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t lda, int6
         return per > 4 && groups > 1 && tiles(64, 128) >= 512 && fits(kI8Half) ? kI8Half : -1;
     if (per > 128 && N > 128 && big_tiles_win(tiles(256, 256), tiles(128, 128)) && fits(kI8Big))
         return kI8Big;
-    if (per > 64 && N > 128 && wide_tiles_win(tiles(128, 256), tiles(128, 128)) && fits(kI8Wide))
+    if (per > 64 && N > 128 && wide_tiles_win(tiles(128, 256), tiles(128, 128), K) && fits(kI8Wide))
         return kI8Wide;
     if (per > 64 && tiles(128, 128) >= 192 && fits(kI8Mid))
         return tiles(128, 128) > kNumCu || K <= 512 ? kI8Two : kI8Mid;
@@ -324,7 +329,7 @@ int select_grouped(const GroupedEntry *table, int lb, int64_t groups, int64_t R,
     if (per > 64 && N > 128) {
         if (per > 128 && big_tiles_win(tiles(256, 256), tiles(128, 128)) && fits(kGroupedBig))
             return kGroupedBig;
-        if (wide_tiles_win(tiles(128, 256), tiles(128, 128)) && fits(kGroupedWide))
+        if (wide_tiles_win(tiles(128, 256), tiles(128, 128), K) && fits(kGroupedWide))
             return kGroupedWide;
     }
     if (per > 64 && tiles(128, 128) >= kNumCu / 2 && fits(kGroupedMid))
@@ -347,7 +352,7 @@ int select_wgrad(const GroupedEntry *table, int64_t groups, int64_t R, int64_t M
     if (cdiv(R, groups) > 128) {
         if (M > 128 && N > 128 && big_tiles_win(tiles(256, 256), tiles(128, 128)) && fits(kGroupedBig))
             return kGroupedBig;
-        if (N > 128 && wide_tiles_win(tiles(128, 256), tiles(128, 128)) && fits(kGroupedWide))
+        if (N > 128 && wide_tiles_win(tiles(128, 256), tiles(128, 128), cdiv(R, groups)) && fits(kGroupedWide))
             return kGroupedWide;
     }
     return tiles(128, 128) >= kNumCu / 2 && fits(kGroupedTwo) ? kGroupedTwo : kWgradSmall;
@@ -379,9 +384,13 @@ void launch_fill(int32_t *v, int64_t count, hipStream_t s)
 template <int XT>
 void launch_quantize(mpg::QuantArgs a, int32_t *inverse, hipStream_t s)
 {
-    // One wave per row where there are rows for every wave slot and a wave
-    // holds a row in 8 vectors per lane; else one workgroup per row.
-    constexpr int64_t kWaveRow = 64 * 8 * (XT == mpg::kTF32 ? 4 : 8);
+    // 16 lanes per row that they hold in 2 vectors each; in 8 where there are
+    // rows for every wave slot at four a wave; a wave where it holds the row
+    // in 8 and there are rows for every slot; else one workgroup (BF16, us:
+    // 131072 rows of 35 values 13.2 by 16 lanes with 2 vectors, 18.3 with 8,
+    // 63.6 by 64; 65536 of 600 24.7 and 40.1, 2048 of 600 4.4 and 3.5).
+    constexpr int64_t VN = XT == mpg::kTF32 ? 4 : 8;
+    constexpr int64_t kWaveRow = 64 * 8 * VN;
     if (inverse) {
         launch_fill(inverse, (int64_t)a.T * a.top_k, s);
         hipLaunchKernelGGL((mpg::quantize_invert<XT>), row_grid(cdiv(a.R, 256)), dim3(256), 0, s, a, inverse);
@@ -392,21 +401,40 @@ void launch_quantize(mpg::QuantArgs a, int32_t *inverse, hipStream_t s)
             hipLaunchKernelGGL((mpg::quantize_rows<XT, 256, 4, true>), row_grid(a.T), dim3(256), 0, s, a);
         return;
     }
-    if (a.R >= 8 * kNumCu && a.H <= kWaveRow)
+    if (a.H <= 16 * 2 * VN)
+        hipLaunchKernelGGL((mpg::quantize_rows<XT, 16, 2>), row_grid(cdiv(a.R, 16)), dim3(256), 0, s, a);
+    else if (a.R >= 32 * kNumCu && a.H <= 16 * 8 * VN)
+        hipLaunchKernelGGL((mpg::quantize_rows<XT, 16, 8>), row_grid(cdiv(a.R, 16)), dim3(256), 0, s, a);
+    else if (a.R >= 8 * kNumCu && a.H <= kWaveRow)
         hipLaunchKernelGGL((mpg::quantize_rows<XT, 64, 8>), row_grid(cdiv(a.R, 4)), dim3(256), 0, s, a);
     else
         hipLaunchKernelGGL((mpg::quantize_rows<XT, 256, 4>), row_grid(a.R), dim3(256), 0, s, a);
 }
 
+// One vector a lane: 16 or 64 lanes per token where they hold its row (16384
+// tokens of 8 slots and 35 FP32 values 7.0 us, by 256 threads 22.5).
+template <int YT, int OT>
+void launch_combine(const mpg::CombineArgs &a, hipStream_t s)
+{
+    constexpr int64_t VN = YT == mpg::kTF32 ? 4 : 8;
+    const int64_t z = cdiv(a.H, 256 * VN);
+    if (a.H <= 16 * VN)
+        hipLaunchKernelGGL((mpg::combine_rows<YT, OT, 16>), row_grid(cdiv(a.T, 16)), dim3(256), 0, s, a);
+    else if (a.H <= 64 * VN)
+        hipLaunchKernelGGL((mpg::combine_rows<YT, OT, 64>), row_grid(cdiv(a.T, 4)), dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((mpg::combine_rows<YT, OT, 256>), row_grid(a.T, z < 65535 ? z : 65535), dim3(256), 0, s, a);
+}
+
 template <int YT>
-void launch_combine(int o_type, const mpg::CombineArgs &a, dim3 grid, hipStream_t s)
+void launch_combine(int o_type, const mpg::CombineArgs &a, hipStream_t s)
 {
     if (o_type == MPGEMM_T_F16)
-        hipLaunchKernelGGL((mpg::combine_rows<YT, mpg::kTF16>), grid, dim3(256), 0, s, a);
+        launch_combine<YT, mpg::kTF16>(a, s);
     else if (o_type == MPGEMM_T_BF16)
-        hipLaunchKernelGGL((mpg::combine_rows<YT, mpg::kTBF16>), grid, dim3(256), 0, s, a);
+        launch_combine<YT, mpg::kTBF16>(a, s);
     else
-        hipLaunchKernelGGL((mpg::combine_rows<YT, mpg::kTF32>), grid, dim3(256), 0, s, a);
+        launch_combine<YT, mpg::kTF32>(a, s);
 }
 
 // Rows of up to 256 values: 16 lanes per pair (78743 pairs of 119 values,
@@ -670,7 +698,12 @@ int mpgemm_gather_rows(int type, int64_t T, int64_t H, const void *X, int64_t ld
         hipLaunchKernelGGL(mpg::gather_invert, row_grid(cdiv(R, 256)), dim3(256), 0, stream_of(stream), a, inverse);
         hipLaunchKernelGGL(mpg::gather_tokens, row_grid(cdiv(T, 4)), dim3(256), 0, stream_of(stream), a, inverse);
     } else {
-        hipLaunchKernelGGL(mpg::gather_rows, row_grid(cdiv(R, 4)), dim3(256), 0, stream_of(stream), a);
+        // rows of up to 512 bytes by 16 lanes (131072 rows of 35 BF16 values 8.5
+        // us, by 64 lanes 24.8)
+        if (a.row_bytes <= 512)
+            hipLaunchKernelGGL(mpg::gather_rows<16>, row_grid(cdiv(R, 16)), dim3(256), 0, stream_of(stream), a);
+        else
+            hipLaunchKernelGGL(mpg::gather_rows<64>, row_grid(cdiv(R, 4)), dim3(256), 0, stream_of(stream), a);
     }
     return launched();
 }
@@ -692,15 +725,13 @@ int mpgemm_combine_rows(int y_type, int o_type, int64_t T, int64_t top_k, int64_
     if (!aligned(Y, size_of(y_type)) || !aligned(O, size_of(o_type)) || !aligned(position, 4) || !aligned(weights, 4))
         return MPGEMM_EALIGN;
     const mpg::CombineArgs a{Y, O, position, weights, ldy, ldo, (int32_t)T, (int32_t)H, (int32_t)R, (int32_t)top_k};
-    const int64_t gz = cdiv(H, y_type == MPGEMM_T_F32 ? 1024 : 2048);
-    const dim3 grid = row_grid(T, gz < 65535 ? gz : 65535);
     forget_error();
     if (y_type == MPGEMM_T_F16)
-        launch_combine<mpg::kTF16>(o_type, a, grid, stream_of(stream));
+        launch_combine<mpg::kTF16>(o_type, a, stream_of(stream));
     else if (y_type == MPGEMM_T_BF16)
-        launch_combine<mpg::kTBF16>(o_type, a, grid, stream_of(stream));
+        launch_combine<mpg::kTBF16>(o_type, a, stream_of(stream));
     else
-        launch_combine<mpg::kTF32>(o_type, a, grid, stream_of(stream));
+        launch_combine<mpg::kTF32>(o_type, a, stream_of(stream));
     return launched();
 }
 

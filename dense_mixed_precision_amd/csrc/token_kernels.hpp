@@ -124,7 +124,8 @@ struct QuantArgs {
 // NT threads per row, 256 / NT rows per workgroup.  The first CACHE vectors
 // of each thread stay in registers between the maximum and the codes; longer
 // rows are read again.  With NT = 64 a row is one wave's: no barrier, and the
-// 32 waves of a compute unit keep as many rows in flight.
+// 32 waves of a compute unit keep as many rows in flight; with NT = 16 a wave
+// has four short ones.
 // TOKENS: a row is a token's, read and coded once and written to each row of
 // Q that one of its pairs has (see invert_order).
 template <int XT, int NT, int CACHE, bool TOKENS = false>
@@ -137,7 +138,7 @@ quantize_rows(QuantArgs args)
     __shared__ uint32_t part[4];
     const int tid = threadIdx.x % NT;
     const int64_t row = wg_number() * (256 / NT) +
-                        (NT == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : 0);
+                        (NT == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : (int)threadIdx.x / NT);
     if (row >= (TOKENS ? args.T : args.R))
         return;
     int64_t src = row;
@@ -178,7 +179,7 @@ quantize_rows(QuantArgs args)
     for (int i = nv * VN + tid; i < H; i += NT)
         see(x[i]);
 #pragma unroll
-    for (int d = 32; d > 0; d /= 2) {
+    for (int d = (NT < 64 ? NT : 64) / 2; d > 0; d /= 2) {
         const uint32_t o = __shfl_xor((int)top, d);
         top = o > top ? o : top;
     }
@@ -514,12 +515,14 @@ struct GatherArgs {
     int32_t row_bytes;
 };
 
-// Y[p] = X[order[p] / top_k]: one wave per row.
+// Y[p] = X[order[p] / top_k]: LANES lanes per row (64, or 16 for short rows).
+template <int LANES>
 __global__ void __launch_bounds__(256)
 gather_rows(GatherArgs a)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t p = wg_number() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x % LANES;
+    const int sub = threadIdx.x / LANES;
+    const int64_t p = wg_number() * (256 / LANES) + (LANES == 64 ? __builtin_amdgcn_readfirstlane(sub) : sub);
     if (p >= a.R)
         return;
     const int pair = a.order[p];
@@ -529,19 +532,20 @@ gather_rows(GatherArgs a)
     const uint8_t *const x = a.X + (int64_t)t * a.ldx;
     uint8_t *const y = a.Y + p * a.ldy;
     const int nv = a.row_bytes / 16;
-    // 4 KiB at a time: the loads first, so that they are in flight together
-    for (int i0 = lane; i0 < nv; i0 += 256) {
+    // 4 vectors a lane at a time: the loads first, so that they are in flight
+    // together
+    for (int i0 = lane; i0 < nv; i0 += 4 * LANES) {
         u32x4 v[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-            if (i0 + 64 * c < nv)
-                v[c] = *(const u32x4_any *)(x + (int64_t)(i0 + 64 * c) * 16);
+            if (i0 + LANES * c < nv)
+                v[c] = *(const u32x4_any *)(x + (int64_t)(i0 + LANES * c) * 16);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-            if (i0 + 64 * c < nv)
-                *(u32x4_any *)(y + (int64_t)(i0 + 64 * c) * 16) = v[c];
+            if (i0 + LANES * c < nv)
+                *(u32x4_any *)(y + (int64_t)(i0 + LANES * c) * 16) = v[c];
     }
-    for (int i = nv * 16 + lane; i < a.row_bytes; i += 64)
+    for (int i = nv * 16 + lane; i < a.row_bytes; i += LANES)
         y[i] = x[i];
 }
 
@@ -608,10 +612,10 @@ struct CombineArgs {
 
 // O[t] = sum_s weights[t][s] * Y[position[t][s]], in FP32, slots ascending
 // (HBM; 33 tokens of 8 slots and 2048 values 3.9 us, a launch and two trips to
-// memory);
-// one thread per 16 bytes of a row of Y.  Four slots' rows are loaded before the
-// first is used.
-template <int YT, int OT>
+// memory); one thread per 16 bytes of a row of Y, LANES threads per token (256
+// and as many workgroups as the row needs, or 64 or 16 for short rows).  Four
+// slots' rows are loaded before the first is used.
+template <int YT, int OT, int LANES>
 __global__ void __launch_bounds__(256)
 combine_rows(CombineArgs a)
 {
@@ -619,11 +623,13 @@ combine_rows(CombineArgs a)
     typedef typename ElemOf<OT>::type EO;
     constexpr int VN = VecOf<EY>::N;
     typedef typename VecOf<EY>::type V;
-    const int64_t t = wg_number();
+    const int lane = threadIdx.x % LANES;
+    const int sub = threadIdx.x / LANES;
+    const int64_t t = wg_number() * (256 / LANES) + (LANES == 16 ? sub : __builtin_amdgcn_readfirstlane(sub));
     if (t >= a.T)
         return;
     const int32_t *const at = a.position + t * a.top_k;
-    for (int64_t c = (int64_t)VN * (blockIdx.z * 256 + threadIdx.x); c < a.H; c += (int64_t)VN * 256 * gridDim.z) {
+    for (int64_t c = (int64_t)VN * (blockIdx.z * LANES + lane); c < a.H; c += (int64_t)VN * LANES * gridDim.z) {
         const int left = (int)(a.H - c);
         float acc[VN];
 #pragma unroll

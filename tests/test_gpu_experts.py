@@ -95,7 +95,8 @@ def test_route_graph():
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("T,k,E,H,gap,shift", [(1, 1, 1, 1, 0, 0), (5, 2, 3, 7, 1, 1), (33, 8, 64, 256, 0, 0),
-                                               (20, 3, 4, 1025, 3, 1), (9, 2, 5, 2048, 0, 0), (4, 2, 3, 0, 0, 0)])
+                                               (20, 3, 4, 1025, 3, 1), (9, 2, 5, 2048, 0, 0), (4, 2, 3, 0, 0, 0),
+                                               (40, 2, 5, 128, 0, 0), (21, 2, 5, 129, 1, 0)])
 def test_gather_rows(dtype, T, k, E, H, gap, shift):
     ids = make_ids(T, k, E, T + H, drop=0.2)
     order, _, offsets = mp.route(ids.to(device()), E)
@@ -163,6 +164,7 @@ def combine_exact(y, position, w, T, H):
 @pytest.mark.parametrize("yt", DTYPES)
 @pytest.mark.parametrize("ot", DTYPES)
 @pytest.mark.parametrize("T,k,E,H,gap,shift", [(1, 1, 1, 1, 0, 0), (6, 2, 3, 7, 1, 1), (17, 8, 64, 256, 0, 0),
+                                               (33, 5, 4, 64, 0, 0), (18, 3, 4, 129, 1, 0), (7, 9, 4, 513, 0, 1),
                                                (5, 3, 4, 2051, 2, 1)])
 def test_combine_rows(yt, ot, T, k, E, H, gap, shift):
     g = torch.Generator().manual_seed(T + H)

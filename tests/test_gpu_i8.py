@@ -56,7 +56,9 @@ def check_quantize(x, dtype, gap=0, shift=0, order=None, top_k=1, rows=None):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("T,H,gap,shift", [(1, 1, 0, 0), (3, 7, 1, 1), (5, 64, 0, 0), (2, 2048, 0, 0), (4, 2049, 3, 1),
-                                           (3, 8192, 0, 0), (2, 20000, 5, 1), (130, 96, 0, 0), (4, 0, 0, 0)])
+                                           (3, 8192, 0, 0), (2, 20000, 5, 1), (130, 96, 0, 0), (4, 0, 0, 0),
+                                           (17, 128, 0, 0), (18, 256, 1, 1), (17, 257, 0, 0), (8200, 300, 1, 1),
+                                           (8192, 1024, 0, 0), (2050, 1025, 0, 1), (2049, 4096, 0, 0)])
 def test_quantize_sizes(dtype, T, H, gap, shift):
     g = torch.Generator().manual_seed(T * 7919 + H)
     check_quantize(torch.randn(T, H, generator=g) * torch.exp(2 * torch.randn(T, 1, generator=g)), dtype, gap, shift)
