@@ -95,7 +95,7 @@ int mpgemm_quantize_rows(int x_type, int64_t T, int64_t H, const void *X, int64_
  * offsets NULL: one product, groups must be 1.  Otherwise rows offsets[g] ..
  * offsets[g+1]-1 of A and C use the weights at W + g*stride_w and row g of
  * scale_w and bias (groups x N, contiguous).
- * K <= MPGEMM_I8_MAX_K; M and N below 2^31; 16 rows of A, W or C within 2 GiB
+ * K <= MPGEMM_I8_MAX_K; M and N below 2^31; 16 rows of A and of W within 2 GiB
  * (else MPGEMM_ELD).
  */
 int mpgemm_i8_gemm(int out_type, int64_t groups, int64_t M, int64_t N, int64_t K,

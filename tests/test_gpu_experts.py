@@ -326,9 +326,17 @@ def test_grouped_shapes(col, N, K, gap, shift):
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("col", [False, True])
 def test_grouped_every_tile_size(dtype, col):
-    """Sizes at which the 128x128 and 256x256 tiles and the narrow kernel are
-    chosen, with ragged edges in every direction."""
+    """Sizes at which each tile size and the narrow kernel are chosen, with
+    ragged edges in every direction, C in whole lines and not."""
     check_grouped([1, 700, 0, 1299, 490], 2500, 1100, 77, dtype, col)
+    check_grouped([300, 700, 0, 1299, 190], 2500, 2048, 530, dtype, col)
+    check_grouped([300, 700, 0, 1299, 190], 2500, 2041, 530, dtype, col)
+    check_grouped([230] * 13, 3000, 800, 300, dtype, col, gap=1)
+    check_grouped([700, 900, 0, 899], 2500, 2048, 40, dtype, col)
+    check_grouped([4000, 4900], 9000, 1024, 69, dtype, col)
+    check_grouped([60] * 20, 1200, 1100, 100, dtype, col)
+    check_grouped([9] * 70, 630, 515, 100, dtype, col)
+    check_grouped([2] * 90, 180, 1030, 100, dtype, col)
     check_grouped([1, 4000, 0, 5, 4901], 9000, 1100, 69, dtype, col, beta=0.5)
     check_grouped([1, 9, 0, 16, 17], 50, 300, 1003, dtype, col, alpha=0.5, beta=2.0, gap=1, shift=1)
 
@@ -371,6 +379,11 @@ def test_grouped_edges_of_stored_rows(dtype, K, N):
 def test_wgrad_every_tile_size(dtype):
     check_wgrad([100, 0, 37, 1], 140, 900, 1100, dtype)
     check_wgrad([30, 7, 0], 40, 2200, 3300, dtype, beta=0.5)
+    check_wgrad([30, 7, 0], 40, 2048, 2048, dtype)
+    check_wgrad([700, 400], 1100, 2000, 2048, dtype)
+    check_wgrad([700, 400], 1100, 2001, 2043, dtype)
+    check_wgrad([70, 0, 400], 470, 2300, 4096, dtype)
+    check_wgrad([70, 0, 400], 470, 2300, 4097, dtype, beta=1.0)
 
 
 def test_grouped_scalars_and_empty():

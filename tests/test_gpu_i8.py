@@ -214,9 +214,11 @@ def test_i8_sizes(dtype, M, N, K):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("M,N,K,gap", [(1500, 1400, 200, 0), (2600, 4100, 141, 0), (2570, 4353, 300, 3),
-                                       (16, 4100, 1000, 0), (12, 300, 5001, 1)])
+                                       (16, 4100, 1000, 0), (12, 300, 5001, 1), (2040, 4000, 600, 0), (1700, 2000, 700, 1),
+                                       (1200, 4400, 130, 1), (1100, 1101, 200, 0), (500, 1000, 333, 2), (300, 1000, 400, 0),
+                                       (16, 16400, 520, 0)])
 def test_i8_every_tile_size(dtype, M, N, K, gap):
-    """Sizes at which the 128x128 and 256x256 tiles and the narrow kernel are
+    """Sizes at which each tile size and the narrow kernel's two forms are
     chosen, with ragged edges in every direction."""
     check_i8(M, N, K, dtype, gap=gap)
 
@@ -224,6 +226,8 @@ def test_i8_every_tile_size(dtype, M, N, K, gap):
 def test_i8_groups_every_tile_size():
     check_i8(2500, 1100, 200, torch.bfloat16, sizes=[1, 700, 0, 1299, 490])
     check_i8(9000, 1100, 133, torch.float32, sizes=[1, 4000, 0, 5, 4901], gap=1)
+    check_i8(2500, 2040, 600, torch.float32, sizes=[300, 700, 0, 1299, 190])
+    check_i8(800, 1030, 300, torch.float16, sizes=[8] * 99 + [7])
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
