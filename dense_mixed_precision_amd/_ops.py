@@ -183,6 +183,11 @@ def _matrices(t, name, dtype):
     return groups, rows, cols, layout, ld, (sg if groups > 1 else 0)
 
 
+def _check_workspace(t):
+    if t is not None and (not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or not t.is_contiguous()):
+        raise TypeError("workspace must be a contiguous int32 tensor on the GPU")
+
+
 def _on(stream, *tensors):
     """(device index, stream handle) of a call: every tensor on one GPU, the
     launch on that GPU's current stream or the one given."""
@@ -214,8 +219,6 @@ def _workspace(on, stream, given, need):
     """(pointer, bytes, tensor) of a workspace: the caller's, or one of `need`
     bytes allocated here."""
     if given is not None:
-        if not isinstance(given, torch.Tensor) or given.dtype is not torch.int32 or not given.is_contiguous():
-            raise TypeError("workspace must be a contiguous int32 tensor on the GPU")
         return given.data_ptr(), 4 * given.numel(), given
     if need <= 0:
         return 0, 0, None
@@ -248,6 +251,7 @@ def quantize_rows(X, Q, scale, order=None, top_k: int = 1, workspace=None, strea
     use."""
     if torch is None:
         _with_torch()
+    _check_workspace(workspace)
     xt = _type(X, "X")
     T, H, ldx = _rows(X, "X", X.dtype)
     R, H2, ldq = _rows(Q, "Q", torch.int8)
@@ -324,6 +328,7 @@ def route(experts, num_experts: int, out=None, workspace=None, stream=None):
     mpgemm_route_workspace bytes; allocated when None and needed."""
     if torch is None:
         _with_torch()
+    _check_workspace(workspace)
     if not isinstance(experts, torch.Tensor) or experts.dtype not in (torch.int32, torch.int64):
         raise TypeError("experts must be an int32 or int64 tensor")
     if not experts.is_cuda or not experts.is_contiguous():
@@ -335,14 +340,14 @@ def route(experts, num_experts: int, out=None, workspace=None, stream=None):
     given = () if out is None else tuple(out)
     if out is not None and len(given) != 3:
         raise ValueError("out must be (order, position, offsets)")
-    on = _on(stream, experts, workspace, *given)
-    wp, wb, _ws = _workspace(on, stream, workspace, need)
     if given:
         order, position, offsets = given
         _flat(order, "order", torch.int32, (pairs,))
         _flat(position, "position", torch.int32, experts.shape)
         _flat(offsets, "offsets", torch.int32, (E + 1,))
-    else:
+    on = _on(stream, experts, workspace, *given)
+    wp, wb, _ws = _workspace(on, stream, workspace, need)
+    if not given:
         order, position, offsets = _new(on, stream, pairs, experts.shape, E + 1)
     _call(load_ops().mpgemm_route, on, MPGEMM_ID_I64 if experts.dtype == torch.int64 else MPGEMM_ID_I32, pairs, E,
           experts.data_ptr(), order.data_ptr(), position.data_ptr(), offsets.data_ptr(), wp, wb)
@@ -359,6 +364,7 @@ def gather_rows(X, order, Y, top_k: int = 1, workspace=None, stream=None):
     by X is ``combine_rows(dY, position, dX)``."""
     if torch is None:
         _with_torch()
+    _check_workspace(workspace)
     ty = _type(X, "X")
     T, H, ldx = _rows(X, "X", X.dtype)
     R, H2, ldy = _rows(Y, "Y", X.dtype)

@@ -25,7 +25,7 @@
 //  * scales and bias wait in LDS behind the ring, and C leaves in whole
 //    128-byte lines.
 // Bound: the matrix cores at the board's power limit for large products (8192^3
-// to FP32 452-467 us, 2.4e15 operations/s, matrix pipes busy 60% of the time at
+// to FP32 452-471 us, 2.3e15-2.4e15 operations/s, matrix pipes busy 60% of the time at
 // 1.84 GHz, no LDS bank conflicts); between rounds of tiles the first copies
 // and the stores show (8192x8192x2048 to BF16 133 us, of which about 40 are not
 // products), and with experts of unequal sizes the last round is part empty

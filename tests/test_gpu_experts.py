@@ -74,6 +74,21 @@ def test_route_out_workspace_stream():
         mp.route(ids, 33, workspace=ws[:10])
 
 
+def test_route_refuses_wrong_out():
+    ids = make_ids(3, 2, 4, 1).to(device())
+    good = [torch.empty(n, dtype=torch.int32, device=device()) for n in ((6,), (3, 2), (5,))]
+    for i, wrong, error in ((0, None, TypeError), (1, [0] * 6, TypeError), (2, good[2].float(), TypeError),
+                            (1, good[0], ValueError), (2, good[2][:4], ValueError), (0, good[0].cpu(), ValueError)):
+        out = list(good)
+        out[i] = wrong
+        with pytest.raises(error):
+            mp.route(ids, 4, out=out)
+    with pytest.raises(ValueError):
+        mp.route(ids, 4, out=good[:2])
+    with pytest.raises(ValueError):
+        mp.route(ids, 4, workspace=torch.zeros(64, dtype=torch.int32))
+
+
 def test_route_graph():
     for T in (100, 3000):
         ids = make_ids(T, 4, 33, 2).to(device())

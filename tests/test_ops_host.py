@@ -228,6 +228,17 @@ def test_tensor_checks(fn, args, error):
         fn(*args)
 
 
+@pytest.mark.parametrize("workspace", ["no tensor", [0, 0], t(8), t(8, 2, dtype=torch.int32).t()])
+@pytest.mark.parametrize("fn,args", [
+    (mp.quantize_rows, (t(2, 4), t(2, 4, dtype=torch.int8), t(2))),
+    (mp.route, (t(2, 2, dtype=torch.int32), 4)),
+    (mp.gather_rows, (t(2, 4), t(2, dtype=torch.int32), t(2, 4))),
+])
+def test_workspace_is_checked_first(fn, args, workspace):
+    with pytest.raises(TypeError, match="workspace"):
+        fn(*args, workspace=workspace)
+
+
 @pytest.fixture(scope="module")
 def device_asm(tmp_path_factory):
     if shutil.which("hipcc") is None and not os.path.exists("/opt/rocm/bin/hipcc"):
