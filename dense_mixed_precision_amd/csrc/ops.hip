@@ -32,6 +32,8 @@ using mpg::PipeCfg;
 constexpr int kNumCu = 256;
 constexpr int64_t kMax32 = 0x7FFFFFFF;
 constexpr int64_t kMaxWidth = (int64_t)1 << 28;  // values of a token's row: a row spans at most 1 GiB
+// slots of a token: the kernels that walk them in runs of 4 or 8 count in 32 bits
+constexpr int64_t kMaxSlots = (int64_t)1 << 30;
 constexpr int64_t kMaxSpan = 0x7FFFFFF0;  // bytes a 32-bit buffer offset may reach
 
 int64_t at_least_one(int64_t v) { return v > 1 ? v : 1; }
@@ -371,7 +373,8 @@ constexpr int64_t kByTokensBytes = (int64_t)64 << 20;
 int64_t inverse_bytes(int64_t T, int64_t R, int64_t top_k, int64_t row_bytes)
 {
     const int64_t pairs = mul_sat(T, top_k);
-    return top_k >= 2 && pairs <= 2 * R && pairs <= kMax32 && mul_sat(R, row_bytes) >= kByTokensBytes ? 4 * pairs : 0;
+    const bool fits = top_k >= 2 && top_k <= kMaxSlots && pairs <= 2 * R && pairs <= kMax32;
+    return fits && mul_sat(R, row_bytes) >= kByTokensBytes ? 4 * pairs : 0;
 }
 
 void launch_fill(int32_t *v, int64_t count, hipStream_t s)
@@ -714,7 +717,7 @@ int mpgemm_combine_rows(int y_type, int o_type, int64_t T, int64_t top_k, int64_
 {
     if (!is_type(y_type) || !is_type(o_type))
         return MPGEMM_ETYPE;
-    if (T < 0 || H < 0 || R < 0 || top_k < 0 || T > kMax32 || H > kMaxWidth || R > kMax32 || top_k > kMax32)
+    if (T < 0 || H < 0 || R < 0 || top_k < 0 || T > kMax32 || H > kMaxWidth || R > kMax32 || top_k > kMaxSlots)
         return MPGEMM_EDIM;
     if (ldy < at_least_one(H) || ldo < at_least_one(H))
         return MPGEMM_ELD;

@@ -148,7 +148,7 @@ int64_t mpgemm_rows_workspace(int type, int64_t T, int64_t H, int64_t R, int64_t
  * in FP32, slots ascending, rounded once to o_type.  Y: R x H of y_type, O:
  * T x H, position and weights (FP32; NULL: all 1) T x top_k, contiguous.  A
  * pair without a position adds nothing; a token without any has a row of
- * zeros.
+ * zeros.  top_k at most 2^30.
  */
 int mpgemm_combine_rows(int y_type, int o_type, int64_t T, int64_t top_k, int64_t H, int64_t R,
                         const void *Y, int64_t ldy, const int32_t *position, const float *weights,
