@@ -29,8 +29,9 @@ torch = None
 def _with_torch():
     global torch, _TYPES
     import torch as module
+    # torch last: another thread's first call takes its presence for all of this
+    _TYPES = {module.float16: MPGEMM_T_F16, module.bfloat16: MPGEMM_T_BF16, module.float32: MPGEMM_T_F32}
     torch = module
-    _TYPES = {torch.float16: MPGEMM_T_F16, torch.bfloat16: MPGEMM_T_BF16, torch.float32: MPGEMM_T_F32}
 
 
 def load_ops():

@@ -1,8 +1,11 @@
 """Host-side tests of the operator library at its edges (no GPU): slots a
-token beyond what the kernels' counters hold."""
+token beyond what the kernels' counters hold, first calls on several threads."""
+import sys
+
 import pytest
 
 import dense_mixed_precision_amd as mp
+from dense_mixed_precision_amd import _ops
 from tests.test_ops_host import COMBINE, call
 
 MOST = 1 << 30  # slots a token; mpgemm_route makes no more pairs
@@ -22,3 +25,27 @@ def test_way_by_tokens_limits_the_slots():
     assert mp.mpgemm_rows_workspace(mp.MPGEMM_T_F16, 1, 4096, rows, MOST) == 4 * MOST
     assert mp.mpgemm_rows_workspace(mp.MPGEMM_T_F16, 1, 4096, rows, MOST + 1) == 0
     assert mp.mpgemm_rows_workspace(mp.MPGEMM_T_F16, 1, 4096, rows, rows) == 0
+
+
+def test_first_call_publishes_nothing_half_made(monkeypatch):
+    """Entry points test `torch is None` alone: whatever line of the first
+    call's preparation another thread comes in at, torch is there only with
+    the table of its types complete."""
+    monkeypatch.setattr(_ops, "torch", None)
+    monkeypatch.setattr(_ops, "_TYPES", {})
+    seen = []
+
+    def trace(frame, event, arg):
+        if frame.f_code is not _ops._with_torch.__code__:
+            return None
+        seen.append((_ops.torch is not None, len(_ops._TYPES)))
+        return trace
+
+    before = sys.gettrace()
+    sys.settrace(trace)
+    try:
+        _ops._with_torch()
+    finally:
+        sys.settrace(before)
+    assert seen[0] == (False, 0) and seen[-1] == (True, 3)
+    assert all(types == 3 for there, types in seen if there)
