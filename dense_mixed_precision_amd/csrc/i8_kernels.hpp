@@ -4,9 +4,9 @@
 //     C[i][j] = (float)(sum_k A[i][k] * W[j][k]) * scale_a[i] * scale_w[j] (+ bias[j])
 //
 // A: tokens x K codes, W: channels x K codes (both K-contiguous), the sum
-// exact in 32-bit integers, rounded once to FP32 before the scales and once
-// more to the output type.  With groups, token rows [offsets[g],
-// offsets[g+1]) use W[g], scale_w[g], bias[g].
+// exact in 32-bit integers, rounded once to FP32 before the scales (see
+// i8_value for theirs) and once more to the output type.  With groups, token rows
+// [offsets[g], offsets[g+1]) use W[g], scale_w[g], bias[g].
 //
 // i8_tile<Cfg>: the schedule of the 16-bit pipelined kernel (an LDS ring of K
 // tiles filled by direct-to-LDS copies, operands one k-step ahead of their
@@ -135,12 +135,14 @@ struct I8Cfg {
 
 typedef int32_t i32x4v __attribute__((ext_vector_type(4)));
 
-// One value of the product: the exact sum, rounded to FP32, then the scales
-// and the bias in FP32.
+// One value of the product: the exact sum and its product with scale_a each
+// rounded to FP32, then the product with scale_w and the bias rounded once.
+// The fma is written out: left to the compiler's contraction of products and
+// sums, that rounding would be an option of the build.
 __device__ __forceinline__ float i8_value(int32_t sum, float sa, float sw, float bias, bool has_bias)
 {
-    const float v = (float)sum * sa * sw;
-    return has_bias ? v + bias : v;
+    const float v = (float)sum * sa;
+    return has_bias ? __builtin_fmaf(v, sw, bias) : v * sw;
 }
 
 // COUNT consecutive channels of one token, from column `col` (left = columns

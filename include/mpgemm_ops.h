@@ -85,8 +85,9 @@ int mpgemm_quantize_rows(int x_type, int64_t T, int64_t H, const void *X, int64_
 /*
  * Product of 8-bit codes:
  *     C[i][j] = (sum_k A[i][k] * W[j][k]) * scale_a[i] * scale_w[j] (+ bias[j])
- * The sum is exact; it is rounded to FP32, multiplied by the two scales in
- * FP32, and the bias is added in FP32; out_type (MPGEMM_T_*) rounds once more.
+ * The sum is exact; it is rounded to FP32 and multiplied by scale_a[i] in FP32;
+ * scale_w[j] and the bias follow in one fused multiply-add in FP32 (without a
+ * bias, one product); out_type (MPGEMM_T_*) rounds once more.
  *
  * A: M x K codes, lda >= max(1,K).  W: N x K codes (a column-major K x N
  * matrix: K consecutive), ldw >= max(1,K).  C: M x N, ldc >= max(1,N).

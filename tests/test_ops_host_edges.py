@@ -1,11 +1,17 @@
 """Host-side tests of the operator library at its edges (no GPU): slots a
-token beyond what the kernels' counters hold, first calls on several threads."""
+token beyond what the kernels' counters hold, first calls on several threads, arithmetic that no compiler
+option may change."""
+import os
+import re
+import shutil
+import subprocess
 import sys
 
 import pytest
 
 import dense_mixed_precision_amd as mp
 from dense_mixed_precision_amd import _ops
+from dense_mixed_precision_amd import build as mpbuild
 from tests.test_ops_host import COMBINE, call
 
 MOST = 1 << 30  # slots a token; mpgemm_route makes no more pairs
@@ -49,3 +55,29 @@ def test_first_call_publishes_nothing_half_made(monkeypatch):
         sys.settrace(before)
     assert seen[0] == (False, 0) and seen[-1] == (True, 3)
     assert all(types == 3 for there, types in seen if there)
+
+
+@pytest.mark.parametrize("contract", ["off", "on", "fast"])
+def test_scales_and_bias_are_one_arithmetic(contract, tmp_path):
+    """The last scale and the bias of the 8-bit product round once, as the
+    header states, whether or not the compiler contracts products and sums."""
+    if shutil.which("hipcc") is None and not os.path.exists("/opt/rocm/bin/hipcc"):
+        pytest.skip("hipcc not available")
+    src, out = tmp_path / "value.hip", tmp_path / "value.s"
+    src.write_text("""
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+#define MPGEMM_GROUPED
+#include "kernels.hpp"
+namespace mpg {
+#include "i8_kernels.hpp"
+__global__ void value(const int *s, const float *a, float *out) { *out = i8_value(*s, a[0], a[1], a[2], true); }
+}
+""")
+    flags = [f for f in mpbuild.flags() if f not in ("-shared", "-fPIC")]
+    res = subprocess.run([mpbuild.hipcc(), *flags, f"-ffp-contract={contract}", "-I", mpbuild.CSRC,
+                          "--cuda-device-only", "-S", str(src), "-o", str(out)], capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr[-2000:]
+    asm = out.read_text()
+    assert len(re.findall(r"\bv_(?:fma|fmac|fmaak|fmamk)_f32", asm)) == 1
+    assert len(re.findall(r"\bv_mul_f32", asm)) == 1 and not re.findall(r"\bv_add_f32", asm)
