@@ -75,7 +75,7 @@ extern "C" {
  * scale: R floats.  order NULL: row i of Q is row i of X, R == T.  Otherwise
  * row p of Q is row order[p] / top_k of X (R values from mpgemm_route), and
  * rows whose order is outside 0 .. T*top_k-1 keep what they hold.
- * T, H and R below 2^31.  workspace: see mpgemm_rows_workspace.
+ * T and R below 2^31, H at most 2^28.  workspace: see mpgemm_rows_workspace.
  */
 int mpgemm_quantize_rows(int x_type, int64_t T, int64_t H, const void *X, int64_t ldx,
                          const int32_t *order, int64_t R, int64_t top_k,

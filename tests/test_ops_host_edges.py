@@ -1,6 +1,6 @@
 """Host-side tests of the operator library at its edges (no GPU): slots a
-token beyond what the kernels' counters hold, first calls on several threads, arithmetic that no compiler
-option may change."""
+token beyond what the kernels' counters hold, the widest rows, first calls on
+several threads, arithmetic that no compiler option may change."""
 import os
 import re
 import shutil
@@ -12,7 +12,7 @@ import pytest
 import dense_mixed_precision_amd as mp
 from dense_mixed_precision_amd import _ops
 from dense_mixed_precision_amd import build as mpbuild
-from tests.test_ops_host import COMBINE, call
+from tests.test_ops_host import BACK, COMBINE, GATHER, QUANT, ROOT, call
 
 MOST = 1 << 30  # slots a token; mpgemm_route makes no more pairs
 
@@ -81,3 +81,15 @@ __global__ void value(const int *s, const float *a, float *out) { *out = i8_valu
     asm = out.read_text()
     assert len(re.findall(r"\bv_(?:fma|fmac|fmaak|fmamk)_f32", asm)) == 1
     assert len(re.findall(r"\bv_mul_f32", asm)) == 1 and not re.findall(r"\bv_add_f32", asm)
+
+
+@pytest.mark.parametrize("fn,defaults,rows", [
+    (mp.mpgemm_quantize_rows, QUANT, dict(T=0, R=0)), (mp.mpgemm_gather_rows, GATHER, dict(R=0)),
+    (mp.mpgemm_combine_rows, COMBINE, dict(T=0)), (mp.mpgemm_combine_rows_backward, BACK, dict(T=0))])
+def test_widest_row(fn, defaults, rows):
+    """The one limit on H that the header states holds for every row function."""
+    text = open(os.path.join(ROOT, "include", "mpgemm_ops.h")).read()
+    assert "row has at\n * most 2^28 values" in text and not re.search(r"\bH\b[^.;]*below 2\^31", text)
+    wide = {n: 1 << 29 for n in defaults if n.startswith("ld")}
+    assert call(fn, defaults, H=1 << 28, **rows, **wide) == 0
+    assert call(fn, defaults, H=(1 << 28) + 1, **rows, **wide) == mp.MPGEMM_EDIM
