@@ -36,8 +36,10 @@ mpgemm_timeline_clear() -- per-workgroup stamps of the pipelined kernel.
 Operators beside the GEMM (libmpgemm_ops.so, include/mpgemm_ops.h): raw entry
 points mpgemm_quantize_rows, mpgemm_i8_gemm, mpgemm_route_workspace,
 mpgemm_route, mpgemm_rows_workspace, mpgemm_gather_rows, mpgemm_combine_rows,
-mpgemm_combine_rows_backward, mpgemm_grouped and mpgemm_grouped_wgrad, and
-for torch tensors
+mpgemm_combine_rows_backward, mpgemm_grouped and mpgemm_grouped_wgrad; the
+kernel a product takes (include/mpgemm_ops_query.h): mpgemm_i8_query,
+mpgemm_grouped_query and mpgemm_grouped_wgrad_query -> dict; and for torch
+tensors
     quantize_rows(X, Q, scale, order, top_k)      rows to 8-bit codes
     gemm_i8(A, B, C, scale_a, scale_b, bias, offsets)   their product
     route(experts, num_experts) -> order, position, offsets
@@ -130,8 +132,11 @@ from ._ops import (  # noqa: F401
     mpgemm_combine_rows_backward,
     mpgemm_gather_rows,
     mpgemm_grouped,
+    mpgemm_grouped_query,
     mpgemm_grouped_wgrad,
+    mpgemm_grouped_wgrad_query,
     mpgemm_i8_gemm,
+    mpgemm_i8_query,
     mpgemm_quantize_rows,
     mpgemm_route,
     mpgemm_route_workspace,

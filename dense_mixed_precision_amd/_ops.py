@@ -1,6 +1,7 @@
-"""ctypes binding for libmpgemm_ops.so (include/mpgemm_ops.h): products of
-8-bit codes and products of tokens with experts.  Argument marshalling only,
-as in ``_binding``: every step runs in the HIP library, there is no fallback."""
+"""ctypes binding for libmpgemm_ops.so (include/mpgemm_ops.h and
+mpgemm_ops_query.h): products of 8-bit codes and products of tokens with
+experts.  Argument marshalling only, as in ``_binding``: every step runs in
+the HIP library, there is no fallback."""
 from __future__ import annotations
 
 import ctypes
@@ -19,6 +20,14 @@ MPGEMM_ID_I64 = 1
 MPGEMM_MAX_GROUPS = 1024
 #: largest K of mpgemm_i8_gemm
 MPGEMM_I8_MAX_K = 131071
+
+
+
+class MpgemmOpsKernel(ctypes.Structure):
+    """mpgemm_ops_kernel of include/mpgemm_ops_query.h."""
+    _fields_ = [*((n, ctypes.c_int32) for n in ("narrow", "bm", "bn", "bk", "stages", "waves")),
+                ("workgroups", ctypes.c_int64)]
+
 
 _lib = None
 #: torch, imported by the first call that takes tensors (the raw entry points
@@ -44,6 +53,7 @@ def load_ops():
                            "(no fallback path exists)")
     lib = ctypes.CDLL(OPS_PATH)
     i64, f32, vp, i32 = ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_int
+    kernel = ctypes.POINTER(MpgemmOpsKernel)
     for name, args, res in (
             ("mpgemm_quantize_rows", [i32, i64, i64, vp, i64, vp, i64, i64, vp, i64, vp, vp, i64, vp], i32),
             ("mpgemm_rows_workspace", [i32, i64, i64, i64, i64], i64),
@@ -55,7 +65,10 @@ def load_ops():
             ("mpgemm_combine_rows_backward",
              [i32, i32, i32, i64, i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp, vp], i32),
             ("mpgemm_grouped", [i32, i32, i64, i64, i64, i64, vp, i64, vp, i64, i64, vp, i64, f32, f32, vp, vp], i32),
-            ("mpgemm_grouped_wgrad", [i32, i64, i64, i64, i64, vp, i64, vp, i64, vp, i64, i64, f32, f32, vp, vp], i32)):
+            ("mpgemm_grouped_wgrad", [i32, i64, i64, i64, i64, vp, i64, vp, i64, vp, i64, i64, f32, f32, vp, vp], i32),
+            ("mpgemm_i8_query", [i64, i64, i64, i64, i64, i64, kernel], i32),
+            ("mpgemm_grouped_query", [i32, i64, i64, i64, i64, i64, i64, i64, kernel], i32),
+            ("mpgemm_grouped_wgrad_query", [i64, i64, i64, i64, i64, i64, i64, kernel], i32)):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = res
@@ -120,6 +133,27 @@ def mpgemm_grouped_wgrad(in_type, groups, R, M, N, A, lda, B, ldb, C, ldc, strid
                          stream=0) -> int:
     return load_ops().mpgemm_grouped_wgrad(in_type, groups, R, M, N, A, lda, B, ldb, C, ldc, stride_c, alpha, beta,
                                            offsets, stream)
+
+
+def _query(name, *args) -> dict:
+    out = MpgemmOpsKernel()
+    rc = getattr(load_ops(), name)(*args, ctypes.byref(out))
+    if rc != MPGEMM_OK:
+        raise MpgemmError(rc, name)
+    return {field: getattr(out, field) for field, _ in out._fields_}
+
+
+def mpgemm_i8_query(groups, M, N, K, lda, ldw) -> dict:
+    """The kernel that mpgemm_i8_gemm takes (groups 0: without offsets)."""
+    return _query("mpgemm_i8_query", groups, M, N, K, lda, ldw)
+
+
+def mpgemm_grouped_query(layout_b, groups, R, N, K, lda, ldb, ldc) -> dict:
+    return _query("mpgemm_grouped_query", layout_b, groups, R, N, K, lda, ldb, ldc)
+
+
+def mpgemm_grouped_wgrad_query(groups, R, M, N, lda, ldb, ldc) -> dict:
+    return _query("mpgemm_grouped_wgrad_query", groups, R, M, N, lda, ldb, ldc)
 
 
 # ---- torch tensors ----------------------------------------------------------

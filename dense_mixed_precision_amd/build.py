@@ -6,8 +6,8 @@
   ``include/mpgemm.h``): the config entries the factory chooses from and the
   fallbacks;
 * ``libmpgemm_ops.so`` -- the operators beside the GEMM (``csrc/ops.hip``,
-  C ABI in ``include/mpgemm_ops.h``): products of 8-bit codes, products of
-  tokens with experts;
+  C ABI in ``include/mpgemm_ops.h``, queries in ``include/mpgemm_ops_query.h``):
+  products of 8-bit codes, products of tokens with experts;
 * ``libmpgemm_probes.so`` -- the diagnostics (``csrc/probes.hip``, C ABI in
   ``include/mpgemm_probes.h``);
 * ``libmpgemm_timeline.so`` -- the product library built with
@@ -37,7 +37,7 @@ SRC = os.path.join(CSRC, "mpgemm.hip")
 PROBES_SRC = os.path.join(CSRC, "probes.hip")
 DEPS = [SRC, os.path.join(CSRC, "kernels.hpp"), os.path.join(ROOT, "include", "mpgemm.h")]
 OPS_SRC = os.path.join(CSRC, "ops.hip")
-OPS_DEPS = [OPS_SRC, os.path.join(ROOT, "include", "mpgemm_ops.h"), *DEPS[1:],
+OPS_DEPS = [OPS_SRC, *(os.path.join(ROOT, "include", f) for f in ("mpgemm_ops.h", "mpgemm_ops_query.h")), *DEPS[1:],
             *(os.path.join(CSRC, f) for f in ("groups.hpp", "i8_kernels.hpp", "narrow_rows.hpp", "token_kernels.hpp"))]
 LIB = os.path.join(HERE, "libmpgemm.so")
 OPS_LIB = os.path.join(HERE, "libmpgemm_ops.so")

@@ -1,6 +1,7 @@
 // ops.hip -- host side of the operators beside the GEMM (include/mpgemm_ops.h):
 // argument validation, the choice of kernel, launches.
 #include "mpgemm_ops.h"
+#include "mpgemm_ops_query.h"
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -102,14 +103,14 @@ void launch_i8(const I8Args &a, dim3 grid, hipStream_t s)
 }
 
 struct I8Entry {
-    int bm, bn, bkb;
+    int bm, bn, bkb, stages, waves;
     i8_launch launch[3];  // by output type
 };
 
 template <class Cfg>
 constexpr I8Entry i8_entry()
 {
-    return I8Entry{Cfg::BM, Cfg::BN, Cfg::BKB,
+    return I8Entry{Cfg::BM, Cfg::BN, Cfg::BKB, Cfg::STAGES, Cfg::NW,
                    {&launch_i8<Cfg, mpg::kTF16>, &launch_i8<Cfg, mpg::kTBF16>, &launch_i8<Cfg, mpg::kTF32>}};
 }
 
@@ -136,10 +137,12 @@ bool i8_fits(const I8Entry &e, int64_t lda, int64_t ldw, int64_t K)
 // workgroups: 6.7 against 6.4; 1x1024x16384, 64: 12.2 against 11.3).
 constexpr int64_t kNarrowManyWgs = 1024;
 
+int narrow_waves(int64_t grid) { return grid >= kNarrowManyWgs ? 4 : 8; }
+
 template <int IN, int OUT>
 void launch_narrow(const mpg::NarrowArgs &a, int64_t grid, hipStream_t s)
 {
-    if (grid >= kNarrowManyWgs)
+    if (narrow_waves(grid) == 4)
         hipLaunchKernelGGL((mpg::narrow_rows<IN, OUT, 8, 4>), dim3((unsigned)grid), dim3(256), 0, s, a);
     else
         hipLaunchKernelGGL((mpg::narrow_rows<IN, OUT, 4, 8>), dim3((unsigned)grid), dim3(512), 0, s, a);
@@ -236,7 +239,7 @@ using grouped_launch = void (*)(const GemmArgs &, const GroupArgs &, dim3, hipSt
 // 128x128 ones two to a compute unit (both gradients of 9 rows over 101
 // experts of 1888x1381 314 and 545).
 struct GroupedEntry {
-    int bm, bn, bk;
+    int bm, bn, bk, stages, waves;
     grouped_launch launch, launch_plain;
 };
 
@@ -249,7 +252,8 @@ void launch_grouped(const GemmArgs &a, const GroupArgs &g, dim3 grid, hipStream_
 template <class Cfg, bool BOTH = false>
 constexpr GroupedEntry grouped_entry()
 {
-    return GroupedEntry{Cfg::BM, Cfg::BN, Cfg::BK, &launch_grouped<Cfg, true>, &launch_grouped<Cfg, !BOTH>};
+    return GroupedEntry{Cfg::BM, Cfg::BN, Cfg::BK, Cfg::STAGES, Cfg::NT / 64, &launch_grouped<Cfg, true>,
+                        &launch_grouped<Cfg, !BOTH>};
 }
 
 // The tiles of one form of the product.  Where the groups split the rows
@@ -358,6 +362,103 @@ int select_wgrad(const GroupedEntry *table, int64_t groups, int64_t R, int64_t M
             return kGroupedWide;
     }
     return tiles(128, 128) >= kNumCu / 2 && fits(kGroupedTwo) ? kGroupedTwo : kWgradSmall;
+}
+
+// ---------------------------------------------------------------------------
+// What a product of checked arguments launches; the queries report it
+// ---------------------------------------------------------------------------
+struct Choice {
+    int error;               // or MPGEMM_OK
+    int id;                  // table entry, or -1: the narrow kernel
+    int64_t tiles_m, tiles_n, grid;
+};
+
+// `groups` 0: without offsets.
+Choice choose_i8(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldw)
+{
+    Choice c{};
+    if (groups == 0)
+        groups = 1;
+    if (!span_fits(16, lda, K, 1) || !span_fits(16, ldw, K, 1)) {
+        c.error = MPGEMM_ELD;
+        return c;
+    }
+    c.id = select_i8(groups, M, N, K, lda, ldw);
+    c.tiles_m = row_tiles(M, groups, c.id < 0 ? 16 : kI8Table[c.id].bm);
+    c.tiles_n = cdiv(N, c.id < 0 ? 16 : kI8Table[c.id].bn);
+    c.grid = mul_sat(c.tiles_m, c.tiles_n);
+    c.error = c.grid > kMaxGrid ? MPGEMM_EDIM : MPGEMM_OK;
+    return c;
+}
+
+Choice choose_grouped(const GroupedEntry *table, int lb, int64_t groups, int64_t R, int64_t N, int64_t K, int64_t lda,
+                      int64_t ldb, int64_t ldc)
+{
+    Choice c{};
+    c.id = select_grouped(table, lb, groups, R, N, K, lda, ldb, ldc);
+    if (c.id < 0 && !(span_fits(16, lda, K, 2) && span_fits(16, ldb, K, 2)))
+        c.id = kGroupedFew;
+    if (c.id >= 0 && !grouped_fits(table[c.id], kRowMajor, lb, lda, ldb, ldc)) {
+        c.error = MPGEMM_ELD;
+        return c;
+    }
+    c.tiles_m = row_tiles(R, groups, c.id < 0 ? 16 : table[c.id].bm);
+    c.tiles_n = cdiv(N, c.id < 0 ? 16 : table[c.id].bn);
+    c.grid = mul_sat(c.tiles_m, c.tiles_n);
+    c.error = c.grid > kMaxGrid ? MPGEMM_EDIM : MPGEMM_OK;
+    return c;
+}
+
+// (tiles of one group's C)
+Choice choose_wgrad(const GroupedEntry *table, int64_t groups, int64_t R, int64_t M, int64_t N, int64_t lda, int64_t ldb,
+                    int64_t ldc)
+{
+    Choice c{};
+    c.id = select_wgrad(table, groups, R, M, N, lda, ldb, ldc);
+    if (!grouped_fits(table[c.id], kColMajor, kRowMajor, lda, ldb, ldc)) {
+        c.error = MPGEMM_ELD;
+        return c;
+    }
+    c.tiles_m = cdiv(M, table[c.id].bm);
+    c.tiles_n = cdiv(N, table[c.id].bn);
+    c.grid = mul_sat(mul_sat(c.tiles_m, c.tiles_n), groups);
+    c.error = c.grid > kMaxGrid ? MPGEMM_EDIM : MPGEMM_OK;
+    return c;
+}
+
+template <class Entry>
+mpgemm_ops_kernel report_tile(const Entry &e, int bk, int64_t grid)
+{
+    return mpgemm_ops_kernel{0, e.bm, e.bn, bk, e.stages, e.waves, grid};
+}
+
+mpgemm_ops_kernel report_narrow(int64_t grid) { return mpgemm_ops_kernel{1, 16, 16, 0, 0, narrow_waves(grid), grid}; }
+
+// Dimensions and leading dimensions of the products; no pointers.
+int check_i8(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldw)
+{
+    if (groups < 1 || groups > MPGEMM_MAX_GROUPS || M < 0 || N < 0 || K < 0 || M > kMax32 || N > kMax32 ||
+        K > MPGEMM_I8_MAX_K)
+        return MPGEMM_EDIM;
+    return lda < at_least_one(K) || ldw < at_least_one(K) ? MPGEMM_ELD : MPGEMM_OK;
+}
+
+int check_grouped(int layout_b, int64_t groups, int64_t R, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldc)
+{
+    if (layout_b != MPGEMM_ROW_MAJOR && layout_b != MPGEMM_COL_MAJOR)
+        return MPGEMM_ELAYOUT;
+    if (groups < 1 || groups > MPGEMM_MAX_GROUPS || R < 0 || N < 0 || K < 0 || R > kMax32 || N > kMax32 || K > kMax32)
+        return MPGEMM_EDIM;
+    return lda < at_least_one(K) || ldb < at_least_one(layout_b == MPGEMM_COL_MAJOR ? K : N) || ldc < at_least_one(N)
+               ? MPGEMM_ELD
+               : MPGEMM_OK;
+}
+
+int check_wgrad(int64_t groups, int64_t R, int64_t M, int64_t N, int64_t lda, int64_t ldb, int64_t ldc)
+{
+    if (groups < 1 || groups > MPGEMM_MAX_GROUPS || R < 0 || M < 0 || N < 0 || R > kMax32 || M > kMax32 || N > kMax32)
+        return MPGEMM_EDIM;
+    return lda < at_least_one(M) || ldb < at_least_one(N) || ldc < at_least_one(N) ? MPGEMM_ELD : MPGEMM_OK;
 }
 
 // ---------------------------------------------------------------------------
@@ -548,10 +649,9 @@ int mpgemm_i8_gemm(int out_type, int64_t groups, int64_t M, int64_t N, int64_t K
 {
     if (!is_type(out_type))
         return MPGEMM_ETYPE;
-    if (groups < 1 || groups > MPGEMM_MAX_GROUPS || M < 0 || N < 0 || K < 0 || M > kMax32 || N > kMax32 ||
-        K > MPGEMM_I8_MAX_K)
-        return MPGEMM_EDIM;
-    if (lda < at_least_one(K) || ldw < at_least_one(K) || ldc < at_least_one(N) || stride_w < 0)
+    if (const int error = check_i8(groups, M, N, K, lda, ldw))
+        return error;
+    if (ldc < at_least_one(N) || stride_w < 0)
         return MPGEMM_ELD;
     if (M == 0 || N == 0)
         return MPGEMM_OK;
@@ -562,14 +662,10 @@ int mpgemm_i8_gemm(int out_type, int64_t groups, int64_t M, int64_t N, int64_t K
         !aligned(offsets, 4))
         return MPGEMM_EALIGN;
     const GroupArgs group_args{offsets, (int32_t)groups, (int32_t)M, stride_w};
-    if (!span_fits(16, lda, K, 1) || !span_fits(16, ldw, K, 1))
-        return MPGEMM_ELD;
-    const int id = select_i8(offsets ? groups : 1, M, N, K, lda, ldw);
-    if (id < 0) {
-        const int64_t tiles_n = cdiv(N, 16);
-        const int64_t grid = mul_sat(row_tiles(M, offsets ? groups : 1, 16), tiles_n);
-        if (grid > kMaxGrid)
-            return MPGEMM_EDIM;
+    const Choice c = choose_i8(offsets ? groups : 0, M, N, K, lda, ldw);
+    if (c.error)
+        return c.error;
+    if (c.id < 0) {
         mpg::NarrowArgs a{};
         a.A = reinterpret_cast<const uint8_t *>(A);
         a.W = reinterpret_cast<const uint8_t *>(W);
@@ -580,20 +676,15 @@ int mpgemm_i8_gemm(int out_type, int64_t groups, int64_t M, int64_t N, int64_t K
         a.stride_w = stride_w;
         a.N = (int32_t)N;
         a.KB = (int32_t)K;
-        a.tiles_n = (int32_t)tiles_n;
+        a.tiles_n = (int32_t)c.tiles_n;
         a.groups = group_args;
         a.scale_a = scale_a;
         a.scale_w = scale_w;
         a.bias = bias;
         forget_error();
-        kNarrowI8Launch[out_type](a, grid, stream_of(stream));
+        kNarrowI8Launch[out_type](a, c.grid, stream_of(stream));
         return launched();
     }
-    const I8Entry &e = kI8Table[id];
-    const int64_t tiles_n = cdiv(N, e.bn);
-    const int64_t grid = mul_sat(row_tiles(M, offsets ? groups : 1, e.bm), tiles_n);
-    if (grid > kMaxGrid)
-        return MPGEMM_EDIM;
     I8Args a{};
     a.A = A;
     a.W = W;
@@ -606,12 +697,12 @@ int mpgemm_i8_gemm(int out_type, int64_t groups, int64_t M, int64_t N, int64_t K
     a.ldc = ldc;
     a.N = (int32_t)N;
     a.K = (int32_t)K;
-    a.tiles_n = (int32_t)tiles_n;
+    a.tiles_n = (int32_t)c.tiles_n;
     a.group_m = 8;
     a.stream_c = aligned(C, 128) && ldc * size_of(out_type) % 128 == 0;
     a.groups = group_args;
     forget_error();
-    e.launch[out_type](a, dim3((unsigned)grid), stream_of(stream));
+    kI8Table[c.id].launch[out_type](a, dim3((unsigned)c.grid), stream_of(stream));
     return launched();
 }
 
@@ -778,12 +869,9 @@ int mpgemm_grouped(int in_type, int layout_b, int64_t groups, int64_t R, int64_t
 {
     if (in_type != MPGEMM_IN_F16 && in_type != MPGEMM_IN_BF16)
         return MPGEMM_ETYPE;
-    if (layout_b != MPGEMM_ROW_MAJOR && layout_b != MPGEMM_COL_MAJOR)
-        return MPGEMM_ELAYOUT;
-    if (groups < 1 || groups > MPGEMM_MAX_GROUPS || R < 0 || N < 0 || K < 0 || R > kMax32 || N > kMax32 || K > kMax32)
-        return MPGEMM_EDIM;
-    if (lda < at_least_one(K) || ldb < at_least_one(layout_b == MPGEMM_COL_MAJOR ? K : N) || ldc < at_least_one(N) ||
-        stride_b < 0)
+    if (const int error = check_grouped(layout_b, groups, R, N, K, lda, ldb, ldc))
+        return error;
+    if (stride_b < 0)
         return MPGEMM_ELD;
     if (R == 0 || N == 0)
         return MPGEMM_OK;
@@ -794,12 +882,10 @@ int mpgemm_grouped(int in_type, int layout_b, int64_t groups, int64_t R, int64_t
         return MPGEMM_EALIGN;
     const GroupArgs group_args{offsets, (int32_t)groups, (int32_t)R, stride_b};
     const GroupedEntry *const table = grouped_family(kRowMajor, layout_b, in_type);
-    const int id = select_grouped(table, layout_b, groups, R, N, K, lda, ldb, ldc);
-    if (id < 0 && span_fits(16, lda, K, 2) && span_fits(16, ldb, K, 2)) {
-        const int64_t tiles_n = cdiv(N, 16);
-        const int64_t grid = mul_sat(row_tiles(R, groups, 16), tiles_n);
-        if (grid > kMaxGrid)
-            return MPGEMM_EDIM;
+    const Choice c = choose_grouped(table, layout_b, groups, R, N, K, lda, ldb, ldc);
+    if (c.error)
+        return c.error;
+    if (c.id < 0) {
         mpg::NarrowArgs a{};
         a.A = reinterpret_cast<const uint8_t *>(A);
         a.W = reinterpret_cast<const uint8_t *>(B);
@@ -810,24 +896,17 @@ int mpgemm_grouped(int in_type, int layout_b, int64_t groups, int64_t R, int64_t
         a.stride_w = 2 * stride_b;
         a.N = (int32_t)N;
         a.KB = (int32_t)(2 * K);
-        a.tiles_n = (int32_t)tiles_n;
+        a.tiles_n = (int32_t)c.tiles_n;
         a.groups = group_args;
         a.alpha = alpha;
         a.beta = beta;
         forget_error();
         if (in_type == MPGEMM_IN_BF16)
-            launch_narrow<kInBF16, mpg::kTF32>(a, grid, stream_of(stream));
+            launch_narrow<kInBF16, mpg::kTF32>(a, c.grid, stream_of(stream));
         else
-            launch_narrow<kInF16, mpg::kTF32>(a, grid, stream_of(stream));
+            launch_narrow<kInF16, mpg::kTF32>(a, c.grid, stream_of(stream));
         return launched();
     }
-    const GroupedEntry &e = table[id < 0 ? kGroupedFew : id];
-    if (!grouped_fits(e, kRowMajor, layout_b, lda, ldb, ldc))
-        return MPGEMM_ELD;
-    const int64_t tiles_n = cdiv(N, e.bn);
-    const int64_t grid = mul_sat(row_tiles(R, groups, e.bm), tiles_n);
-    if (grid > kMaxGrid)
-        return MPGEMM_EDIM;
     GemmArgs a{};
     a.A = A;
     a.B = B;
@@ -840,11 +919,12 @@ int mpgemm_grouped(int in_type, int layout_b, int64_t groups, int64_t R, int64_t
     a.ldc = ldc;
     a.alpha = alpha;
     a.beta = beta;
-    a.tiles_n = (int32_t)tiles_n;
+    a.tiles_n = (int32_t)c.tiles_n;
     a.group_m = 8;
     a.splits = 1;
     forget_error();
-    (whole_lines(C, ldc) ? e.launch : e.launch_plain)(a, group_args, dim3((unsigned)grid), stream_of(stream));
+    const GroupedEntry &e = table[c.id];
+    (whole_lines(C, ldc) ? e.launch : e.launch_plain)(a, group_args, dim3((unsigned)c.grid), stream_of(stream));
     return launched();
 }
 
@@ -855,9 +935,9 @@ int mpgemm_grouped_wgrad(int in_type, int64_t groups, int64_t R, int64_t M, int6
 {
     if (in_type != MPGEMM_IN_F16 && in_type != MPGEMM_IN_BF16)
         return MPGEMM_ETYPE;
-    if (groups < 1 || groups > MPGEMM_MAX_GROUPS || R < 0 || M < 0 || N < 0 || R > kMax32 || M > kMax32 || N > kMax32)
-        return MPGEMM_EDIM;
-    if (lda < at_least_one(M) || ldb < at_least_one(N) || ldc < at_least_one(N) || stride_c < 0)
+    if (const int error = check_wgrad(groups, R, M, N, lda, ldb, ldc))
+        return error;
+    if (stride_c < 0)
         return MPGEMM_ELD;
     if (M == 0 || N == 0)
         return MPGEMM_OK;
@@ -870,13 +950,9 @@ int mpgemm_grouped_wgrad(int in_type, int64_t groups, int64_t R, int64_t M, int6
     if (!aligned(C, 4) || !aligned(offsets, 4) || (reads && (!aligned(A, 2) || !aligned(B, 2))))
         return MPGEMM_EALIGN;
     const GroupedEntry *const table = grouped_family(kColMajor, kRowMajor, in_type);
-    const GroupedEntry &e = table[select_wgrad(table, groups, R, M, N, lda, ldb, ldc)];
-    if (!grouped_fits(e, kColMajor, kRowMajor, lda, ldb, ldc))
-        return MPGEMM_ELD;
-    const int64_t tiles_m = cdiv(M, e.bm), tiles_n = cdiv(N, e.bn);
-    const int64_t grid = mul_sat(mul_sat(tiles_m, tiles_n), groups);
-    if (grid > kMaxGrid)
-        return MPGEMM_EDIM;
+    const Choice c = choose_wgrad(table, groups, R, M, N, lda, ldb, ldc);
+    if (c.error)
+        return c.error;
     GemmArgs a{};
     a.A = A;
     a.B = B;
@@ -889,15 +965,70 @@ int mpgemm_grouped_wgrad(int in_type, int64_t groups, int64_t R, int64_t M, int6
     a.ldc = ldc;
     a.alpha = alpha;
     a.beta = beta;
-    a.tiles_m = (int32_t)tiles_m;
-    a.tiles_n = (int32_t)tiles_n;
+    a.tiles_m = (int32_t)c.tiles_m;
+    a.tiles_n = (int32_t)c.tiles_n;
     a.group_m = 8;
     a.splits = 1;
     forget_error();
+    const GroupedEntry &e = table[c.id];
     const bool lines = whole_lines(C, ldc) && stride_c % 32 == 0;
     (lines ? e.launch : e.launch_plain)(a, GroupArgs{offsets, (int32_t)groups, (int32_t)R, stride_c},
-                                        dim3((unsigned)grid), stream_of(stream));
+                                        dim3((unsigned)c.grid), stream_of(stream));
     return launched();
+}
+
+int mpgemm_i8_query(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldw,
+                    mpgemm_ops_kernel *out)
+{
+    if (const int error = check_i8(groups == 0 ? 1 : groups, M, N, K, lda, ldw))
+        return error;
+    if (out == nullptr)
+        return MPGEMM_ENULL;
+    *out = mpgemm_ops_kernel{};
+    if (M == 0 || N == 0)
+        return MPGEMM_OK;
+    const Choice c = choose_i8(groups, M, N, K, lda, ldw);
+    if (c.error)
+        return c.error;
+    *out = c.id < 0 ? report_narrow(c.grid) : report_tile(kI8Table[c.id], kI8Table[c.id].bkb, c.grid);
+    return MPGEMM_OK;
+}
+
+int mpgemm_grouped_query(int layout_b, int64_t groups, int64_t R, int64_t N, int64_t K, int64_t lda, int64_t ldb,
+                         int64_t ldc, mpgemm_ops_kernel *out)
+{
+    if (const int error = check_grouped(layout_b, groups, R, N, K, lda, ldb, ldc))
+        return error;
+    if (out == nullptr)
+        return MPGEMM_ENULL;
+    *out = mpgemm_ops_kernel{};
+    if (R == 0 || N == 0)
+        return MPGEMM_OK;
+    // (the tiles are the same for both input types)
+    const GroupedEntry *const table = grouped_family(kRowMajor, layout_b, kInF16);
+    const Choice c = choose_grouped(table, layout_b, groups, R, N, K, lda, ldb, ldc);
+    if (c.error)
+        return c.error;
+    *out = c.id < 0 ? report_narrow(c.grid) : report_tile(table[c.id], table[c.id].bk, c.grid);
+    return MPGEMM_OK;
+}
+
+int mpgemm_grouped_wgrad_query(int64_t groups, int64_t R, int64_t M, int64_t N, int64_t lda, int64_t ldb, int64_t ldc,
+                               mpgemm_ops_kernel *out)
+{
+    if (const int error = check_wgrad(groups, R, M, N, lda, ldb, ldc))
+        return error;
+    if (out == nullptr)
+        return MPGEMM_ENULL;
+    *out = mpgemm_ops_kernel{};
+    if (M == 0 || N == 0)
+        return MPGEMM_OK;
+    const GroupedEntry *const table = grouped_family(kColMajor, kRowMajor, kInF16);
+    const Choice c = choose_wgrad(table, groups, R, M, N, lda, ldb, ldc);
+    if (c.error)
+        return c.error;
+    *out = report_tile(table[c.id], table[c.id].bk, c.grid);
+    return MPGEMM_OK;
 }
 
 }  // extern "C"
