@@ -188,7 +188,9 @@ bool wide_tiles_win(int64_t twide, int64_t t128, int64_t K)
 constexpr int64_t kNarrowFewTiles = 512;
 
 // Table entry of an 8-bit product, or -1 for the narrow kernel.  By sweeps of
-// every entry (us, graph-replayed, M, N, K in order), besides the rules above:
+// every entry (us, graph-replayed, M, N, K in order, one set of operands: what
+// fits the memory-side cache is read from there; three sets in turn take
+// 128x8192x8192 29 and 256x8192x8192 40), besides the rules above:
 //   up to 16 rows a group: narrow (8x8192x8192 15.1, 16x64 tiles 15.8;
 //     16x4096x4096 6.4 against 9.3), but 64x128 tiles for 5 rows and more
 //     a group over at least 512 of them (512 rows over 64 experts of

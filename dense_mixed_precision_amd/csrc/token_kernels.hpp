@@ -127,7 +127,7 @@ struct QuantArgs {
 // 32 waves of a compute unit keep as many rows in flight; with NT = 16 a wave
 // has four short ones.
 // TOKENS: a row is a token's, read and coded once and written to each row of
-// Q that one of its pairs has (see invert_order).
+// Q that one of its pairs has (see quantize_invert).
 template <int XT, int NT, int CACHE, bool TOKENS = false>
 __global__ void __launch_bounds__(256)
 quantize_rows(QuantArgs args)
