@@ -49,6 +49,13 @@ tensors
     combine_rows(Y, position, out, weights)       back to tokens, weighted
     combine_rows_backward(dout, Y, position, weights, dY, dweights)
 
+4-bit weights (libmpgemm_w4.so, include/mpgemm_w4.h): raw entry points
+mpgemm_w4_quantize, mpgemm_w4_dequantize, mpgemm_w4_gemm and mpgemm_w4_query
+-> dict; and for torch tensors
+    quantize_w4(W, Q, scale, group)               rows to 4-bit codes
+    dequantize_w4(Q, scale, W, group)             and back
+    gemm_w4(A, Q, scale, C, group, bias, offsets) products with them
+
 Tensor convenience: ``gemm(A, B, C, alpha, beta)`` for torch tensors on the
 GPU (A, B both float16 or both bfloat16, each row- or column-major, e.g. a
 transposed view; C float32 row-major), launched on torch's current stream.
@@ -143,4 +150,15 @@ from ._ops import (  # noqa: F401
     mpgemm_rows_workspace,
     quantize_rows,
     route,
+)
+from ._w4 import (  # noqa: F401
+    W4_PATH,
+    dequantize_w4,
+    gemm_w4,
+    load_w4,
+    mpgemm_w4_dequantize,
+    mpgemm_w4_gemm,
+    mpgemm_w4_quantize,
+    mpgemm_w4_query,
+    quantize_w4,
 )

@@ -8,6 +8,8 @@
 * ``libmpgemm_ops.so`` -- the operators beside the GEMM (``csrc/ops.hip``,
   C ABI in ``include/mpgemm_ops.h``, queries in ``include/mpgemm_ops_query.h``):
   products of 8-bit codes, products of tokens with experts;
+* ``libmpgemm_w4.so`` -- products with 4-bit weights (``csrc/w4.hip``, C ABI
+  in ``include/mpgemm_w4.h``);
 * ``libmpgemm_probes.so`` -- the diagnostics (``csrc/probes.hip``, C ABI in
   ``include/mpgemm_probes.h``);
 * ``libmpgemm_timeline.so`` -- the product library built with
@@ -38,9 +40,14 @@ PROBES_SRC = os.path.join(CSRC, "probes.hip")
 DEPS = [SRC, os.path.join(CSRC, "kernels.hpp"), os.path.join(ROOT, "include", "mpgemm.h")]
 OPS_SRC = os.path.join(CSRC, "ops.hip")
 OPS_DEPS = [OPS_SRC, *(os.path.join(ROOT, "include", f) for f in ("mpgemm_ops.h", "mpgemm_ops_query.h")), *DEPS[1:],
-            *(os.path.join(CSRC, f) for f in ("groups.hpp", "i8_kernels.hpp", "narrow_rows.hpp", "token_kernels.hpp"))]
+            *(os.path.join(CSRC, f) for f in ("elements.hpp", "groups.hpp", "host_util.hpp", "i8_kernels.hpp",
+                                              "narrow_rows.hpp", "token_kernels.hpp"))]
+W4_SRC = os.path.join(CSRC, "w4.hip")
+W4_DEPS = [W4_SRC, *(os.path.join(ROOT, "include", f) for f in ("mpgemm_w4.h", "mpgemm_ops.h", "mpgemm_ops_query.h")),
+           *DEPS[1:], *(os.path.join(CSRC, f) for f in ("elements.hpp", "groups.hpp", "host_util.hpp", "w4_kernels.hpp"))]
 LIB = os.path.join(HERE, "libmpgemm.so")
 OPS_LIB = os.path.join(HERE, "libmpgemm_ops.so")
+W4_LIB = os.path.join(HERE, "libmpgemm_w4.so")
 PROBES_LIB = os.path.join(HERE, "libmpgemm_probes.so")
 CANDIDATES_LIB = os.path.join(HERE, "libmpgemm_candidates.so")
 TIMELINE_LIB = os.path.join(HERE, "libmpgemm_timeline.so")
@@ -81,10 +88,11 @@ def _finish(job):
 def build(extra=(), out: str = LIB, verbose: bool = False, probes: bool = True,
           candidates: bool = False) -> str:
     """Compile the product library to ``out`` (default: in-tree
-    ``libmpgemm.so``), the operator library, the diagnostics libraries
+    ``libmpgemm.so``), the operator libraries, the diagnostics libraries
     (probes, timeline), and optionally the candidates library, in parallel.
     Returns ``out``."""
-    jobs = [_start(SRC, out, extra, verbose), _start(OPS_SRC, OPS_LIB, extra, verbose)]
+    jobs = [_start(SRC, out, extra, verbose), _start(OPS_SRC, OPS_LIB, extra, verbose),
+            _start(W4_SRC, W4_LIB, extra, verbose)]
     if probes:
         jobs.append(_start(PROBES_SRC, PROBES_LIB, extra, verbose))
         jobs.append(_start(SRC, TIMELINE_LIB, (*extra, "-DMPGEMM_TIMELINE"), verbose))
@@ -124,7 +132,7 @@ def build_c_check(verbose: bool = False) -> str:
 
 
 def is_stale() -> bool:
-    for lib, deps in ((LIB, DEPS), (OPS_LIB, OPS_DEPS)):
+    for lib, deps in ((LIB, DEPS), (OPS_LIB, OPS_DEPS), (W4_LIB, W4_DEPS)):
         if not os.path.exists(lib) or any(os.path.getmtime(d) > os.path.getmtime(lib) for d in deps):
             return True
     return False

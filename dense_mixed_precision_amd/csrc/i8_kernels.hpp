@@ -35,6 +35,8 @@
 // A[l%16][16*(l/16) + 0..15] and B[16*(l/16) + 0..15][l%16]; accumulator v
 // of lane l holds D[4*(l/16) + v][l%16].
 
+#include "elements.hpp"
+
 struct I8Args {
     const int8_t *A;
     const int8_t *W;
@@ -48,36 +50,6 @@ struct I8Args {
     int32_t group_m;
     int32_t stream_c;        // rows of C start on 128-byte lines: stores past the caches
     GroupArgs groups;
-};
-
-// Element types of tensors, as MPGEMM_T_* in the header.
-constexpr int kTF16 = 0;
-constexpr int kTBF16 = 1;
-constexpr int kTF32 = 2;
-
-template <int T>
-struct ElemOf;
-template <>
-struct ElemOf<kTF16> {
-    typedef _Float16 type;
-};
-template <>
-struct ElemOf<kTBF16> {
-    typedef __bf16 type;
-};
-template <>
-struct ElemOf<kTF32> {
-    typedef float type;
-};
-
-// 16 bytes at any address
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
-
-// N elements at any element-aligned address (the vector memory of gfx9
-// devices runs in unaligned mode under ROCm).
-template <class E, int N>
-struct __attribute__((packed, aligned(sizeof(E)))) Pack {
-    E v[N];
 };
 
 // One K-contiguous operand tile of BX rows of BKB bytes in LDS; see OpTile.
@@ -143,26 +115,6 @@ __device__ __forceinline__ float i8_value(int32_t sum, float sa, float sw, float
 {
     const float v = (float)sum * sa;
     return has_bias ? __builtin_fmaf(v, sw, bias) : v * sw;
-}
-
-// COUNT consecutive channels of one token, from column `col` (left = columns
-// from it to the edge).
-template <int OUT, int COUNT>
-__device__ __forceinline__ void i8_store(typename ElemOf<OUT>::type *row, int col, int left, const float *v)
-{
-    typedef typename ElemOf<OUT>::type E;
-    if (left >= COUNT) {
-        Pack<E, COUNT> p;
-#pragma unroll
-        for (int e = 0; e < COUNT; ++e)
-            p.v[e] = (E)v[e];
-        *(Pack<E, COUNT> *)(row + col) = p;
-    } else {
-#pragma unroll
-        for (int e = 0; e < COUNT; ++e)
-            if (e < left)
-                row[col + e] = (E)v[e];
-    }
 }
 
 // Wait until at most `newer` whole tiles' copies (0 .. MOST) are in flight.

@@ -1,7 +1,7 @@
 // token_kernels.hpp -- rows of tokens: 8-bit codes with a scale per row, the
 // order of (token, slot) pairs by expert, rows brought into that order and
 // back, and the gradients (gfx950).  Included by ops.hip in kernels.hpp's
-// namespace, after i8_kernels.hpp (element types).
+// namespace, after elements.hpp.
 //
 // All of these stream their operands once; they are bound by HBM, and at
 // decoding sizes by the launch.  Index arrays are read as untrusted data:
@@ -28,17 +28,6 @@ __device__ __forceinline__ void invert_one(const int32_t *order, int32_t *invers
     if (old >= 0)
         redo(pair, old);
 }
-
-// Workgroup number of a launch over x and y (see row_grid): one dimension holds
-// fewer than 2^32 threads.
-__device__ __forceinline__ int64_t wg_number() { return blockIdx.x + (int64_t)blockIdx.y * gridDim.x; }
-
-// Rows are read and written in vectors of 16 bytes at any element alignment.
-template <class E>
-struct VecOf {
-    static constexpr int N = 16 / sizeof(E);
-    typedef Pack<E, N> type;
-};
 
 // ---------------------------------------------------------------------------
 // Rows to 8-bit codes

@@ -1,0 +1,299 @@
+// w4.hip -- host side of the products with 4-bit weights (include/mpgemm_w4.h):
+// argument validation, the choice of kernel, launches.
+#include "mpgemm_w4.h"
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+// The GEMM's device code, for its matrix instructions, copies and groups, in a
+// namespace of its own: a program may link the other libraries too.
+#define MPGEMM_GROUPED
+#define mpg mpg_w4
+#include "kernels.hpp"
+
+namespace mpg {
+#include "elements.hpp"
+#include "w4_kernels.hpp"
+}  // namespace mpg
+
+#include "host_util.hpp"
+
+namespace {
+
+using mpg::W4Args;
+
+constexpr int64_t kMaxGroup = (int64_t)1 << 28;
+
+bool is_scale_type(int t) { return t == MPGEMM_T_F16 || t == MPGEMM_T_BF16; }
+
+// log2 of a group's size, or -1.
+int group_shift(int64_t group)
+{
+    if (group < 32 || group > kMaxGroup || (group & (group - 1)) != 0)
+        return -1;
+    return __builtin_ctzll((uint64_t)group);
+}
+
+// ---------------------------------------------------------------------------
+// Products
+// ---------------------------------------------------------------------------
+using w4_launch = void (*)(const W4Args &, dim3, hipStream_t);
+
+template <int IN, int GS, int MT, int NF, int WAVES, int DEPTH>
+void launch_narrow(const W4Args &a, dim3 grid, hipStream_t s)
+{
+    hipLaunchKernelGGL((mpg::w4_narrow<IN, GS, MT, NF, WAVES, DEPTH>), grid, dim3(64 * WAVES), 0, s, a);
+}
+
+template <class Cfg>
+void launch_tile(const W4Args &a, dim3 grid, hipStream_t s)
+{
+    hipLaunchKernelGGL(mpg::w4_tile<Cfg>, grid, dim3(Cfg::NT), 0, s, a);
+}
+
+struct W4Entry {
+    bool narrow;
+    int bm, bn, bk, stages, waves;
+    w4_launch launch[2][3];  // by input type, group size
+};
+
+template <int MT, int NF, int WAVES, int DEPTH>
+constexpr W4Entry narrow_entry()
+{
+    using mpg::kCoarse, mpg::kGroup32, mpg::kGroup64, mpg::kInBF16, mpg::kInF16;
+    return W4Entry{true, 16 * MT, 16 * NF, 0, 0, WAVES,
+                   {{&launch_narrow<kInF16, kCoarse, MT, NF, WAVES, DEPTH>,
+                     &launch_narrow<kInF16, kGroup64, MT, NF, WAVES, DEPTH>,
+                     &launch_narrow<kInF16, kGroup32, MT, NF, WAVES, DEPTH>},
+                    {&launch_narrow<kInBF16, kCoarse, MT, NF, WAVES, DEPTH>,
+                     &launch_narrow<kInBF16, kGroup64, MT, NF, WAVES, DEPTH>,
+                     &launch_narrow<kInBF16, kGroup32, MT, NF, WAVES, DEPTH>}}};
+}
+
+template <int BM, int NF, int NW>
+constexpr W4Entry tile_entry()
+{
+    using mpg::kCoarse, mpg::kGroup32, mpg::kGroup64, mpg::kInBF16, mpg::kInF16, mpg::W4Cfg;
+    return W4Entry{false, BM, 16 * NF * NW, W4Cfg<kInF16, kCoarse, BM, NF, NW>::BK, 2, NW,
+                   {{&launch_tile<W4Cfg<kInF16, kCoarse, BM, NF, NW>>, &launch_tile<W4Cfg<kInF16, kGroup64, BM, NF, NW>>,
+                     &launch_tile<W4Cfg<kInF16, kGroup32, BM, NF, NW>>},
+                    {&launch_tile<W4Cfg<kInBF16, kCoarse, BM, NF, NW>>,
+                     &launch_tile<W4Cfg<kInBF16, kGroup64, BM, NF, NW>>,
+                     &launch_tile<W4Cfg<kInBF16, kGroup32, BM, NF, NW>>}}};
+}
+
+enum : int { kNarrow16 = 0, kNarrow32 = 1, kNarrow64 = 2, kTile64 = 3, kTile128 = 4 };
+const W4Entry kTable[] = {
+    narrow_entry<1, 2, 8, 4>(),
+    narrow_entry<2, 2, 8, 2>(),
+    narrow_entry<4, 2, 8, 1>(),
+    tile_entry<64, 2, 8>(),
+    tile_entry<128, 2, 8>(),
+};
+
+bool entry_fits(const W4Entry &e, int64_t lda, int64_t K)
+{
+    return span_fits(e.bm, lda, K, 2);
+}
+
+// Table entry of a product.
+int select_w4(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t lda)
+{
+    const int64_t per = cdiv(M, groups);
+    auto tiles = [&](int id) { return likely_tiles(M, groups, kTable[id].bm, cdiv(N, kTable[id].bn)); };
+    if (per <= 16)
+        return kNarrow16;
+    if (per <= 32)
+        return kNarrow32;
+    if (per > 64 && tiles(kTile128) >= kNumCu / 2 && entry_fits(kTable[kTile128], lda, K))
+        return kTile128;
+    if (per > 64 && tiles(kTile64) >= kNumCu / 2)
+        return kTile64;
+    return kNarrow64;
+}
+
+struct Choice {
+    int error;
+    int id;
+    int64_t tiles_n, grid;
+};
+
+int check_w4(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t group, int64_t lda, int64_t ldq, int64_t lds)
+{
+    if (groups < 1 || groups > MPGEMM_MAX_GROUPS || M < 0 || N < 0 || K < 0 || M > kMax32 || N > kMax32 ||
+        K > kMaxWidth || group_shift(group) < 0)
+        return MPGEMM_EDIM;
+    const int64_t bytes = cdiv(K, 2), count = cdiv(K, group);
+    if (lda < at_least_one(K) || ldq < at_least_one(bytes) || lds < at_least_one(count) || !span_fits(64, lda, K, 2) ||
+        !span_fits(32, ldq, bytes, 1) || !span_fits(32, lds, count, 2))
+        return MPGEMM_ELD;
+    return MPGEMM_OK;
+}
+
+// `groups` 0: without offsets.
+Choice choose_w4(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t lda)
+{
+    Choice c{};
+    if (groups == 0)
+        groups = 1;
+    c.id = select_w4(groups, M, N, K, lda);
+    c.tiles_n = cdiv(N, kTable[c.id].bn);
+    c.grid = mul_sat(row_tiles(M, groups, kTable[c.id].bm), c.tiles_n);
+    c.error = c.grid > kMaxGrid ? MPGEMM_EDIM : MPGEMM_OK;
+    return c;
+}
+
+// ---------------------------------------------------------------------------
+// Rows to codes and back
+// ---------------------------------------------------------------------------
+template <int WT>
+void launch_pack(int s_type, const mpg::W4PackArgs &a, hipStream_t s)
+{
+    const dim3 grid = row_grid(cdiv((int64_t)a.N * a.parts, 4));
+    if (s_type == MPGEMM_T_F16)
+        hipLaunchKernelGGL((mpg::w4_pack<WT, mpg::kTF16>), grid, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((mpg::w4_pack<WT, mpg::kTBF16>), grid, dim3(256), 0, s, a);
+}
+
+template <int WT>
+void launch_unpack(int s_type, const mpg::W4UnpackArgs &a, hipStream_t s)
+{
+    const dim3 grid = row_grid(cdiv((int64_t)a.N * a.parts, 4));
+    if (s_type == MPGEMM_T_F16)
+        hipLaunchKernelGGL((mpg::w4_unpack<mpg::kTF16, WT>), grid, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((mpg::w4_unpack<mpg::kTBF16, WT>), grid, dim3(256), 0, s, a);
+}
+
+// What both directions ask of their arguments; `parts` waves a row.
+int check_pack(int w_type, int s_type, int64_t N, int64_t K, int64_t group, const void *W, int64_t ldw, const void *Q,
+               int64_t ldq, const void *scale, int64_t lds, int64_t span, int64_t &parts)
+{
+    if (!is_type(w_type) || !is_scale_type(s_type))
+        return MPGEMM_ETYPE;
+    if (N < 0 || K < 0 || N > kMax32 || K > kMaxWidth || group_shift(group) < 0)
+        return MPGEMM_EDIM;
+    parts = cdiv(K, span > 512 ? span : 512);
+    if (mul_sat(N, parts) > kMax32)
+        return MPGEMM_EDIM;
+    if (ldw < at_least_one(K) || ldq < at_least_one(cdiv(K, 2)) || lds < at_least_one(cdiv(K, group)))
+        return MPGEMM_ELD;
+    if (N == 0 || K == 0)
+        return MPGEMM_OK;
+    if (W == nullptr || Q == nullptr || scale == nullptr)
+        return MPGEMM_ENULL;
+    return !aligned(W, size_of(w_type)) || !aligned(scale, 2) ? MPGEMM_EALIGN : MPGEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mpgemm_w4_quantize(int w_type, int s_type, int64_t N, int64_t K, int64_t group,
+                       const void *W, int64_t ldw, uint8_t *Q, int64_t ldq,
+                       void *scale, int64_t lds, void *stream)
+{
+    int64_t parts = 0;
+    if (const int error = check_pack(w_type, s_type, N, K, group, W, ldw, Q, ldq, scale, lds, group, parts))
+        return error;
+    if (N == 0 || K == 0)
+        return MPGEMM_OK;
+    const mpg::W4PackArgs a{W, Q, static_cast<uint16_t *>(scale), ldw, ldq, lds, (int32_t)N, (int32_t)K,
+                            group_shift(group), (int32_t)parts};
+    forget_error();
+    if (w_type == MPGEMM_T_F16)
+        launch_pack<mpg::kTF16>(s_type, a, stream_of(stream));
+    else if (w_type == MPGEMM_T_BF16)
+        launch_pack<mpg::kTBF16>(s_type, a, stream_of(stream));
+    else
+        launch_pack<mpg::kTF32>(s_type, a, stream_of(stream));
+    return launched();
+}
+
+int mpgemm_w4_dequantize(int w_type, int s_type, int64_t N, int64_t K, int64_t group,
+                         const uint8_t *Q, int64_t ldq, const void *scale, int64_t lds,
+                         void *W, int64_t ldw, void *stream)
+{
+    int64_t parts = 0;
+    if (const int error = check_pack(w_type, s_type, N, K, group, W, ldw, Q, ldq, scale, lds, 512, parts))
+        return error;
+    if (N == 0 || K == 0)
+        return MPGEMM_OK;
+    const mpg::W4UnpackArgs a{Q, static_cast<const uint16_t *>(scale), W, ldq, lds, ldw, (int32_t)N, (int32_t)K,
+                              group_shift(group), (int32_t)parts};
+    forget_error();
+    if (w_type == MPGEMM_T_F16)
+        launch_unpack<mpg::kTF16>(s_type, a, stream_of(stream));
+    else if (w_type == MPGEMM_T_BF16)
+        launch_unpack<mpg::kTBF16>(s_type, a, stream_of(stream));
+    else
+        launch_unpack<mpg::kTF32>(s_type, a, stream_of(stream));
+    return launched();
+}
+
+int mpgemm_w4_gemm(int in_type, int out_type, int64_t groups, int64_t M, int64_t N, int64_t K, int64_t group,
+                   const uint16_t *A, int64_t lda, const uint8_t *Q, int64_t ldq, int64_t stride_q,
+                   const void *scale, int64_t lds, int64_t stride_s, void *C, int64_t ldc,
+                   const float *bias, const int32_t *offsets, void *stream)
+{
+    if ((in_type != MPGEMM_IN_F16 && in_type != MPGEMM_IN_BF16) || !is_type(out_type))
+        return MPGEMM_ETYPE;
+    if (const int error = check_w4(groups, M, N, K, group, lda, ldq, lds))
+        return error;
+    if (ldc < at_least_one(N) || stride_q < 0 || stride_s < 0)
+        return MPGEMM_ELD;
+    if (M == 0 || N == 0)
+        return MPGEMM_OK;
+    if (C == nullptr || (K > 0 && (A == nullptr || Q == nullptr || scale == nullptr)) ||
+        (groups > 1 && offsets == nullptr))
+        return MPGEMM_ENULL;
+    if (!aligned(A, 2) || !aligned(scale, 2) || !aligned(C, size_of(out_type)) || !aligned(bias, 4) ||
+        !aligned(offsets, 4))
+        return MPGEMM_EALIGN;
+    const Choice c = choose_w4(offsets ? groups : 0, M, N, K, lda);
+    if (c.error)
+        return c.error;
+    W4Args a{};
+    a.A = A;
+    a.Q = Q;
+    a.S = static_cast<const uint16_t *>(scale);
+    a.C = C;
+    a.bias = bias;
+    a.lda = lda;
+    a.ldq = ldq;
+    a.lds = lds;
+    a.ldc = ldc;
+    a.stride_s = stride_s;
+    a.N = (int32_t)N;
+    a.K = (int32_t)K;
+    a.shift = group_shift(group);
+    a.out_type = out_type;
+    a.tiles_n = (int32_t)c.tiles_n;
+    a.group_m = 8;
+    a.groups = mpg::GroupArgs{offsets, (int32_t)groups, (int32_t)M, stride_q};
+    forget_error();
+    const int gs = a.shift >= 7 ? mpg::kCoarse : a.shift == 6 ? mpg::kGroup64 : mpg::kGroup32;
+    kTable[c.id].launch[in_type][gs](a, dim3((unsigned)c.grid), stream_of(stream));
+    return launched();
+}
+
+int mpgemm_w4_query(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t group,
+                    int64_t lda, int64_t ldq, int64_t lds, mpgemm_ops_kernel *out)
+{
+    if (const int error = check_w4(groups == 0 ? 1 : groups, M, N, K, group, lda, ldq, lds))
+        return error;
+    if (out == nullptr)
+        return MPGEMM_ENULL;
+    *out = mpgemm_ops_kernel{};
+    if (M == 0 || N == 0)
+        return MPGEMM_OK;
+    const Choice c = choose_w4(groups, M, N, K, lda);
+    if (c.error)
+        return c.error;
+    const W4Entry &e = kTable[c.id];
+    *out = mpgemm_ops_kernel{e.narrow, e.bm, e.bn, e.bk, e.stages, e.waves, c.grid};
+    return MPGEMM_OK;
+}
+
+}  // extern "C"
