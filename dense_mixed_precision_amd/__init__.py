@@ -56,6 +56,14 @@ mpgemm_w4_quantize, mpgemm_w4_dequantize, mpgemm_w4_gemm and mpgemm_w4_query
     dequantize_w4(Q, scale, W, group)             and back
     gemm_w4(A, Q, scale, C, group, bias, offsets) products with them
 
+The router in front of the experts (libmpgemm_router.so,
+include/mpgemm_router.h): raw entry points mpgemm_select_experts,
+mpgemm_balance_workspace, mpgemm_balance_loss and mpgemm_router_backward; and
+for torch tensors
+    select_experts(logits, ids, weights, normalize)     each token's top_k experts
+    balance_loss(logits, ids, loss, counts, probs, coefficient)   their use, and the loss that evens it
+    router_backward(logits, ids, dlogits, dweights, normalize, counts, dloss, coefficient)
+
 Tensor convenience: ``gemm(A, B, C, alpha, beta)`` for torch tensors on the
 GPU (A, B both float16 or both bfloat16, each row- or column-major, e.g. a
 transposed view; C float32 row-major), launched on torch's current stream.
@@ -150,6 +158,18 @@ from ._ops import (  # noqa: F401
     mpgemm_rows_workspace,
     quantize_rows,
     route,
+)
+from ._router import (  # noqa: F401
+    MPGEMM_MAX_SELECT,
+    ROUTER_PATH,
+    balance_loss,
+    load_router,
+    mpgemm_balance_loss,
+    mpgemm_balance_workspace,
+    mpgemm_router_backward,
+    mpgemm_select_experts,
+    router_backward,
+    select_experts,
 )
 from ._w4 import (  # noqa: F401
     W4_PATH,

@@ -10,6 +10,8 @@
   products of 8-bit codes, products of tokens with experts;
 * ``libmpgemm_w4.so`` -- products with 4-bit weights (``csrc/w4.hip``, C ABI
   in ``include/mpgemm_w4.h``);
+* ``libmpgemm_router.so`` -- the router in front of the experts
+  (``csrc/router.hip``, C ABI in ``include/mpgemm_router.h``);
 * ``libmpgemm_probes.so`` -- the diagnostics (``csrc/probes.hip``, C ABI in
   ``include/mpgemm_probes.h``);
 * ``libmpgemm_timeline.so`` -- the product library built with
@@ -45,9 +47,13 @@ OPS_DEPS = [OPS_SRC, *(os.path.join(ROOT, "include", f) for f in ("mpgemm_ops.h"
 W4_SRC = os.path.join(CSRC, "w4.hip")
 W4_DEPS = [W4_SRC, *(os.path.join(ROOT, "include", f) for f in ("mpgemm_w4.h", "mpgemm_ops.h", "mpgemm_ops_query.h")),
            *DEPS[1:], *(os.path.join(CSRC, f) for f in ("elements.hpp", "groups.hpp", "host_util.hpp", "w4_kernels.hpp"))]
+ROUTER_SRC = os.path.join(CSRC, "router.hip")
+ROUTER_DEPS = [ROUTER_SRC, *(os.path.join(ROOT, "include", f) for f in ("mpgemm_router.h", "mpgemm_ops.h", "mpgemm.h")),
+               *(os.path.join(CSRC, f) for f in ("elements.hpp", "host_util.hpp", "router_kernels.hpp"))]
 LIB = os.path.join(HERE, "libmpgemm.so")
 OPS_LIB = os.path.join(HERE, "libmpgemm_ops.so")
 W4_LIB = os.path.join(HERE, "libmpgemm_w4.so")
+ROUTER_LIB = os.path.join(HERE, "libmpgemm_router.so")
 PROBES_LIB = os.path.join(HERE, "libmpgemm_probes.so")
 CANDIDATES_LIB = os.path.join(HERE, "libmpgemm_candidates.so")
 TIMELINE_LIB = os.path.join(HERE, "libmpgemm_timeline.so")
@@ -92,7 +98,7 @@ def build(extra=(), out: str = LIB, verbose: bool = False, probes: bool = True,
     (probes, timeline), and optionally the candidates library, in parallel.
     Returns ``out``."""
     jobs = [_start(SRC, out, extra, verbose), _start(OPS_SRC, OPS_LIB, extra, verbose),
-            _start(W4_SRC, W4_LIB, extra, verbose)]
+            _start(W4_SRC, W4_LIB, extra, verbose), _start(ROUTER_SRC, ROUTER_LIB, extra, verbose)]
     if probes:
         jobs.append(_start(PROBES_SRC, PROBES_LIB, extra, verbose))
         jobs.append(_start(SRC, TIMELINE_LIB, (*extra, "-DMPGEMM_TIMELINE"), verbose))
@@ -132,7 +138,7 @@ def build_c_check(verbose: bool = False) -> str:
 
 
 def is_stale() -> bool:
-    for lib, deps in ((LIB, DEPS), (OPS_LIB, OPS_DEPS), (W4_LIB, W4_DEPS)):
+    for lib, deps in ((LIB, DEPS), (OPS_LIB, OPS_DEPS), (W4_LIB, W4_DEPS), (ROUTER_LIB, ROUTER_DEPS)):
         if not os.path.exists(lib) or any(os.path.getmtime(d) > os.path.getmtime(lib) for d in deps):
             return True
     return False
