@@ -131,15 +131,6 @@ __device__ __forceinline__ void wait_tiles(int newer)
     }
 }
 
-// One wave instruction: lane l copies 4 bytes from rsrc at voff into LDS at
-// byte address lds_addr + 4*l (see dma16).
-__device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t lds_addr, uint32_t voff)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                 ::"s"(lds_addr), "v"(voff), "s"(rsrc)
-                 : "memory", "m0");
-}
-
 template <class Cfg, int OUT>
 __global__ void __launch_bounds__(Cfg::NT)
 i8_tile(I8Args args)

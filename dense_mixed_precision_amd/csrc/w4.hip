@@ -39,10 +39,10 @@ int group_shift(int64_t group)
 // ---------------------------------------------------------------------------
 using w4_launch = void (*)(const W4Args &, dim3, hipStream_t);
 
-template <int IN, int GS, int MT, int NF, int WAVES, int DEPTH>
+template <int IN, int GS, int NA, int NF, int WAVES, int STAGES>
 void launch_narrow(const W4Args &a, dim3 grid, hipStream_t s)
 {
-    hipLaunchKernelGGL((mpg::w4_narrow<IN, GS, MT, NF, WAVES, DEPTH>), grid, dim3(64 * WAVES), 0, s, a);
+    hipLaunchKernelGGL((mpg::w4_narrow<IN, GS, NA, NF, WAVES, STAGES>), grid, dim3(64 * WAVES), 0, s, a);
 }
 
 template <class Cfg>
@@ -57,24 +57,24 @@ struct W4Entry {
     w4_launch launch[2][3];  // by input type, group size
 };
 
-template <int MT, int NF, int WAVES, int DEPTH>
+template <int NA, int NF, int WAVES, int STAGES>
 constexpr W4Entry narrow_entry()
 {
     using mpg::kCoarse, mpg::kGroup32, mpg::kGroup64, mpg::kInBF16, mpg::kInF16;
-    return W4Entry{true, 16 * MT, 16 * NF, 0, 0, WAVES,
-                   {{&launch_narrow<kInF16, kCoarse, MT, NF, WAVES, DEPTH>,
-                     &launch_narrow<kInF16, kGroup64, MT, NF, WAVES, DEPTH>,
-                     &launch_narrow<kInF16, kGroup32, MT, NF, WAVES, DEPTH>},
-                    {&launch_narrow<kInBF16, kCoarse, MT, NF, WAVES, DEPTH>,
-                     &launch_narrow<kInBF16, kGroup64, MT, NF, WAVES, DEPTH>,
-                     &launch_narrow<kInBF16, kGroup32, MT, NF, WAVES, DEPTH>}}};
+    return W4Entry{true, 4 * NA, 16 * NF, 128, STAGES, WAVES,
+                   {{&launch_narrow<kInF16, kCoarse, NA, NF, WAVES, STAGES>,
+                     &launch_narrow<kInF16, kGroup64, NA, NF, WAVES, STAGES>,
+                     &launch_narrow<kInF16, kGroup32, NA, NF, WAVES, STAGES>},
+                    {&launch_narrow<kInBF16, kCoarse, NA, NF, WAVES, STAGES>,
+                     &launch_narrow<kInBF16, kGroup64, NA, NF, WAVES, STAGES>,
+                     &launch_narrow<kInBF16, kGroup32, NA, NF, WAVES, STAGES>}}};
 }
 
 template <int BM, int NF, int NW>
 constexpr W4Entry tile_entry()
 {
     using mpg::kCoarse, mpg::kGroup32, mpg::kGroup64, mpg::kInBF16, mpg::kInF16, mpg::W4Cfg;
-    return W4Entry{false, BM, 16 * NF * NW, W4Cfg<kInF16, kCoarse, BM, NF, NW>::BK, 2, NW,
+    return W4Entry{false, BM, 16 * NF * NW, 128, 3, NW,
                    {{&launch_tile<W4Cfg<kInF16, kCoarse, BM, NF, NW>>, &launch_tile<W4Cfg<kInF16, kGroup64, BM, NF, NW>>,
                      &launch_tile<W4Cfg<kInF16, kGroup32, BM, NF, NW>>},
                     {&launch_tile<W4Cfg<kInBF16, kCoarse, BM, NF, NW>>,
@@ -82,34 +82,60 @@ constexpr W4Entry tile_entry()
                      &launch_tile<W4Cfg<kInBF16, kGroup32, BM, NF, NW>>}}};
 }
 
-enum : int { kNarrow16 = 0, kNarrow32 = 1, kNarrow64 = 2, kTile64 = 3, kTile128 = 4 };
+// Narrow kernels by tokens x channels and waves, then tiles.
+enum : int {
+    kFew4 = 0, kFew16 = 1, kNarrow8 = 2, kNarrow8Four = 3, kNarrow16 = 4, kNarrow16Four = 5, kNarrow32 = 6,
+    kNarrow64 = 7, kTile64 = 8, kTile64Wide = 9, kTile128 = 10
+};
 const W4Entry kTable[] = {
-    narrow_entry<1, 2, 8, 4>(),
-    narrow_entry<2, 2, 8, 2>(),
-    narrow_entry<4, 2, 8, 1>(),
-    tile_entry<64, 2, 8>(),
-    tile_entry<128, 2, 8>(),
+    narrow_entry<1, 1, 8, 3>(), narrow_entry<4, 1, 8, 2>(), narrow_entry<2, 2, 8, 2>(), narrow_entry<2, 2, 4, 2>(),
+    narrow_entry<4, 2, 8, 2>(), narrow_entry<4, 2, 4, 2>(), narrow_entry<8, 2, 4, 2>(), narrow_entry<16, 2, 4, 2>(),
+    tile_entry<64, 2, 4>(), tile_entry<64, 2, 8>(), tile_entry<128, 2, 8>(),
 };
 
-bool entry_fits(const W4Entry &e, int64_t lda, int64_t K)
-{
-    return span_fits(e.bm, lda, K, 2);
-}
-
-// Table entry of a product.
+// Table entry of a product.  By sweeps of every entry (us, graph-replayed,
+// three sets of operands in turn, M, N, K in order; groups of 128, BF16):
+//   the narrow kernel with the smallest tile whose workgroups go around the
+//     compute units once: 16x16 (16x1024x8192 8.0, 16x32 10.6; 64x1024x8192 8.6
+//     against 11.2), for few tokens 4x16 (1x4096x4096 5.2, 8x32 6.3), then 8x32
+//     (8x8192x8192 11.7, 16x32 12.4), 16x32 (128x1024x8192 11.5, 32x32 15.8),
+//     32x32 (256x1024x8192 16.1, 64x32 23.3);
+//   8 waves where each has 4 steps of K at least, else 4 (8x8192x8192 11.7
+//     against 13.3; 8x8192x1024 4.6 against 4.4);
+//   few rows a group are the reading of the weights: 4 waves, 8x32 up to 4
+//     rows a group, 16x32 up to 16 (64 rows over 64 experts of 2048x2048 25.3
+//     and 29.4; 64 over 8 of 4096x4096 25.0 and 21.8; 8 waves 33 to 55);
+//   128x256 tiles from 192 of them above 64 rows a group (1024x8192x8192 133,
+//     64x256 174; 512x8192x8192, 128 of them, 116 against 88; 1200 rows over 32
+//     experts of 2048x2048 39 against 53);
+//   64x256 from 160 (512x8192x8192 88, 64x128 95; 256x8192x8192, 128 of them, 85
+//     against 67);
+//   64x128, two workgroups a compute unit, from 192 (256x8192x8192 67, 64x32 89;
+//     128x8192x8192, 128 of them, 66 against 46);
+//   else 64x32.
+// The tiles take K in whole steps of 128 and K >= 128.
 int select_w4(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t lda)
 {
     const int64_t per = cdiv(M, groups);
     auto tiles = [&](int id) { return likely_tiles(M, groups, kTable[id].bm, cdiv(N, kTable[id].bn)); };
+    const bool deep = K >= 8 * 4 * 128;
+    if (tiles(kFew16) <= kNumCu)
+        return per <= 4 ? kFew4 : kFew16;
+    if (per <= 8 && tiles(kNarrow8) <= kNumCu)
+        return deep ? kNarrow8 : kNarrow8Four;
+    if (tiles(kNarrow16) <= kNumCu)
+        return deep ? kNarrow16 : kNarrow16Four;
     if (per <= 16)
-        return kNarrow16;
-    if (per <= 32)
+        return per <= 4 ? kNarrow8Four : kNarrow16Four;
+    if (tiles(kNarrow32) <= kNumCu)
         return kNarrow32;
-    if (per > 64 && tiles(kTile128) >= kNumCu / 2 && entry_fits(kTable[kTile128], lda, K))
+    if (K < 128)
+        return kNarrow64;
+    if (per > 64 && tiles(kTile128) >= 192 && span_fits(kTable[kTile128].bm, lda, K, 2))
         return kTile128;
-    if (per > 64 && tiles(kTile64) >= kNumCu / 2)
-        return kTile64;
-    return kNarrow64;
+    if (tiles(kTile64Wide) >= 160)
+        return kTile64Wide;
+    return tiles(kTile64) >= 192 ? kTile64 : kNarrow64;
 }
 
 struct Choice {

@@ -48,10 +48,12 @@ __device__ __forceinline__ half8 codes8(uint32_t w)
 {
     u32x4 out;
     if constexpr (IN == kInF16) {
+        uint32_t mask = 0x00F0000Fu;
+        asm("" : "+v"(mask));  // (in a register, for one instruction of and and or)
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
             uint32_t x = __builtin_amdgcn_perm(0u, w, 0x0C000C00u | (uint32_t)(p << 16) | (uint32_t)p);
-            x = (x & 0x00F0000Fu) | 0x54006400u;
+            x = (x & mask) | 0x54006400u;
             const half2v h = __builtin_bit_cast(half2v, x) + half2v{(_Float16)-1032.0f, (_Float16)-72.0f};
             out[p] = __builtin_bit_cast(uint32_t, h);
         }
@@ -154,182 +156,224 @@ __device__ __forceinline__ void store_values(int type, void *C, int64_t at, int 
 }
 
 // ---------------------------------------------------------------------------
-// Few tokens: the weights straight from memory into operand registers
+// Few tokens: each wave streams its part of K through LDS of its own
 // ---------------------------------------------------------------------------
-// A workgroup makes 16*MT tokens x 16*NF channels, its WAVES waves splitting K in
-// steps of 128 values; a lane's 16 bytes of a weight row are 32 codes.  Tokens
-// are the first operand, so a lane's accumulators are four tokens of one
+// A workgroup makes up to 4*NA tokens (MT operands of 16) x 16*NF channels, its
+// WAVES waves splitting K in steps of 128 values.  Tokens are the matrix
+// instruction's first operand, so a lane's accumulators are four tokens of one
 // channel and one scale serves them; its NF channels are neighbours, stored
 // together.  The waves' sums are added in LDS in wave order.
-template <int IN, int GS, int MT, int NF, int WAVES, int DEPTH>
+//
+// An operand's lane l holds row l % 16, so loaded straight into registers every
+// four neighbouring lanes would ask for four cache lines, one after the other
+// (measured: 42 cycles an instruction, 15.4 us for 8x8192x8192 whatever is kept
+// in flight).  So a step's rows go to LDS by direct copies whose neighbouring
+// lanes copy neighbouring bytes, STAGES steps ahead, and are read from there:
+//   codes   channels NF*r + f together, 64 bytes each, piece p at p ^ (r / 4)
+//   tokens  256 bytes a row, chunk c of row r at c ^ (r % 16)
+//   scales  the 4-byte words of each channel that hold the step's
+// (both orders spread the 16 rows of an operand read over all banks).  A wave
+// waits for its own copies only; there is no barrier before the sums.  Every
+// step issues the same copies, those behind the wave's last from empty buffers,
+// so that one count waits for all of them, and the loop has one copy of its
+// body: the instructions of a launch come from memory once more, about 0.1 us
+// for 128 bytes of them, which a call of few microseconds notices.
+template <int IN, int GS, int NA, int NF, int WAVES, int STAGES>
 __global__ void __launch_bounds__(64 * WAVES)
 w4_narrow(W4Args args)
 {
+    constexpr int MT = (NA + 3) / 4;                                // operands of 16 tokens
     constexpr int NS = GS == kCoarse ? 1 : GS == kGroup64 ? 2 : 4;  // scales per step
     constexpr int PER = 4 / NS;                                     // instructions per scale
-    __shared__ floatx4 part[WAVES][MT * NF][64];
+    constexpr int CH = 16 * NF;                                     // channels
+    constexpr int WORDS = NS / 2 + 1;                               // 4-byte words that NS scales may touch
+    constexpr int COPY_S = (WORDS * CH + 63) / 64;
+    constexpr int COPIES = NF + NA + COPY_S;
+    constexpr int AT_A = 1024 * NF, AT_S = AT_A + 1024 * NA;
+    constexpr int SLOT = AT_S + 256 * COPY_S;
+    constexpr int RING = STAGES * SLOT > 1024 * MT * NF ? STAGES * SLOT : 1024 * MT * NF;
+    static_assert(NA < 4 ? 4 % NA == 0 : NA % 4 == 0, "whole operands, or an even part of one");
+    static_assert(COPIES * (STAGES - 1) < 64, "vmcnt is 6 bits");
+    static_assert(WAVES * RING <= 160 * 1024, "gfx950 has 160 KiB of LDS per workgroup");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[WAVES * RING];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    lds_u8 *const lds = (lds_u8 *)smem + wave * RING;
+    const uint32_t lds_base = (uint32_t)(uintptr_t)lds;
     GroupTile gt;
-    if (!find_row_tile(args.groups, 16 * MT, args.tiles_n, args.group_m, gt))
+    if (!find_row_tile(args.groups, 4 * NA, args.tiles_n, args.group_m, gt))
         return;
-    const int row0 = gt.start + gt.tm * 16 * MT;
-    const int rows = min(gt.rows - gt.tm * 16 * MT, 16 * MT);
-    const int n0 = gt.tn * 16 * NF;
+    const int row0 = gt.start + gt.tm * 4 * NA;
+    const int rows = min(gt.rows - gt.tm * 4 * NA, 4 * NA);
+    const int n0 = gt.tn * CH;
     const int cols = args.N - n0;
     const int K = args.K, KB = (K + 1) / 2, KA = 2 * K;
     const int groups_k = (K + (1 << args.shift) - 1) >> args.shift;
     const int r = lane & 15, kg = lane >> 4;
-    const __amdgpu_buffer_rsrc_t rsA = make_rsrc(args.A + (int64_t)row0 * args.lda);
-    const __amdgpu_buffer_rsrc_t rsQ =
-        make_rsrc(args.Q + (int64_t)gt.group * args.groups.stride + (int64_t)n0 * args.ldq);
-    const __amdgpu_buffer_rsrc_t rsS = make_rsrc(args.S + (int64_t)gt.group * args.stride_s + (int64_t)n0 * args.lds);
-    // 32-bit offsets of rows: the host checks that a tile's rows span less than 2 GiB
-    uint32_t offA[MT], offQ[NF], offS[NF];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-        offA[m] = 16 * m + r < rows ? (uint32_t)(2 * (16 * m + r) * (int)args.lda) : kOOB;
-#pragma unroll
-    for (int f = 0; f < NF; ++f) {
-        const int c = NF * r + f;
-        offQ[f] = c < cols ? (uint32_t)(c * (int)args.ldq) : kOOB;
-        offS[f] = c < cols ? (uint32_t)(2 * c * (int)args.lds) : kOOB;
-    }
+    const uint16_t *const Ap = args.A + (int64_t)row0 * args.lda;
+    const uint8_t *const Qp = args.Q + (int64_t)gt.group * args.groups.stride + (int64_t)n0 * args.ldq;
+    const uint16_t *const Sp = args.S + (int64_t)gt.group * args.stride_s + (int64_t)n0 * args.lds;
+    const int odd = (int)(reinterpret_cast<uintptr_t>(Sp) >> 1 & 1);  // Sp lies in the middle of a word
     const int steps = (K + 127) / 128, full = K / 128;
     const int per = (steps + WAVES - 1) / WAVES;
     const int s0 = min(wave * per, steps), s1 = min(s0 + per, steps);
 
-    u32x4 rq[DEPTH][NF], ra[DEPTH][MT][4];
-    uint32_t rs[DEPTH][NF][NS];
-    auto issue = [&](int d, int s) __attribute__((always_inline)) {
-        if (s < full) {
+    // ---- copies
+    // 32-bit offsets of rows: the host checks that a tile's rows span less than 2 GiB
+    const int rowQ = lane >> 2, pieceQ = (lane & 3) ^ (lane >> 4);
+    const int rowA = lane >> 4;
+    uint32_t offQ[NF];
 #pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                rq[d][f] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsQ, offQ[f] + 16 * kg,
-                                                                                           64 * s, 0));
-                if constexpr (GS == kCoarse) {
-                    rs[d][f][0] = __builtin_amdgcn_raw_buffer_load_b16(rsS, offS[f], 2 * (s >> (args.shift - 7)), 0);
-                } else if constexpr (GS == kGroup64) {
-                    const uint32_t x = __builtin_amdgcn_raw_buffer_load_b32(rsS, offS[f], 4 * s, 0);
-                    rs[d][f][0] = x & 0xFFFFu;
-                    rs[d][f][1] = x >> 16;
-                } else {
-                    const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rsS, offS[f], 8 * s, 0));
-                    rs[d][f][0] = x[0] & 0xFFFFu;
-                    rs[d][f][1] = x[0] >> 16;
-                    rs[d][f][2] = x[1] & 0xFFFFu;
-                    rs[d][f][3] = x[1] >> 16;
-                }
-            }
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    ra[d][m][j] = __builtin_bit_cast(
-                        u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsA, offA[m] + 2 * slot_value<GS>(j, kg), 256 * s, 0));
-            return;
-        }
-        // the step that K ends in
+    for (int f = 0; f < NF; ++f)
+        offQ[f] = NF * rowQ + f < cols ? (uint32_t)((NF * rowQ + f) * (int)args.ldq) : kOOB;
+    i32x4 rsA = make_rsrc4(Ap), rsQ = make_rsrc4(Qp), rsS = make_rsrc4(Sp - odd);
+    auto issue = [&](int s) __attribute__((always_inline)) {
+        const uint32_t to = lds_base + (s - s0) % STAGES * SLOT;
+        rsA[2] = rsQ[2] = rsS[2] = s < s1 ? kNumRecords : 0;
+        const bool end = s == full;
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
-            const int at = 64 * s + 16 * kg;
-            if (KB >= 16)
-                rq[d][f] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                         rsQ, end_offset(offQ[f], at, KB), 0, 0));
-            else
-                rq[d][f] = short_row<1>(rsQ, offQ[f], at, KB);
-#pragma unroll
-            for (int g = 0; g < NS; ++g) {
-                const int i = GS == kCoarse ? s >> (args.shift - 7) : NS * s + g;
-                rs[d][f][g] = __builtin_amdgcn_raw_buffer_load_b16(
-                    rsS, offS[f] != kOOB && i < groups_k ? offS[f] + 2 * i : kOOB, 0, 0);
-            }
+            const uint32_t off = offQ[f] + 16 * pieceQ;
+            dma16(rsQ, to + 1024 * f, end ? end_offset(offQ[f], 64 * s + 16 * pieceQ, KB) : off, end ? 0 : 64 * s);
         }
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int q = 0; q < NA; ++q) {
+            const int row = 4 * q + rowA, chunk = (lane & 15) ^ (row & 15);
+            const uint32_t off = row < rows ? (uint32_t)(2 * row * (int)args.lda) : kOOB;
+            dma16(rsA, to + AT_A + 1024 * q, end ? end_offset(off, 256 * s + 16 * chunk, KA) : off + 16 * chunk,
+                  end ? 0 : 256 * s);
+        }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int at = 256 * s + 2 * slot_value<GS>(j, kg);
-                if (KA >= 16)
-                    ra[d][m][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                                rsA, end_offset(offA[m], at, KA), 0, 0));
-                else
-                    ra[d][m][j] = short_row<2>(rsA, offA[m], at, KA);
-            }
+        for (int q = 0; q < COPY_S; ++q) {
+            const int c = (64 * q + lane) % CH, word = (64 * q + lane) / CH;
+            const int first = GS == kCoarse ? s >> (args.shift - 7) : NS * s;
+            const int i = odd + c * (int)args.lds + first;   // in 16-bit values from the aligned base
+            const bool ok = c < cols && word < WORDS && 2 * (i / 2 + word) < i + min(NS, groups_k - first);
+            dma4(rsS, to + AT_S + 256 * q, ok ? (uint32_t)(4 * (i / 2 + word)) : kOOB);
+        }
     };
+
     floatx4 acc[MT][NF];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int f = 0; f < NF; ++f)
             acc[m][f] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-    auto multiply = [&](int d, int s) __attribute__((always_inline)) {
-        if (s >= full) {
-            if (KB >= 16)
-#pragma unroll
-                for (int f = 0; f < NF; ++f)
-                    rq[d][f] = end_shift(rq[d][f], KB - (64 * s + 16 * kg));
-            if (KA >= 16)
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        ra[d][m][j] = end_shift(ra[d][m][j], KA - (256 * s + 2 * slot_value<GS>(j, kg)));
-        }
+    auto multiply = [&](const u32x4 (&rq)[NF], const u32x4 (&ra)[MT][4], const float (&scale)[NF][NS])
+        __attribute__((always_inline)) {
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
-            const u32x4 w = deal_codes<GS>(rq[d][f]);
+            const u32x4 w = deal_codes<GS>(rq[f]);
             half8 b[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 b[j] = codes8<IN>(w[j]);
 #pragma unroll
-            for (int g = 0; g < NS; ++g) {
-                const float scale = scale_value<IN>(rs[d][f][g]);
+            for (int g = 0; g < NS; ++g)
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     floatx4 p = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int j = g * PER; j < (g + 1) * PER; ++j)
-                        p = mfma16<IN>(__builtin_bit_cast(half8, ra[d][m][j]), b[j], p);
+                        p = mfma16<IN>(__builtin_bit_cast(half8, ra[m][j]), b[j], p);
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
-                        acc[m][f][v] = __builtin_fmaf(scale, p[v], acc[m][f][v]);
+                        acc[m][f][v] = __builtin_fmaf(scale[f][g], p[v], acc[m][f][v]);
                 }
-            }
         }
     };
+    u32x4 rq[NF], ra[MT][4];
+    float scale[NF][NS];
+    if (full > 0) {
+        for (int d = 0; d < STAGES - 1; ++d)
+            issue(s0 + d);
+        for (int s = s0; s < s1; ++s) {
+            // (what was read from the slot that is filled now has arrived)
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            issue(s + STAGES - 1);
+            wait_vmcnt<COPIES * (STAGES - 1)>();
+            const lds_u8 *const from = lds + (s - s0) % STAGES * SLOT;
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-        if (s0 + d < s1)
-            issue(d, s0 + d);
-    for (int s = s0; s < s1; s += DEPTH) {
+            for (int f = 0; f < NF; ++f) {
+                const int c = NF * r + f;
+                rq[f] = *(const lds_u32x4 *)(from + 1024 * f + 64 * r + 16 * (kg ^ (r >> 2)));
+                const int i = odd + c * (int)args.lds + (GS == kCoarse ? s >> (args.shift - 7) : 0);
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-            if (s + d < s1) {
-                multiply(d, s + d);
-                if (s + d + DEPTH < s1)
-                    issue(d, s + d + DEPTH);
+                for (int g = 0; g < NS; ++g) {
+                    const int at = (i & 1) + g;
+                    const uint32_t x = *(const __attribute__((address_space(3))) uint16_t *)(
+                        from + AT_S + 4 * ((at >> 1) * CH + c) + 2 * (at & 1));
+                    scale[f][g] = scale_value<IN>(x);
+                }
             }
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    // (operand rows without a token repeat those of the others)
+                    const int row = NA < 4 ? r % (4 * NA) : 16 * m + r;
+                    ra[m][j] = *(const lds_u32x4 *)(from + AT_A + 256 * row +
+                                                    16 * ((slot_value<GS>(j, kg) / 8) ^ (row & 15)));
+                }
+            if (s == full) {
+                // K ends in this step
+#pragma unroll
+                for (int f = 0; f < NF; ++f) {
+                    rq[f] = end_shift(rq[f], KB - (64 * s + 16 * kg));
+                    if constexpr (NS > 1)
+#pragma unroll
+                        for (int g = 0; g < NS; ++g)
+                            scale[f][g] = NS * s + g < groups_k ? scale[f][g] : 0.0f;
+                }
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        ra[m][j] = end_shift(ra[m][j], KA - (256 * s + 2 * slot_value<GS>(j, kg)));
+            }
+            multiply(rq, ra, scale);
         }
+    } else if (s0 < s1) {
+        // K < 128: the only step, by single values
+        const __amdgpu_buffer_rsrc_t bA = make_rsrc(Ap), bQ = make_rsrc(Qp), bS = make_rsrc(Sp);
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            const int c = NF * r + f;
+            rq[f] = short_row<1>(bQ, c < cols ? (uint32_t)(c * (int)args.ldq) : kOOB, 16 * kg, KB);
+#pragma unroll
+            for (int g = 0; g < NS; ++g)
+                scale[f][g] = scale_value<IN>(__builtin_amdgcn_raw_buffer_load_b16(
+                    bS, c < cols && g < groups_k ? (uint32_t)(2 * (c * (int)args.lds + g)) : kOOB, 0, 0) & 0xFFFFu);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                ra[m][j] = short_row<2>(bA, 16 * m + r < rows ? (uint32_t)(2 * (16 * m + r) * (int)args.lda) : kOOB,
+                                        2 * slot_value<GS>(j, kg), KA);
+        multiply(rq, ra, scale);
     }
+    wait_vmcnt<0>();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    typedef __attribute__((address_space(3))) floatx4 lds_f32x4;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int f = 0; f < NF; ++f)
-            part[wave][m * NF + f][lane] = acc[m][f];
+            *(lds_f32x4 *)(lds + 1024 * (m * NF + f) + 16 * lane) = acc[m][f];
     __syncthreads();
     const int c = NF * r;
     const int left = cols - c;
     for (int m = wave; m < MT; m += WAVES) {
         floatx4 sum[NF];
 #pragma unroll
-        for (int f = 0; f < NF; ++f) {
-            sum[f] = part[0][m * NF + f][lane];
+        for (int f = 0; f < NF; ++f)
+            sum[f] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int w = 0; w < WAVES; ++w)
 #pragma unroll
-            for (int w = 1; w < WAVES; ++w)
-                sum[f] += part[w][m * NF + f][lane];
-        }
+            for (int f = 0; f < NF; ++f)
+                sum[f] += *(const lds_f32x4 *)((lds_u8 *)smem + w * RING + 1024 * (m * NF + f) + 16 * lane);
         if (left <= 0)
             continue;
         float bias[NF];
@@ -353,31 +397,41 @@ w4_narrow(W4Args args)
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: token tiles through LDS
+// Many tokens: token tiles shared by the waves
 // ---------------------------------------------------------------------------
-// A workgroup makes BM tokens x 16*NF*NW channels.  Its token tile (BM x 256
-// values, K-contiguous) goes through two LDS buffers by direct copies; each
-// wave has channels of its own, whose codes come straight into registers, two K
-// tiles ahead, and are expanded once, one register of them beside each 16 tokens'
-// matrix instructions.  Per step of 128 values and 16 tokens x 16 channels the
-// group's sum is a chain of matrix instructions of its own, joined to the running
-// sum by the scale.
-// LDS: chunk c (16 bytes) of row r stands at c ^ (r % 16), so the 16 rows of
-// an operand read touch all banks once.
+// A workgroup makes BM tokens x 16*NF*NW channels in steps of 128 values of K.
+// All waves read the tokens of a step from LDS; each has channels of its own,
+// whose codes it expands once, in registers, one step ahead and between the
+// matrix instructions of the step before (an expansion into LDS would be read
+// by no one else and cost the LDS as much again).  Per step and 16 x 16 outputs
+// the sum of a group is a chain of matrix instructions of its own, joined to the
+// running sum by the scale.
+// Tokens, codes and scales come by direct copies, laid out as in w4_narrow, into
+// three slots each.  Before its last 16 tokens' instructions, whose operands are
+// in registers, a step publishes the next: it waits for that one's tokens and
+// scales and the codes of the one behind it (a later batch stays in flight),
+// passes the barrier, and goes on with the next step's first reads underway; that
+// one issues the batch that takes the slots it freed, a few copies after each 16
+// tokens.  The sums of 16 tokens join the running ones beside the next 16 tokens'
+// instructions.
 template <int IN_, int GS_, int BM_, int NF_, int NW_>
 struct W4Cfg {
     static constexpr int IN = IN_, GS = GS_, BM = BM_, NF = NF_, NW = NW_;
-    static constexpr int BN = 16 * NF * NW, BK = 256, NT = 64 * NW;
+    static constexpr int BN = 16 * NF * NW, BK = 128, STAGES = 3, NT = 64 * NW;
     static constexpr int FM = BM / 16;
-    static constexpr int ROW = 2 * BK;                  // bytes of a row of the tile
-    static constexpr int BUF = BM * ROW;
-    static constexpr int COPIES = BUF / 1024 / NW;      // per wave and tile
-    static constexpr int NS = GS == kCoarse ? 1 : GS == kGroup64 ? 2 : 4;
-    static constexpr int PER = 4 / NS;
-    static constexpr int EXPAND = 4 * NF / FM;          // registers of codes per 16 tokens
-    static_assert(COPIES >= 1 && BUF % (1024 * NW) == 0, "copies split evenly over waves");
-    static_assert(EXPAND >= 1 && (4 * NF) % FM == 0, "codes are expanded evenly over the tokens");
-    static_assert(2 * BUF <= 160 * 1024, "gfx950 has 160 KiB of LDS per workgroup");
+    static constexpr int NS = GS == kCoarse ? 1 : GS == kGroup64 ? 2 : 4;  // scales per step
+    static constexpr int PER = 4 / NS;                                     // instructions per scale
+    static constexpr int CH = 16 * NF;                                     // channels of a wave
+    static constexpr int WORDS = NS / 2 + 1;                               // 4-byte words that NS scales may touch
+    static constexpr int COPY_A = BM / 4 / NW, COPY_S = (WORDS * CH + 63) / 64;
+    static constexpr int COPIES = COPY_A + NF + COPY_S;                    // of a wave and step
+    static constexpr int BUF_A = 256 * BM, BUF_Q = 1024 * NF, BUF_S = 256 * COPY_S;  // (Q and S: of a wave)
+    static constexpr int AT_Q = STAGES * BUF_A, AT_S = AT_Q + STAGES * NW * BUF_Q;
+    static constexpr int LDS_BYTES = AT_S + STAGES * NW * BUF_S;
+    static constexpr int EXPAND = (4 * NF + FM - 1) / FM;                  // registers of codes per 16 tokens
+    static_assert(BM % (4 * NW) == 0, "copies split evenly over waves");
+    static_assert(COPIES * 2 < 64, "vmcnt is 6 bits");
+    static_assert(LDS_BYTES <= 160 * 1024, "gfx950 has 160 KiB of LDS per workgroup");
 };
 
 template <class Cfg>
@@ -385,8 +439,8 @@ __global__ void __launch_bounds__(Cfg::NT)
 w4_tile(W4Args args)
 {
     constexpr int IN = Cfg::IN, GS = Cfg::GS, BM = Cfg::BM, NF = Cfg::NF, NW = Cfg::NW, FM = Cfg::FM;
-    constexpr int NS = Cfg::NS, PER = Cfg::PER;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * Cfg::BUF];
+    constexpr int NS = Cfg::NS, PER = Cfg::PER, CH = Cfg::CH, STAGES = Cfg::STAGES;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[Cfg::LDS_BYTES];
     lds_u8 *const lds = (lds_u8 *)smem;
     const uint32_t lds_base = (uint32_t)(uintptr_t)lds;
     const int lane = threadIdx.x & 63;
@@ -396,111 +450,88 @@ w4_tile(W4Args args)
         return;
     const int row0 = gt.start + gt.tm * BM;
     const int rows = gt.rows - gt.tm * BM;               // > 0
-    const int n0 = gt.tn * Cfg::BN + wave * 16 * NF;     // this wave's channels
-    const int cols = args.N - n0;
+    const int n0 = gt.tn * Cfg::BN + wave * CH;          // this wave's channels
+    const int cols = args.N - n0;                        // (none: it only copies)
     const int K = args.K, KB = (K + 1) / 2, KA = 2 * K;
     const int groups_k = (K + (1 << args.shift) - 1) >> args.shift;
     const int r = lane & 15, kg = lane >> 4;
     const uint16_t *const Ap = args.A + (int64_t)row0 * args.lda;
-    const int num_k = (K + 255) / 256;
+    const int64_t first = cols > 0 ? n0 : 0;
+    const uint8_t *const Qp = args.Q + (int64_t)gt.group * args.groups.stride + first * args.ldq;
+    const uint16_t *const Sp = args.S + (int64_t)gt.group * args.stride_s + first * args.lds;
+    const int odd = (int)(reinterpret_cast<uintptr_t>(Sp) >> 1 & 1);  // Sp lies in the middle of a word
+    const int steps = (K + 127) / 128, full = K / 128;
 
-    // ---- token copies: copy q of this wave fills rows 2*(q*NW + wave), + 1
-    const i32x4 rsA = make_rsrc4(Ap);
-    uint32_t voff[Cfg::COPIES];
+    // ---- copies, as in w4_narrow
+    const int pieceQ = (lane & 3) ^ (lane >> 4), rowA = lane >> 4;
+    uint32_t offA[Cfg::COPY_A], offQ[NF];
 #pragma unroll
-    for (int q = 0; q < Cfg::COPIES; ++q) {
-        const int row = 2 * (q * NW + wave) + (lane >> 5);
-        const int chunk = (lane & 31) ^ (row & 15);
-        voff[q] = row < rows ? (uint32_t)(row * (int)args.lda * 2 + 16 * chunk) : kOOB;
+    for (int q = 0; q < Cfg::COPY_A; ++q) {
+        const int row = 4 * (q * NW + wave) + rowA;
+        const int chunk = (lane & 15) ^ (row & 15);
+        offA[q] = row < rows ? (uint32_t)(2 * row * (int)args.lda + 16 * chunk) : kOOB;
     }
-    auto copy_tokens = [&](int t) __attribute__((always_inline)) {
-        const uint32_t region = lds_base + (t & 1) * Cfg::BUF;
-        const int left = KA - 512 * t;                   // bytes of a row from this tile on
+    int firstS[Cfg::COPY_S];
+    bool okS[Cfg::COPY_S];
 #pragma unroll
-        for (int q = 0; q < Cfg::COPIES; ++q) {
-            uint32_t off = voff[q];
-            if (left < 512) {
-                const int row = 2 * (q * NW + wave) + (lane >> 5);
-                const int chunk = (lane & 31) ^ (row & 15);
-                if (16 * chunk + 16 > left)
-                    off = kOOB;
-            }
-            dma16(rsA, region + (q * NW + wave) * 1024, off, 512 * t);
-        }
-    };
-    // The chunk that K ends inside, into the places where the copies wrote
-    // zeros: one row per thread.
-    auto fill_end = [&](int t) __attribute__((always_inline)) {
-        const int left = KA - 512 * t;
-        const int chunk = left / 16, bytes = left % 16;
-        for (int row = threadIdx.x; row < BM && row < rows; row += Cfg::NT) {
-            u32x4 v;
-            const uint16_t *const a = Ap + (int64_t)row * args.lda;
-            if (K >= 8) {
-                v = end_shift(*(const u32x4_any *)(a + K - 8), bytes);
-            } else {
-                unsigned __int128 x = 0;
-                for (int e = 0; e < K; ++e)
-                    x |= (unsigned __int128)a[e] << (16 * e);
-                v = __builtin_bit_cast(u32x4, x);
-            }
-            *(lds_u32x4 *)(lds + (t & 1) * Cfg::BUF + row * 512 + 16 * (chunk ^ (row & 15))) = v;
-        }
-    };
-
-    // ---- codes and scales
-    const bool works = cols > 0;
-    const __amdgpu_buffer_rsrc_t rsQ =
-        make_rsrc(args.Q + (int64_t)gt.group * args.groups.stride + (int64_t)(works ? n0 : 0) * args.ldq);
-    const __amdgpu_buffer_rsrc_t rsS =
-        make_rsrc(args.S + (int64_t)gt.group * args.stride_s + (int64_t)(works ? n0 : 0) * args.lds);
-    uint32_t offQ[NF], offS[NF];
+    for (int q = 0; q < Cfg::COPY_S; ++q) {
+        const int c = (64 * q + lane) % CH;
+        firstS[q] = odd + c * (int)args.lds;
+        okS[q] = c < cols && (64 * q + lane) / CH < Cfg::WORDS;
+    }
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
-        const int c = NF * r + f;
+        const int c = NF * (lane >> 2) + f;
         offQ[f] = c < cols ? (uint32_t)(c * (int)args.ldq) : kOOB;
-        offS[f] = c < cols ? (uint32_t)(2 * c * (int)args.lds) : kOOB;
     }
-    u32x4 raw[2][2][NF];     // [tile % 2][step][channel]
-    uint32_t scales[2][2][NF][NS];
-    auto load_codes = [&](u32x4 (&to)[2][NF], int t) __attribute__((always_inline)) {
-        const bool whole = 256 * t + 256 <= K;
+    i32x4 rsA = make_rsrc4(Ap), rsQ = make_rsrc4(Qp), rsS = make_rsrc4(Sp - odd);
+    // Copy q of batch s: tokens and scales of step s into slot `slot`, codes of
+    // step s + 1 into the next.
+    auto next_slot = [](int slot) __attribute__((always_inline)) { return slot + 1 == STAGES ? 0 : slot + 1; };
+    auto copy_codes = [&](int s, int slot, int f) __attribute__((always_inline)) {
+        rsQ[2] = s < steps ? kNumRecords : 0;
+        const bool end = s == full;
+        const uint32_t off = end ? end_offset(offQ[f], 64 * full + 16 * pieceQ, KB) : offQ[f] + 16 * pieceQ;
+        dma16(rsQ, lds_base + Cfg::AT_Q + (slot * NW + wave) * Cfg::BUF_Q + 1024 * f, off, end ? 0 : 64 * s);
+    };
+    auto copy_one = [&](int s, int slot, int q) __attribute__((always_inline)) {
+        if (q < Cfg::COPY_A) {
+            rsA[2] = s < steps ? kNumRecords : 0;
+            // (the chunk that K ends inside is filled by fill_end)
+            const int chunk = (lane & 15) ^ ((4 * (q * NW + wave) + rowA) & 15);
+            const int left = s == full ? KA - 256 * full : 256;
+            dma16(rsA, lds_base + slot * Cfg::BUF_A + 1024 * (NW * q + wave), 16 * chunk + 16 > left ? kOOB : offA[q],
+                  256 * s);
+        } else if (q < Cfg::COPY_A + Cfg::COPY_S) {
+            q -= Cfg::COPY_A;
+            rsS[2] = s < steps ? kNumRecords : 0;
+            const int word = (64 * q + lane) / CH;
+            const int g = GS == kCoarse ? s >> (args.shift - 7) : NS * s;
+            const int i = firstS[q] + g;                 // in 16-bit values from the aligned base
+            const bool ok = (i & ~1) + 2 * word < i + min(NS, groups_k - g);
+            dma4(rsS, lds_base + Cfg::AT_S + (slot * NW + wave) * Cfg::BUF_S + 256 * q,
+                 okS[q] && ok ? (uint32_t)(2 * (i & ~1) + 4 * word) : kOOB);
+        } else {
+            copy_codes(s + 1, next_slot(slot), q - Cfg::COPY_A - Cfg::COPY_S);
+        }
+    };
+    auto copy_batch = [&](int s, int slot) __attribute__((always_inline)) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int q = 0; q < Cfg::COPIES; ++q)
+            copy_one(s, slot, q);
+    };
+    // The chunk that K ends inside, into the places where this wave's own
+    // copies wrote zeros.
+    auto fill_end = [&](int slot) __attribute__((always_inline)) {
+        const int left = KA - 256 * full, chunk = left / 16;
 #pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                const int at = 128 * t + 64 * h + 16 * kg;
-                if (whole)
-                    to[h][f] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                             rsQ, offQ[f] + 64 * h + 16 * kg, 128 * t, 0));
-                else if (KB >= 16)
-                    to[h][f] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                             rsQ, end_offset(offQ[f], at, KB), 0, 0));
-                else
-                    to[h][f] = short_row<1>(rsQ, offQ[f], at, KB);
+        for (int q = 0; q < Cfg::COPY_A; ++q) {
+            const int row = 4 * (q * NW + wave) + rowA;
+            if ((lane & 15) == 0 && row < rows) {
+                const u32x4 v = *(const u32x4_any *)(Ap + (int64_t)row * args.lda + K - 8);
+                *(lds_u32x4 *)(lds + slot * Cfg::BUF_A + 256 * row + 16 * (chunk ^ (row & 15))) = end_shift(v, left % 16);
             }
-    };
-    // (only a row's end is shifted, and tiles behind K have none)
-    auto end_codes = [&](u32x4 (&to)[2][NF], int t) __attribute__((always_inline)) {
-        if (256 * t + 256 <= K || KB < 16)
-            return;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int f = 0; f < NF; ++f)
-                to[h][f] = end_shift(to[h][f], KB - (128 * t + 64 * h + 16 * kg));
-    };
-    auto load_scales = [&](uint32_t (&to)[2][NF][NS], int t) __attribute__((always_inline)) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int f = 0; f < NF; ++f)
-#pragma unroll
-                for (int g = 0; g < NS; ++g) {
-                    const int i = GS == kCoarse ? (2 * t + h) >> (args.shift - 7) : NS * (2 * t + h) + g;
-                    to[h][f][g] = __builtin_amdgcn_raw_buffer_load_b16(
-                        rsS, offS[f] != kOOB && i < groups_k ? offS[f] + 2 * i : kOOB, 0, 0);
-                }
+        }
     };
 
     floatx4 acc[FM][NF];
@@ -510,118 +541,172 @@ w4_tile(W4Args args)
         for (int f = 0; f < NF; ++f)
             acc[i][f] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
     half8 code[2][NF][4];    // [step % 2][channel][instruction]
-    u32x4 dealt[NF];         // the next step's codes, before they are expanded
-    auto expand = [&](int set, int n) __attribute__((always_inline)) {
-        code[set][n / 4][n % 4] = codes8<IN>(dealt[n / 4][n % 4]);
-    };
-
-    if (num_k > 0) {
-        copy_tokens(0);
-        if (works) {
-            load_codes(raw[0], 0);
-            load_codes(raw[1], 1);
-            load_scales(scales[0], 0);
-            end_codes(raw[0], 0);
+    u32x4 raw[NF];           // the next step's, before they are expanded
+    auto read_codes = [&](int s, int slot) __attribute__((always_inline)) {
+        const lds_u8 *const from = lds + Cfg::AT_Q + (slot * NW + wave) * Cfg::BUF_Q + 64 * r + 16 * (kg ^ (r >> 2));
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+            raw[f] = *(const lds_u32x4 *)(from + 1024 * f);
+        if (s == full)
 #pragma unroll
             for (int f = 0; f < NF; ++f)
-                dealt[f] = deal_codes<GS>(raw[0][0][f]);
+                raw[f] = end_shift(raw[f], KB - (64 * s + 16 * kg));
+    };
+    auto expand = [&](int set, int n) __attribute__((always_inline)) {
+        if (n < 4 * NF) {
+            if (n % 4 == 0)
+                raw[n / 4] = deal_codes<GS>(raw[n / 4]);
+            code[set][n / 4][n % 4] = codes8<IN>(raw[n / 4][n % 4]);
+            // (here, and not where the next step uses them)
+            asm volatile("" : "+v"(code[set][n / 4][n % 4]));
+        }
+    };
+    half8 a[2][4];           // operands of 16 tokens, and of the next
+    auto read_tokens = [&](int set, int slot, int i) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            a[set][j] = *(const __attribute__((address_space(3))) half8 *)(
+                lds + slot * Cfg::BUF_A + 4096 * i + 256 * r + 16 * ((slot_value<GS>(j, kg) / 8) ^ r));
+    };
+    float scale[2][NF][NS];  // [step % 2]
+    auto read_scales = [&](int set, int s, int slot) __attribute__((always_inline)) {
+        const lds_u8 *const from = lds + Cfg::AT_S + (slot * NW + wave) * Cfg::BUF_S;
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            const int c = NF * r + f;
+            const int i = odd + c * (int)args.lds + (GS == kCoarse ? s >> (args.shift - 7) : 0);
+#pragma unroll
+            for (int g = 0; g < NS; ++g) {
+                const int at = (i & 1) + g;
+                scale[set][f][g] = scale_value<IN>(*(const __attribute__((address_space(3))) uint16_t *)(
+                    from + 4 * ((at >> 1) * CH + c) + 2 * (at & 1)));
+                if (NS > 1 && s == full)
+                    scale[set][f][g] = NS * s + g < groups_k ? scale[set][f][g] : 0.0f;
+            }
+        }
+    };
+    constexpr bool LATER = NS == 1;   // sums join a step of 16 tokens later (fine groups have too many)
+    floatx4 p[LATER ? 2 : 1][NF][NS];
+    auto join = [&](int set, int sums, int i) __attribute__((always_inline)) {
+#pragma unroll
+        for (int g = 0; g < NS; ++g)
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    acc[i][f][v] = __builtin_fmaf(scale[set][f][g], p[sums][f][g][v], acc[i][f][v]);
+        // (here, and not where the next sums join: those would wait in registers)
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+            asm volatile("" : "+v"(acc[i][f]));
+    };
+    const bool works = cols > 0;
+
+    // Makes step s visible; LEFT later copies of this wave may be in flight.
+    auto publish = [&](int s, int slot, auto later) __attribute__((always_inline)) {
+        if (s == full && (KA & 15) != 0) {
+            wait_vmcnt<0>();
+            fill_end(slot);
+        } else {
+            wait_vmcnt<decltype(later)::value>();
+        }
+        __syncthreads();
+    };
+    if (steps > 0) {
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+            copy_codes(0, 0, f);
+        copy_batch(0, 0);
+        copy_batch(1, 1);
+        wait_vmcnt<2 * Cfg::COPIES>();
+        if (works) {
+            read_codes(0, 0);
 #pragma unroll
             for (int n = 0; n < 4 * NF; ++n)
                 expand(0, n);
         }
-    }
-    // One K tile, P = t % 2 (so that registers are named at compile time).
-    auto tile = [&](int t, auto parity) __attribute__((always_inline)) {
-        constexpr int P = decltype(parity)::value;
-        wait_vmcnt<0>();
-        if (t == num_k - 1 && (KA & 15) != 0)
-            fill_end(t);
-        __syncthreads();
-        if (t + 1 < num_k)
-            copy_tokens(t + 1);
-        if (!works)
-            return;
-        // what landed before the barrier is taken here, so that no wait for it
-        // comes behind the loads below
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                asm volatile("" : "+v"(raw[0][h][f]), "+v"(raw[1][h][f]));
-#pragma unroll
-                for (int g = 0; g < NS; ++g)
-                    asm volatile("" : "+v"(scales[P][h][f][g]));
-            }
-        end_codes(raw[P ^ 1], t + 1);
-        const u32x4 *const second = raw[P][1];
-        u32x4 later[NF];
-#pragma unroll
-        for (int f = 0; f < NF; ++f)
-            later[f] = second[f];
-        load_scales(scales[P ^ 1], t + 1);
-        u32x4 fresh[2][NF];
-        load_codes(fresh, t + 2);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float s[NF][NS];
-#pragma unroll
-            for (int f = 0; f < NF; ++f)
-#pragma unroll
-                for (int g = 0; g < NS; ++g)
-                    s[f][g] = scale_value<IN>(scales[P][h][f][g]);
-#pragma unroll
-            for (int f = 0; f < NF; ++f)
-                dealt[f] = deal_codes<GS>(h == 0 ? later[f] : raw[P ^ 1][0][f]);
-            half8 a[2][4];
-            auto read = [&](int set, int i) __attribute__((always_inline)) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int chunk = (16 * h + slot_value<GS>(j, kg) / 8) ^ r;
-                    a[set][j] = *(const __attribute__((address_space(3))) half8 *)(lds + P * Cfg::BUF +
-                                                                                   (16 * i + r) * 512 + 16 * chunk);
-                }
-            };
-            read(0, 0);
-#pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                if (i + 1 < FM)
-                    read((i + 1) & 1, i + 1);
-                floatx4 p[NF][NS];
-#pragma unroll
-                for (int g = 0; g < NS; ++g)
-#pragma unroll
-                    for (int f = 0; f < NF; ++f)
-                        p[f][g] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int f = 0; f < NF; ++f)
-                        p[f][j / PER] = mfma16<IN>(a[i & 1][j], code[h][f][j], p[f][j / PER]);
-#pragma unroll
-                for (int e = 0; e < Cfg::EXPAND; ++e)
-                    expand(h ^ 1, i * Cfg::EXPAND + e);
-#pragma unroll
-                for (int g = 0; g < NS; ++g)
-#pragma unroll
-                    for (int f = 0; f < NF; ++f)
-#pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            acc[i][f][v] = __builtin_fmaf(s[f][g], p[f][g][v], acc[i][f][v]);
-            }
+        publish(0, 0, std::integral_constant<int, Cfg::COPIES>{});
+        if (works) {
+            read_tokens(0, 0, 0);
+            read_codes(1, 1);
+            read_scales(0, 0, 0);
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int f = 0; f < NF; ++f)
-                raw[P][h][f] = fresh[h][f];
-    };
-    for (int t = 0; t < num_k; t += 2) {
-        tile(t, std::integral_constant<int, 0>{});
-        if (t + 1 < num_k)
-            tile(t + 1, std::integral_constant<int, 1>{});
     }
-    if (!works)
+    // One step, P = s % 2 (so that registers are named at compile time).
+    int slot = 0;
+    auto step = [&](int s, auto parity) __attribute__((always_inline)) {
+        constexpr int P = decltype(parity)::value;
+        const int after = next_slot(slot), third = next_slot(after);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const bool last = i + 1 == FM;
+            if (last && s + 1 < steps) {
+                publish(s + 1, after, std::integral_constant<int, Cfg::COPIES>{});
+                read_tokens((i + 1) & 1, after, 0);
+                read_scales(P ^ 1, s + 1, after);
+            } else if (!last) {
+                read_tokens((i + 1) & 1, slot, i + 1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int g = 0; g < NS; ++g)
+#pragma unroll
+                for (int f = 0; f < NF; ++f)
+                    p[LATER ? i & 1 : 0][f][g] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int f = 0; f < NF; ++f) {
+                    floatx4 &sum = p[LATER ? i & 1 : 0][f][j / PER];
+                    sum = mfma16<IN>(a[i & 1][j], code[P][f][j], sum);
+                }
+            if constexpr (LATER) {
+                if (i > 0)
+                    join(P, (i - 1) & 1, i - 1);
+                else if (s > 0)
+                    join(P ^ 1, (FM - 1) & 1, FM - 1);
+            } else {
+                join(P, 0, i);
+            }
+#pragma unroll
+            for (int e = 0; e < Cfg::EXPAND; ++e)
+                expand(P ^ 1, i * Cfg::EXPAND + e);
+            __builtin_amdgcn_sched_barrier(0);
+            // a few copies at a time: all at once would hold up the wave
+            constexpr int SLICE = (Cfg::COPIES + FM - 2) / (FM - 1);
+            if (!last)
+#pragma unroll
+                for (int q = i * SLICE; q < (i + 1) * SLICE; ++q)
+                    if (q < Cfg::COPIES)
+                        copy_one(s + 2, third, q);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        read_codes(s + 2, third);
+        slot = after;
+    };
+    // A wave without channels only copies: the matrix cores are left to the
+    // waves with work.
+    if (!works) {
+        for (int s = 0; s + 1 < steps; ++s) {
+            slot = next_slot(slot);
+            copy_batch(s + 2, next_slot(slot));
+            publish(s + 1, slot, std::integral_constant<int, Cfg::COPIES>{});
+        }
+        wait_vmcnt<0>();
         return;
+    }
+    for (int s = 0; s < steps; s += 2) {
+        step(s, std::integral_constant<int, 0>{});
+        if (s + 1 < steps)
+            step(s + 1, std::integral_constant<int, 1>{});
+    }
+    if (LATER && steps > 0) {
+        if (steps % 2)
+            join(0, (FM - 1) & 1, FM - 1);
+        else
+            join(1, (FM - 1) & 1, FM - 1);
+    }
+    wait_vmcnt<0>();  // (copies from empty buffers: none may land in another workgroup's LDS)
     const int c = NF * r;
     const int left = cols - c;
     if (left <= 0)

@@ -124,10 +124,79 @@ def test_gemm_few_rows(dtype, group, M, N, K, gap, shift):
     check_gemm(M, N, K, group, dtype, dtype if N % 2 else F32, gap, shift, bias=M % 3 == 1)
 
 
+# kernel: (rows, columns, K) that take it
+KERNELS = {
+    "4x16": (3, 70, [128, 129, 260, 1025, 3000]),
+    "16x16": (19, 45, [128, 200, 385, 2049]),
+    "8x32, 8 waves": (7, 5001, [4096, 4111]),
+    "8x32, 4 waves": (5, 4501, [64, 127, 130, 515]),
+    "16x32, 8 waves": (16, 4700, [4096, 4230]),
+    "16x32, 4 waves": (14, 4801, [100, 131, 640, 777]),
+    "32x32": (29, 8190, [77, 128, 270, 513]),
+    "64x32": (61, 9001, [96, 128, 391, 905]),
+    "64x128": (70, 12500, [128, 135, 257, 650]),
+    "64x256": (63, 41001, [128, 129, 384, 523]),
+    "128x256": (130, 24601, [128, 264, 391, 777]),
+}
+
+
+def kernel(M, N, K, group, gap=0, groups=0):
+    k = mp.mpgemm_w4_query(groups, M, N, K, group, K + gap, (K + 1) // 2 + gap, -(-K // group) + gap)
+    name = f"{k['bm']}x{k['bn']}"
+    return f"{name}, {k['waves']} waves" if name in ("8x32", "16x32") else name
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("group", [32, 64, 128, 512])
-@pytest.mark.parametrize("M,N,K,gap,shift", [
-    (130, 33000, 64, 0, 0), (70, 33001, 1, 1, 1), (100, 32999, 300, 1, 1), (257, 16500, 513, 0, 0),
-    (65, 32800, 8, 8, 0), (129, 33000, 263, 0, 1)])
-def test_gemm_many_rows(dtype, group, M, N, K, gap, shift):
-    check_gemm(M, N, K, group, dtype, F32 if N % 2 else dtype, gap, shift, bias=M % 2 == 1)
+@pytest.mark.parametrize("name", list(KERNELS))
+def test_gemm_every_kernel(dtype, group, name):
+    M, N, depths = KERNELS[name]
+    for i, K in enumerate(depths):
+        gap, shift = (0, 0) if i % 2 == 0 else (1, 1)
+        assert kernel(M, N, K, group, gap) == name
+        check_gemm(M, N, K, group, dtype, [F32, dtype, F16 if dtype == BF16 else BF16][i % 3], gap, shift, bias=i == 1)
+
+
+def check_groups(sizes, behind, N, K, group, dtype, out, gap=0, shift=0, bias=False, start=0):
+    """Rows of each group by its own matrix; `behind` rows of none stay."""
+    G, M = len(sizes), start + sum(sizes) + behind
+    g = torch.Generator().manual_seed(M * 31 + N * 7 + K)
+    a = torch.randn(M, K, generator=g).to(dtype)
+    _, packed, scale = random_weights(g, N, K, group, dtype, G)
+    b = torch.randn(G, N, generator=g) if bias else None
+    A = Buffer(M, K, dtype, a, gap, shift)
+    Q = Buffer(G * N, (K + 1) // 2, torch.uint8, packed.view(G * N, -1), gap, shift)
+    S = Buffer(G * N, -(-K // group), dtype, scale.view(G * N, -1), gap, shift)
+    C = Buffer(M, N, out, gap=gap, shift=shift)
+    offsets = offsets_of(sizes) + start
+    mp.gemm_w4(A.view, Q.view.unflatten(0, (G, N)), S.view.unflatten(0, (G, N)), C.view, group=group,
+               bias=None if b is None else b.to(device()), offsets=offsets)
+    torch.cuda.synchronize()
+    before = torch.as_strided(C.before, C.view.shape, C.view.stride(), C.view.storage_offset())
+    at = start
+    for e, n in enumerate(sizes):
+        here = slice(at, at + n)
+        exact, mag = product(a[here], packed[e], scale[e], group, None if b is None else b[e])
+        assert_within(C.view[here], exact, bound(exact, mag, K, out, None if b is None else b[e]), f"group {e}")
+        at += n
+    for rest in (slice(0, start), slice(at, M)):
+        assert torch.equal(bits(C.view[rest].contiguous()), bits(before[rest].contiguous()))
+    assert untouched(C)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("sizes,behind,N,K,gap,shift,start", [
+    ([3, 0, 1, 7], 2, 33, 100, 1, 1, 0), ([0, 0, 0], 4, 40, 64, 0, 0, 0), ([1], 0, 16, 256, 0, 0, 0),
+    ([2, 0, 5, 1, 0, 9], 0, 3001, 390, 0, 0, 0), ([17, 40, 0, 3], 5, 2003, 257, 1, 1, 3),
+    ([100, 0, 300, 65], 7, 5003, 129, 0, 0, 0), ([200, 1, 0, 290], 1, 9003, 391, 1, 1, 2),
+    ([500, 0, 700], 3, 9000, 264, 0, 0, 0), ([70] * 9, 0, 45, 640, 3, 1, 1)])
+def test_gemm_groups(dtype, group, sizes, behind, N, K, gap, shift, start):
+    check_groups(sizes, behind, N, K, group, dtype, F32 if N % 2 else dtype, gap, shift, bias=N % 4 == 3, start=start)
+
+
+def test_gemm_many_groups():
+    g = torch.Generator().manual_seed(9)
+    sizes = torch.randint(0, 4, (200,), generator=g).tolist()
+    check_groups(sizes, 3, 100, 300, 64, BF16, BF16)
+    check_groups(sizes, 0, 100, 64, 32, F16, F32, gap=1, shift=1)
