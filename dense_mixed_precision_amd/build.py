@@ -42,11 +42,12 @@ PROBES_SRC = os.path.join(CSRC, "probes.hip")
 DEPS = [SRC, os.path.join(CSRC, "kernels.hpp"), os.path.join(ROOT, "include", "mpgemm.h")]
 OPS_SRC = os.path.join(CSRC, "ops.hip")
 OPS_DEPS = [OPS_SRC, *(os.path.join(ROOT, "include", f) for f in ("mpgemm_ops.h", "mpgemm_ops_query.h")), *DEPS[1:],
-            *(os.path.join(CSRC, f) for f in ("elements.hpp", "groups.hpp", "host_util.hpp", "i8_kernels.hpp",
-                                              "narrow_rows.hpp", "token_kernels.hpp"))]
+            *(os.path.join(CSRC, f) for f in ("copy4.hpp", "elements.hpp", "groups.hpp", "host_util.hpp",
+                                              "i8_kernels.hpp", "narrow_rows.hpp", "token_kernels.hpp"))]
 W4_SRC = os.path.join(CSRC, "w4.hip")
 W4_DEPS = [W4_SRC, *(os.path.join(ROOT, "include", f) for f in ("mpgemm_w4.h", "mpgemm_ops.h", "mpgemm_ops_query.h")),
-           *DEPS[1:], *(os.path.join(CSRC, f) for f in ("elements.hpp", "groups.hpp", "host_util.hpp", "w4_kernels.hpp"))]
+           *DEPS[1:], *(os.path.join(CSRC, f) for f in ("copy4.hpp", "elements.hpp", "groups.hpp", "host_util.hpp",
+                                                        "w4_kernels.hpp"))]
 ROUTER_SRC = os.path.join(CSRC, "router.hip")
 ROUTER_DEPS = [ROUTER_SRC, *(os.path.join(ROOT, "include", f) for f in ("mpgemm_router.h", "mpgemm_ops.h", "mpgemm.h")),
                *(os.path.join(CSRC, f) for f in ("elements.hpp", "host_util.hpp", "router_kernels.hpp"))]

@@ -44,15 +44,6 @@ struct VecOf {
 // fewer than 2^32 threads.
 __device__ __forceinline__ int64_t wg_number() { return blockIdx.x + (int64_t)blockIdx.y * gridDim.x; }
 
-// One wave instruction: lane l copies 4 bytes from rsrc at voff into LDS at
-// byte address lds_addr + 4*l (see dma16).
-__device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t lds_addr, uint32_t voff)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-                 ::"s"(lds_addr), "v"(voff), "s"(rsrc)
-                 : "memory", "m0");
-}
-
 // COUNT consecutive channels of one token, from column `col` (left = columns
 // from it to the edge).
 template <int OUT, int COUNT>

@@ -35,6 +35,7 @@
 // A[l%16][16*(l/16) + 0..15] and B[16*(l/16) + 0..15][l%16]; accumulator v
 // of lane l holds D[4*(l/16) + v][l%16].
 
+#include "copy4.hpp"
 #include "elements.hpp"
 
 struct I8Args {

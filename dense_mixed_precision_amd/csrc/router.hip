@@ -117,7 +117,7 @@ int64_t mpgemm_balance_workspace(int64_t T, int64_t E, int64_t top_k)
 {
     if (T < 0 || T > kMax32 || E < 1 || E > MPGEMM_MAX_GROUPS || top_k < 0 || mul_sat(T, top_k) > kMax32)
         return MPGEMM_EDIM;
-    return 4 * (plan_balance(T).blocks * (2 * E + 1) + 1 + 2 * balance_sums(E));
+    return 4 * (plan_balance(T).blocks * (2 * E + 1) + 1 + 3 * balance_sums(E));
 }
 
 int mpgemm_balance_loss(int l_type, int id_type, int64_t T, int64_t E, int64_t top_k,
@@ -158,7 +158,7 @@ int mpgemm_balance_loss(int l_type, int id_type, int64_t T, int64_t E, int64_t t
     });
     if (const int error = launched())
         return error;
-    hipLaunchKernelGGL(mpg::balance_sum, dim3((unsigned)balance_sums(E)), dim3(256), 0, stream_of(stream), a);
+    hipLaunchKernelGGL(mpg::balance_sum, dim3((unsigned)balance_sums(E)), dim3(1024), 0, stream_of(stream), a);
     return launched();
 }
 
@@ -189,7 +189,7 @@ int mpgemm_router_backward(int l_type, int d_type, int id_type, int64_t T, int64
         by_type(d_type, [&](auto dt) {
             by_width(E, dweights ? top_k : 0, [&](auto lpt, auto v) {
                 const int64_t blocks = cdiv(T, 256 / lpt.value);
-                const dim3 grid((unsigned)(blocks < 8 * kNumCu ? blocks : 8 * kNumCu));
+                const dim3 grid((unsigned)(blocks < 4 * kNumCu ? blocks : 4 * kNumCu));
                 if (id_type == MPGEMM_ID_I64)
                     hipLaunchKernelGGL((mpg::router_backward<lt.value, dt.value, lpt.value, v.value, 1>), grid,
                                        dim3(256), 0, stream_of(stream), a);

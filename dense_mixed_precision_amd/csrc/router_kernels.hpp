@@ -98,34 +98,43 @@ __device__ __forceinline__ void load_row(const E *row, int at, int count, float 
     }
 }
 
-// A row's largest key.
+// The larger of two, NaN if one is.
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
+// A row's largest logit: NaN where the row holds one.
 template <int LPT, int V>
-__device__ __forceinline__ uint32_t top_key(const float (&x)[V])
+__device__ __forceinline__ float top_of(const float (&x)[V])
 {
-    uint32_t m = 0;
+    float m = x[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        m = max(m, key_of(x[i]));
-    return most_of<LPT>(m);
+    for (int i = 1; i < V; ++i)
+        m = larger(m, x[i]);
+    return __builtin_bit_cast(float, over_lanes<LPT>(__builtin_bit_cast(uint32_t, m), [](uint32_t a, uint32_t b) {
+        return __builtin_bit_cast(uint32_t, larger(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
+    }));
 }
 
-// Probabilities of a row from its largest key: zeros without any expert, NaN
+// Has a row with this largest logit probabilities, and are they numbers?
+__device__ __forceinline__ bool has_any(float top) { return top != -__builtin_inff(); }
+__device__ __forceinline__ bool is_finite_row(float top) { return top < __builtin_inff(); }
+
+// Probabilities of a row from its largest logit: zeros without any expert, NaN
 // with a NaN or +inf.
 template <int LPT, int V>
-__device__ __forceinline__ void softmax(const float (&x)[V], uint32_t top, float (&p)[V])
+__device__ __forceinline__ void softmax(const float (&x)[V], float top, float (&p)[V])
 {
-    const float m = logit_of(top);
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        p[i] = exp_of(x[i] - m);
+        p[i] = exp_of(x[i] - top);
         sum += p[i];
     }
     sum = sum_of<LPT>(sum);
-    const float inv = top >= kInfKey ? __builtin_nanf("") : 1.0f / sum;
+    // (-inf minus -inf went to exp_of as a NaN and came back as 0)
+    const float inv = !has_any(top) ? 0.0f : is_finite_row(top) ? 1.0f / sum : __builtin_nanf("");
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        p[i] = top == 0 ? 0.0f : p[i] * inv;
+        p[i] *= inv;
 }
 
 // ---------------------------------------------------------------------------
@@ -133,8 +142,7 @@ __device__ __forceinline__ void softmax(const float (&x)[V], uint32_t top, float
 // ---------------------------------------------------------------------------
 // top_k times: the largest key left over all lanes, the first lane that has it,
 // and in that lane its first value; it is taken out.  Every lane learns the
-// key, so lane s keeps slot s's logit and all of them the sum; the lane that
-// has the expert writes its id.
+// key, and lane s keeps slot s's; the lane that has the expert writes its id.
 template <int LT, int LPT, int V>
 __global__ void __launch_bounds__(256)
 select_experts(RouterArgs args, int normalize, int32_t *ids, float *weights)
@@ -152,18 +160,15 @@ select_experts(RouterArgs args, int normalize, int32_t *ids, float *weights)
     for (int i = 0; i < V; ++i)
         key[i] = key_of(x[i]);
     const int k = args.top_k;
-    float mine = 0.0f, sum = 0.0f, m = 0.0f;
-    bool nan = false, has = false;
+    uint32_t first = 0, mine = 0;                     // keys of the first slot and of this lane's
     for (int s = 0; s < k; ++s) {
         uint32_t best = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i)
             best = max(best, key[i]);
         const uint32_t top = most_of<LPT>(best);
-        if (s == 0) {
-            m = logit_of(top);
-            nan = top >= kInfKey;
-        }
+        first = s == 0 ? top : first;
+        mine = lane == s ? top : mine;
         const uint64_t holders = __ballot(best == top) >> base;
         const bool winner = (int)__builtin_ctzll(holders) == lane;
         int at = 0;
@@ -175,14 +180,13 @@ select_experts(RouterArgs args, int normalize, int32_t *ids, float *weights)
             key[i] = winner && i == at ? 0u : key[i];
         if (winner && there)
             ids[t * k + s] = top == 0 ? -1 : lane * V + at;
-        const float e = top == 0 ? 0.0f : exp_of(logit_of(top) - m);
-        sum += e;
-        if (lane == s) {
-            mine = e;
-            has = top != 0;
-        }
     }
-    if (!normalize) {
+    const float m = logit_of(first);
+    const float e = mine == 0 ? 0.0f : exp_of(logit_of(mine) - m);
+    float sum;
+    if (normalize) {
+        sum = sum_of<LPT>(e);
+    } else {
         sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -190,7 +194,7 @@ select_experts(RouterArgs args, int normalize, int32_t *ids, float *weights)
         sum = sum_of<LPT>(sum);
     }
     if (there && lane < k)
-        weights[t * k + lane] = !has ? 0.0f : nan ? __builtin_nanf("") : mine / sum;
+        weights[t * k + lane] = mine == 0 ? 0.0f : first >= kInfKey ? __builtin_nanf("") : e / sum;
 }
 
 // ---------------------------------------------------------------------------
@@ -204,7 +208,7 @@ struct BalanceArgs {
     int32_t *counts;
     // workspace: per block E sums of probabilities, E + 1 counts; then a word
     // that counts finished blocks of the second launch, and per such block its
-    // share of sum counts * probs and of pairs
+    // share of sum counts * probs, of pairs and of tokens
     uint32_t *ws;
     int32_t blocks, per_block;     // of the first launch; tokens of each
 };
@@ -249,21 +253,27 @@ balance_tokens(BalanceArgs args)
     for (int i = 0; i < V; ++i)
         sum[i] = 0.0f;
     int tokens = 0;
-    for (int64_t t = t0 + threadIdx.x / LPT; t < t1 + TOKENS; t += TOKENS) {
-        // (whole waves leave together; lanes of tokens behind the last add nothing)
-        if (t - threadIdx.x / LPT >= t1)
-            break;
-        const bool there = t < t1;
-        float x[V], p[V];
-        load_row<E, V>((const E *)args.r.logits + (there ? t : t0) * args.r.ldl, lane * V, n, x);
-        const uint32_t top = top_key<LPT, V>(x);
+    // (lanes of tokens behind the last read the block's first and add nothing)
+    const E *const logits = (const E *)args.r.logits;
+    float x[V], next[V];
+    const int64_t mine = t0 + threadIdx.x / LPT;
+    if (t0 < t1)
+        load_row<E, V>(logits + (mine < t1 ? mine : t0) * args.r.ldl, lane * V, n, x);
+    for (int64_t t = mine, first = t0; first < t1; t += TOKENS, first += TOKENS) {
+        if (first + TOKENS < t1)
+            load_row<E, V>(logits + (t + TOKENS < t1 ? t + TOKENS : t0) * args.r.ldl, lane * V, n, next);
+        const float top = top_of<LPT, V>(x);
+        float p[V];
         softmax<LPT, V>(x, top, p);
-        if (there) {
+        if (t < t1) {
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 sum[i] += p[i];
-            tokens += lane == 0 && top != 0;
+            tokens += lane == 0 && has_any(top);
         }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            x[i] = next[i];
     }
     if (tokens != 0)
         atomicAdd(&cnt[n], tokens);
@@ -289,78 +299,93 @@ balance_tokens(BalanceArgs args)
     }
 }
 
-// Second launch: a block adds up its experts over the first launch's blocks (16
+// Second launch: a block adds up its experts over the first launch's blocks (64
 // threads each, in a fixed order), and the last block to finish the loss.
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
 balance_sum(BalanceArgs args)
 {
-    __shared__ float shares[kBalanceExperts];
-    __shared__ int32_t pairs[kBalanceExperts];
-    __shared__ bool last;
+    constexpr int SLICES = 1024 / kBalanceExperts;
     const int n = args.r.E, words = 2 * n + 1;
     // threads 0..15 of a row of 16 have expert `e`'s neighbours: loads of one
     // block's words side by side
     const int col = threadIdx.x % kBalanceExperts, slice = threadIdx.x / kBalanceExperts;
     const int e = blockIdx.x * kBalanceExperts + col;
-    __shared__ float psum[256 / kBalanceExperts][kBalanceExperts];
-    __shared__ int32_t csum[256 / kBalanceExperts][kBalanceExperts];
+    __shared__ float psum[16][kBalanceExperts];
+    __shared__ int32_t csum[16][kBalanceExperts];
     float p = 0.0f;
     int32_t c = 0;
     if (e <= n) {
-#pragma unroll 4
-        for (int b = slice; b < args.blocks; b += 256 / kBalanceExperts) {
+#pragma unroll 8
+        for (int b = slice; b < args.blocks; b += SLICES) {
             const uint32_t *const w = args.ws + (int64_t)b * words;
             if (e < n)
                 p += __builtin_bit_cast(float, w[e]);
             c += (int32_t)w[n + e];
         }
     }
-    psum[slice][col] = p;
-    csum[slice][col] = c;
-    __syncthreads();
-    if (slice == 0) {
-        p = 0.0f;
-        c = 0;
-        for (int s = 0; s < 256 / kBalanceExperts; ++s) {
-            p += psum[s][col];
-            c += csum[s][col];
-        }
-        if (e <= n)
-            args.counts[e] = c;
-        if (e < n && args.probs)
-            args.probs[e] = p;
-        shares[col] = e < n ? (float)c * p : 0.0f;
-        pairs[col] = e < n ? c : 0;
+    // a wave's four threads of an expert, then the waves in order
+    p += __shfl_xor(p, 16);
+    p += __shfl_xor(p, 32);
+    c += __shfl_xor(c, 16);
+    c += __shfl_xor(c, 32);
+    if ((threadIdx.x & 63) < kBalanceExperts) {
+        psum[threadIdx.x >> 6][col] = p;
+        csum[threadIdx.x >> 6][col] = c;
     }
     __syncthreads();
-    uint32_t *const done = args.ws + (int64_t)args.blocks * words;
-    float *const share = (float *)(done + 1);
-    int32_t *const pair = (int32_t *)(share + gridDim.x);
-    if (threadIdx.x == 0) {
-        float a = 0.0f;
-        int32_t b = 0;
-        for (int i = 0; i < kBalanceExperts; ++i) {
-            a += shares[i];
-            b += pairs[i];
-        }
-        share[blockIdx.x] = a;
-        pair[blockIdx.x] = b;
-        __threadfence();
-        last = atomicAdd(done, 1u) == gridDim.x - 1;
-    }
-    __syncthreads();
-    if (!last || threadIdx.x != 0)
+    if (threadIdx.x >= 64)
         return;
-    __threadfence();
-    float a = 0.0f;
-    int32_t b = 0;
-    for (unsigned i = 0; i < gridDim.x; ++i) {
-        a += __hip_atomic_load(&share[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        b += __hip_atomic_load(&pair[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    p = 0.0f;
+    c = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+        p += psum[w][col];
+        c += csum[w][col];
     }
-    const int32_t tokens = __hip_atomic_load(&args.counts[n], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const float per = (float)b * (float)tokens;
-    *args.loss = b == 0 || tokens == 0 ? 0.0f : args.coefficient * (float)n * a / per;
+    const bool mine = threadIdx.x < kBalanceExperts;
+    if (mine && e <= n)
+        args.counts[e] = c;
+    if (mine && e < n && args.probs)
+        args.probs[e] = p;
+    float a = mine && e < n ? (float)c * p : 0.0f;
+    int32_t b = mine && e < n ? c : 0;
+    int32_t tokens = mine && e == n ? c : 0;
+    auto add_up = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            a += __shfl_xor(a, d);
+            b += __shfl_xor(b, d);
+            tokens += __shfl_xor(tokens, d);
+        }
+    };
+    add_up();
+    if (gridDim.x > 1) {
+        uint32_t *const done = args.ws + (int64_t)args.blocks * words;
+        uint32_t *const share = done + 1;              // per block: sum, pairs, tokens
+        bool last = false;
+        if (threadIdx.x == 0) {
+            share[3 * blockIdx.x] = __builtin_bit_cast(uint32_t, a);
+            share[3 * blockIdx.x + 1] = (uint32_t)b;
+            share[3 * blockIdx.x + 2] = (uint32_t)tokens;
+            __threadfence();
+            last = atomicAdd(done, 1u) == gridDim.x - 1;
+        }
+        if (__ballot(last) == 0)
+            return;
+        __threadfence();
+        a = 0.0f;
+        b = 0;
+        tokens = 0;
+        for (unsigned i = threadIdx.x; i < gridDim.x; i += 64) {
+            a += __builtin_bit_cast(float, __hip_atomic_load(&share[3 * i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+            b += (int32_t)__hip_atomic_load(&share[3 * i + 1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            tokens += (int32_t)__hip_atomic_load(&share[3 * i + 2], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        add_up();
+    }
+    if (threadIdx.x == 0)
+        *args.loss = b == 0 || tokens == 0 ? 0.0f
+                                           : args.coefficient * (float)n * a / ((float)b * (float)tokens);
 }
 
 // ---------------------------------------------------------------------------
@@ -378,13 +403,13 @@ struct RouterBackArgs {
     int64_t ldd;
 };
 
-// A token's slots are its first top_k lanes.  Where a slot's value belongs is
-// found through a row of LDS of the token's own: the logits at the slots'
-// experts are read from it, then the slots' parts are put there and read back
-// by the lanes that have those experts.  Slots of one expert are added up
-// first, in slot order, by the first of them, so nothing depends on the order
-// of stores.  One wave's LDS operations happen in order; the fences keep the
-// compiler to it.
+// A token's slots are its first top_k lanes.  Their parts reach the lanes that
+// have their experts through a row of LDS of the token's own (value i of lane l
+// at i*LPT + l, so that a wave's accesses spread over the banks): put there, read
+// by all, and cleared again.  Slots of one expert are added up first, in slot
+// order, by the first of them, so nothing depends on the order of stores; they
+// are found by what is left of their lane numbers in that row.  One wave's LDS
+// operations happen in order; the fences keep the compiler to it.
 template <int LT, int DT, int LPT, int V, int WIDE>
 __global__ void __launch_bounds__(256)
 router_backward(RouterBackArgs args)
@@ -392,7 +417,7 @@ router_backward(RouterBackArgs args)
     typedef typename ElemOf<LT>::type E;
     typedef typename ElemOf<DT>::type D;
     constexpr int TOKENS = 256 / LPT;
-    __shared__ float rows[TOKENS][LPT * V + 1];
+    __shared__ float rows[TOKENS][LPT * V];
     const int lane = threadIdx.x % LPT;
     const int n = args.r.E, k = args.dweights ? args.r.top_k : 0;
     float *const row = rows[threadIdx.x / LPT];
@@ -421,27 +446,42 @@ router_backward(RouterBackArgs args)
             pull[i] = unit * c[i];
     }
     const bool by_prob = args.counts != nullptr || !args.normalize;
-    for (int64_t first = wg_number() * TOKENS; first < args.r.T; first += (int64_t)gridDim.x * gridDim.y * TOKENS) {
+    if (k > 0)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            row[i * LPT + lane] = 0.0f;
+    // (lanes of tokens behind the last go along with the block's first token)
+    const int64_t stride = (int64_t)gridDim.x * TOKENS;
+    float next[V], next_dw = 0.0f;
+    int64_t next_id = -1;
+    auto load = [&](int64_t first) __attribute__((always_inline)) {
+        const int64_t t = first + threadIdx.x / LPT, src = t < args.r.T ? t : first;
+        load_row<E, V>((const E *)args.r.logits + src * args.r.ldl, lane * V, n, next);
+        if (lane < k) {
+            const int64_t i = src * k + lane;
+            if constexpr (WIDE != 0)
+                next_id = ((const int64_t *)args.ids)[i];
+            else
+                next_id = ((const int32_t *)args.ids)[i];
+            next_dw = args.dweights[i];
+        }
+    };
+    const int64_t start = (int64_t)blockIdx.x * TOKENS;
+    if (start < args.r.T)
+        load(start);
+    for (int64_t first = start; first < args.r.T; first += stride) {
         const int64_t t = first + threadIdx.x / LPT;
         const bool there = t < args.r.T;
         const int64_t src = there ? t : first;
         float x[V];
-        load_row<E, V>((const E *)args.r.logits + src * args.r.ldl, lane * V, n, x);
-        int id = -1;
-        float dw = 0.0f;
-        if (lane < k) {
-            const int64_t i = src * k + lane;
-            if constexpr (WIDE != 0) {
-                const int64_t v = ((const int64_t *)args.ids)[i];
-                id = v >= 0 && v < n ? (int)v : -1;
-            } else {
-                const int v = ((const int32_t *)args.ids)[i];
-                id = v >= 0 && v < n ? v : -1;
-            }
-            if (id >= 0)
-                dw = args.dweights[i];
-        }
-        const uint32_t top = top_key<LPT, V>(x);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            x[i] = next[i];
+        const int id = next_id >= 0 && next_id < n ? (int)next_id : -1;
+        const float dw = id >= 0 ? next_dw : 0.0f;
+        if (first + stride < args.r.T)
+            load(first + stride);
+        const float top = top_of<LPT, V>(x);
         float z[V];              // the slots' parts
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -449,12 +489,7 @@ router_backward(RouterBackArgs args)
         if (k > 0) {
             float part = dw;
             if (args.normalize) {
-                fence();
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    row[lane * V + i] = x[i];
-                fence();
-                const float l = id >= 0 ? row[id] : -__builtin_inff();
+                const float l = id >= 0 ? (float)((const E *)args.r.logits)[src * args.r.ldl + id] : -__builtin_inff();
                 const uint32_t key = key_of(l), best = most_of<LPT>(key);
                 float w = key == 0 ? 0.0f : exp_of(l - logit_of(best));
                 const float sum = sum_of<LPT>(w);
@@ -462,28 +497,35 @@ router_backward(RouterBackArgs args)
                 const float mean = sum_of<LPT>(w * dw);
                 part = key == 0 ? 0.0f : w * (dw - mean);
             }
-            // slots of the same expert, in order, to the first of them
-            float total = 0.0f;
+            float *const place = row + id % V * LPT + id / V;
+            float total = part;
             bool is_first = id >= 0;
-            for (int s = 0; s < k; ++s) {
-                const int other = __shfl(id, s, LPT);
-                const float v = __shfl(part, s, LPT);
-                if (other == id) {
-                    total += v;
-                    is_first = is_first && s >= lane;
+            fence();
+            if (id >= 0)
+                *place = (float)lane;
+            fence();
+            if (__ballot(id >= 0 && *place != (float)lane) != 0) {
+                // some token has an expert in several slots
+                total = 0.0f;
+                for (int s = 0; s < k; ++s) {
+                    const int other = __shfl(id, s, LPT);
+                    const float v = __shfl(part, s, LPT);
+                    if (other == id) {
+                        total += v;
+                        is_first = is_first && s >= lane;
+                    }
                 }
             }
             fence();
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                row[lane * V + i] = 0.0f;
-            fence();
             if (is_first)
-                row[id] = total;
+                *place = total;
             fence();
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                z[i] = row[lane * V + i];
+                z[i] = row[i * LPT + lane];
+            fence();
+            if (id >= 0)
+                *place = 0.0f;
         }
         float out[V];
         if (by_prob) {
@@ -502,7 +544,7 @@ router_backward(RouterBackArgs args)
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                out[i] = top >= kInfKey ? __builtin_nanf("") : z[i];
+                out[i] = has_any(top) && !is_finite_row(top) ? __builtin_nanf("") : z[i];
         }
         if (!there)
             continue;

@@ -12,6 +12,7 @@
 #include "kernels.hpp"
 
 namespace mpg {
+#include "copy4.hpp"
 #include "elements.hpp"
 #include "w4_kernels.hpp"
 }  // namespace mpg
