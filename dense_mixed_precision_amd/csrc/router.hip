@@ -189,7 +189,7 @@ int mpgemm_router_backward(int l_type, int d_type, int id_type, int64_t T, int64
         by_type(d_type, [&](auto dt) {
             by_width(E, dweights ? top_k : 0, [&](auto lpt, auto v) {
                 const int64_t blocks = cdiv(T, 256 / lpt.value);
-                const dim3 grid((unsigned)(blocks < 4 * kNumCu ? blocks : 4 * kNumCu));
+                const dim3 grid((unsigned)(blocks < 8 * kNumCu ? blocks : 8 * kNumCu));
                 if (id_type == MPGEMM_ID_I64)
                     hipLaunchKernelGGL((mpg::router_backward<lt.value, dt.value, lpt.value, v.value, 1>), grid,
                                        dim3(256), 0, stream_of(stream), a);

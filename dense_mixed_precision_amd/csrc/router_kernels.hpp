@@ -431,13 +431,20 @@ router_backward(RouterBackArgs args)
     for (int i = 0; i < V; ++i)
         pull[i] = 0.0f;
     if (args.counts) {
-        float mine = 0.0f;
-        float c[V];
+        float mine = 0.0f, c[V];
+        if (lane * V + V <= n) {
+            const Pack<int32_t, V> w = *(const Pack<int32_t, V> *)(args.counts + lane * V);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            c[i] = lane * V + i < n ? (float)args.counts[lane * V + i] : 0.0f;
-            mine += c[i];
+            for (int i = 0; i < V; ++i)
+                c[i] = (float)w.v[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                c[i] = lane * V + i < n ? (float)args.counts[lane * V + i] : 0.0f;
         }
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            mine += c[i];
         const float pairs = sum_of<LPT>(mine), tokens = (float)args.counts[n];
         const float g = (args.dloss ? *args.dloss : 1.0f) * args.coefficient * (float)n;
         const float unit = pairs > 0.0f && tokens > 0.0f ? g / (pairs * tokens) : 0.0f;
