@@ -193,7 +193,8 @@ void launch_unpack(int s_type, const mpg::W4UnpackArgs &a, hipStream_t s)
         hipLaunchKernelGGL((mpg::w4_unpack<mpg::kTBF16, WT>), grid, dim3(256), 0, s, a);
 }
 
-// What both directions ask of their arguments; `parts` waves a row.
+// What both directions ask of their arguments; `parts` waves a row, of `span`
+// values each.
 int check_pack(int w_type, int s_type, int64_t N, int64_t K, int64_t group, const void *W, int64_t ldw, const void *Q,
                int64_t ldq, const void *scale, int64_t lds, int64_t span, int64_t &parts)
 {
@@ -201,7 +202,7 @@ int check_pack(int w_type, int s_type, int64_t N, int64_t K, int64_t group, cons
         return MPGEMM_ETYPE;
     if (N < 0 || K < 0 || N > kMax32 || K > kMaxWidth || group_shift(group) < 0)
         return MPGEMM_EDIM;
-    parts = cdiv(K, span > 512 ? span : 512);
+    parts = cdiv(K, span);
     if (mul_sat(N, parts) > kMax32)
         return MPGEMM_EDIM;
     if (ldw < at_least_one(K) || ldq < at_least_one(cdiv(K, 2)) || lds < at_least_one(cdiv(K, group)))
@@ -222,7 +223,8 @@ int mpgemm_w4_quantize(int w_type, int s_type, int64_t N, int64_t K, int64_t gro
                        void *scale, int64_t lds, void *stream)
 {
     int64_t parts = 0;
-    if (const int error = check_pack(w_type, s_type, N, K, group, W, ldw, Q, ldq, scale, lds, group, parts))
+    if (const int error = check_pack(w_type, s_type, N, K, group, W, ldw, Q, ldq, scale, lds,
+                                     group > mpg::kPackSpan ? group : mpg::kPackSpan, parts))
         return error;
     if (N == 0 || K == 0)
         return MPGEMM_OK;

@@ -747,48 +747,75 @@ struct W4PackArgs {
 
 // A group's scale and codes.  With m the largest magnitude, s is m/7 rounded to
 // FP32 and then to the scale's type; a value's code is the whole number of
-// -8 .. 7 nearest to w/s, the even one in the middle, decided exactly: both are
-// scaled by the power of two that brings s to [0.5, 1), q = rint(w * (1/s)) is
-// off by one at most, and the remainder w - q*s (one fused multiply-add, exact
-// near the middle of two codes: q*s has at most 15 bits, and what is left is a
-// multiple of 2^-25 below 1) against s/2 says which way.  A group with an
-// infinity or a NaN, or whose scale its type does not hold, has a NaN scale
-// and codes 0.
-template <int ST>
+// -8 .. 7 nearest to w/s, the even one in the middle, decided exactly.  Both are
+// first multiplied by the power of two that brings s to [0.5, 1) or near it
+// (exact: s stays a normal number, and a w that would become too small for one
+// has code 0 either way).  A group with an infinity or a NaN, or whose scale its
+// type does not hold, has a NaN scale and codes 0.
+//
+// 16-bit w: with w = P*2^j and s = A*2^i, P and A of 11 bits, a quotient that is
+// no middle of two codes differs from one by at least 2^-16 of itself, so FP32
+// decides; a middle is an FP32 number itself, which t = w * (1/s) plus its exact
+// remainder times 1/s gives, whatever the last digit of 1/s is.
+// FP32 w: q = rint(w * (1/s)) is off by one at most, and the remainder w - q*s
+// (one fused multiply-add, exact near a middle: q*s has at most 15 bits, and
+// what is left is a multiple of 2^-25 of s) against s/2 says which way.
+template <int WT, int ST>
 struct W4Scale {
-    float s, half, inv;
-    int ex;
-    bool live;
+    float s, f, inv;
     uint16_t bits;
     __device__ __forceinline__ explicit W4Scale(uint32_t top)
     {
         typedef typename ElemOf<ST>::type E;
         const float most = __builtin_bit_cast(float, top);
-        E e = (E)(most / 7.0f);
-        float v = (float)e;
+        // m/7 rounded correctly: m * (1/7) plus its exact remainder times 1/7
+        constexpr float seventh = 1.0f / 7.0f;
+        float v = most * seventh;
+        v = __builtin_fmaf(__builtin_fmaf(-7.0f, v, most), seventh, v);
+        if (most < 0x1p-100f)
+            v = most / 7.0f;  // (where that would round twice)
+        E e = (E)v;
+        v = (float)e;
         if (top >= 0x7F800000u || __builtin_bit_cast(uint32_t, v) >= 0x7F800000u) {
             e = (E)__builtin_nanf("");
             v = 0.0f;
         }
         bits = __builtin_bit_cast(uint16_t, e);
-        live = v > 0.0f;
-        ex = live ? __builtin_amdgcn_frexp_expf(v) : 0;
-        s = live ? __builtin_amdgcn_ldexpf(v, -ex) : 1.0f;
-        half = 0.5f * s;
-        inv = 1.0f / s;
+        int ex = __builtin_amdgcn_frexp_expf(v);
+        ex = ex < -126 ? -126 : ex > 126 ? 126 : ex;
+        // (without a scale every code is 0: by f = 0, for infinities see code)
+        f = v > 0.0f ? __builtin_bit_cast(float, (uint32_t)(127 - ex) << 23) : 0.0f;
+        s = v > 0.0f ? v * f : 1.0f;
+        inv = __builtin_amdgcn_rcpf(s);
     }
-    __device__ __forceinline__ uint32_t nibble(float w) const
+    // The code of a value, as a float.
+    __device__ __forceinline__ float code(float w) const
     {
-        const float x = __builtin_amdgcn_ldexpf(w, -ex);
-        float q = __builtin_rintf(x * inv);
-        const float rest = __builtin_fmaf(-q, s, x);
-        const bool odd = ((int)q & 1) != 0;
-        if (rest > half || (rest == half && odd))
-            q += 1.0f;
-        else if (rest < -half || (rest == -half && odd))
-            q -= 1.0f;
-        q = q < -8.0f ? -8.0f : q > 7.0f ? 7.0f : q;
-        return live ? (uint32_t)((int)q + 8) : 8u;
+        const float x = w * f;
+        float q;
+        if constexpr (WT != kTF32) {
+            const float t = x * inv;
+            q = __builtin_rintf(__builtin_fmaf(__builtin_fmaf(-t, s, x), inv, t));
+        } else {
+            q = __builtin_rintf(x * inv);
+            const float rest = __builtin_fmaf(-q, s, x), half = 0.5f * s;
+            const bool odd = ((int)q & 1) != 0;
+            if (rest > half || (rest == half && odd))
+                q += 1.0f;
+            else if (rest < -half || (rest == -half && odd))
+                q -= 1.0f;
+        }
+        q = __builtin_amdgcn_fmed3f(q, -8.0f, 7.0f);
+        return f == 0.0f ? 0.0f : q;
+    }
+    // Eight codes in four bytes: the pairs' bytes are whole FP32 numbers.
+    __device__ __forceinline__ uint32_t pack(const float (&v)[8]) const
+    {
+        uint32_t o = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            o = __builtin_amdgcn_cvt_pk_u8_f32(__builtin_fmaf(16.0f, code(v[2 * e + 1]), code(v[2 * e]) + 136.0f), e, o);
+        return o;
     }
 };
 
@@ -810,8 +837,30 @@ __device__ __forceinline__ void load_values(const E *w, int64_t k, int64_t K, fl
     }
 }
 
-// A lane has 8 neighbouring values, a wave 512 of a row.  Groups of up to 512
+// The largest of 2^n neighbouring lanes' numbers, lanes that start at a multiple
+// of that: within 16 lanes by register moves.
+__device__ __forceinline__ uint32_t most_of_lanes(uint32_t v, int lanes)
+{
+    auto with = [&](uint32_t other) __attribute__((always_inline)) { v = max(v, other); };
+    if (lanes >= 2)
+        with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1 /* quad_perm 1 0 3 2 */, 0xF, 0xF, true));
+    if (lanes >= 4)
+        with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E /* quad_perm 2 3 0 1 */, 0xF, 0xF, true));
+    if (lanes >= 8)
+        with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141 /* row_half_mirror */, 0xF, 0xF, true));
+    if (lanes >= 16)
+        with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140 /* row_mirror */, 0xF, 0xF, true));
+    if (lanes >= 32)
+        with((uint32_t)__shfl_xor((int)v, 16));
+    if (lanes >= 64)
+        with((uint32_t)__shfl_xor((int)v, 32));
+    return v;
+}
+
+// A lane has 16 neighbouring values, a wave 1024 of a row.  Groups of up to 1024
 // values are the lanes of one wave; of larger ones a wave has one, read twice.
+constexpr int kPackSpan = 1024;
+
 template <int WT, int ST>
 __global__ void __launch_bounds__(256)
 w4_pack(W4PackArgs args)
@@ -823,40 +872,39 @@ w4_pack(W4PackArgs args)
     if (row >= args.N)
         return;
     const int64_t K = args.K, size = (int64_t)1 << args.shift;
-    const int64_t span = size > 512 ? size : 512;
+    const int64_t span = size > kPackSpan ? size : kPackSpan;
     const int64_t first = (unit - row * args.parts) * span, end = first + span < K ? first + span : K;
     const E *const w = (const E *)args.W + row * args.ldw;
-    float v[8];
+    float v[2][8];
     uint32_t top = 0;
-    for (int64_t k = first + 8 * lane; k < end; k += 512) {
-        load_values(w, k, K, v);
+    const int64_t at = first + 16 * lane;
+    auto load = [&](int64_t k) __attribute__((always_inline)) {
+        load_values(w, k, K, v[0]);
+        load_values(w, k + 8, K, v[1]);
+    };
+    for (int64_t k = at; k < end; k += kPackSpan) {
+        load(k);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            top = max(top, magnitude(v[e]));
+        for (int e = 0; e < 16; ++e)
+            top = max(top, magnitude(v[e / 8][e % 8]));
     }
-    const int lanes = args.shift >= 9 ? 64 : 1 << (args.shift - 3);
-    for (int d = 1; d < lanes; d *= 2)
-        top = max(top, (uint32_t)__shfl_xor((int)top, d));
-    const W4Scale<ST> scale(top);
-    const int64_t at = first + 8 * lane;
+    const int lanes = args.shift >= 10 ? 64 : 1 << (args.shift - 4);
+    top = most_of_lanes(top, lanes);
+    const W4Scale<WT, ST> scale(top);
     if ((lane & (lanes - 1)) == 0 && at < end)
         args.S[row * args.lds + (at >> args.shift)] = scale.bits;
     uint8_t *const q = args.Q + row * args.ldq;
-    for (int64_t k = at; k < end; k += 512) {
-        if (size > 512)
-            load_values(w, k, K, v);
-        Pack<uint8_t, 4> o;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            o.v[e] = (uint8_t)(scale.nibble(v[2 * e]) | scale.nibble(v[2 * e + 1]) << 4);
-        if (k + 8 <= K) {
-            *(Pack<uint8_t, 4> *)(q + k / 2) = o;
+    for (int64_t k = at; k < end; k += kPackSpan) {
+        if (size > kPackSpan)
+            load(k);
+        const u32x2 o = {scale.pack(v[0]), scale.pack(v[1])};
+        if (k + 16 <= K) {
+            *(Pack<uint8_t, 8> *)(q + k / 2) = __builtin_bit_cast(Pack<uint8_t, 8>, o);
         } else {
             // (a value behind the row is 0, so the spare nibble is 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 8; ++e)
                 if (k + 2 * e < K)
-                    q[k / 2 + e] = o.v[e];
+                    q[k / 2 + e] = (uint8_t)(o[e / 4] >> (8 * (e % 4)));
         }
     }
 }
