@@ -180,6 +180,8 @@ def _rows(t, name, dtype):
         rows, cols = t.shape
         if step == 1 and rows > 1 and ld >= cols > 0:
             return rows, cols, ld
+        if step == 1 and rows == 1 and cols > 0:
+            return 1, cols, cols
     ld = _check_tensor(t, name, dtype)[1]
     return t.shape[0], t.shape[1], ld
 

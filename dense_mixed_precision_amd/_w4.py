@@ -75,7 +75,7 @@ def _packed(Q, scale, N, K, group, types):
     st = _type(scale, "scale", types)
     Nq, B, ldq = _rows(Q, "Q", _ops.torch.uint8)
     Ns, G, lds = _rows(scale, "scale", scale.dtype)
-    if Nq != N or Ns != N or B != (K + 1) // 2 or G != -(-K // group):
+    if Nq != N or Ns != N or B != (K + 1) >> 1 or G != -(-K // group):
         raise ValueError(f"shape mismatch: Q {tuple(Q.shape)} and scale {tuple(scale.shape)} for {N} x {K} values in "
                          f"groups of {group}")
     return Q.data_ptr(), ldq, scale.data_ptr(), lds, st
