@@ -81,33 +81,29 @@ __device__ __forceinline__ float scale_value(uint32_t bits)
         return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
 }
 
-// Groups of a row's values by the number that share a scale.  With 128 or more
-// (COARSE) a lane's 32 consecutive codes go to four matrix instructions as they
-// lie: instruction j takes values 32*kg + 8*j + 0..7 of a step of 128 from the
-// lanes of part kg = lane / 16.  With fewer, an instruction's 32 values must lie
-// in one group: the four registers of codes are transposed over the four parts,
-// and instruction j takes 32*j + 8*kg + 0..7.
+// Groups of a row's values by the number that share a scale: 128 or more, 64, 32.
 constexpr int kCoarse = 0, kGroup64 = 1, kGroup32 = 2;
 
-template <int GS>
+// A lane's 16 bytes are 32 consecutive codes of its row, part kg = lane / 16 of a
+// step of 128.  A matrix instruction's 32 values shall lie in one group, and 8 of
+// them in each part's tokens side by side: the four registers of codes are
+// transposed over the four parts, and instruction j takes the values 32*j +
+// 8*kg + 0..7.
 __device__ __forceinline__ u32x4 deal_codes(u32x4 w)
 {
-    if constexpr (GS != kCoarse) {
-        const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-        const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-        const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-        const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-        return u32x4{(uint32_t)c[0], (uint32_t)c[1], (uint32_t)d[0], (uint32_t)d[1]};
-    }
-    return w;
+    const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    return u32x4{(uint32_t)c[0], (uint32_t)c[1], (uint32_t)d[0], (uint32_t)d[1]};
 }
 
-// Value (of a step of 128) that lane part kg's first slot of instruction j takes.
-template <int GS>
-__device__ __forceinline__ constexpr int slot_value(int j, int kg)
-{
-    return GS == kCoarse ? 32 * kg + 8 * j : 32 * j + 8 * kg;
-}
+// Rows in LDS.  An operand read takes four turns, of lanes 0-3, 12-15, 20-27 and
+// so on: rows 0-3 and 12-15 of one part with rows 4-11 of the next.  Chunk c of a
+// row of tokens (16 of them) stands at c ^ (r % 16), and piece p of a row of codes
+// (four of them) at p ^ -(r / 4): the 16 lanes of a turn then have 16 different
+// places of 16 bytes in the banks' 256.
+__device__ __forceinline__ int piece_place(int p, int r) { return p ^ (-(r >> 2) & 3); }
 
 // ---- 16 bytes of a row that may end inside them --------------------------------
 // `left` bytes of the row remain at the place (of `len` in all, len >= 16): where
@@ -169,10 +165,10 @@ __device__ __forceinline__ void store_values(int type, void *C, int64_t at, int 
 // (measured: 42 cycles an instruction, 15.4 us for 8x8192x8192 whatever is kept
 // in flight).  So a step's rows go to LDS by direct copies whose neighbouring
 // lanes copy neighbouring bytes, STAGES steps ahead, and are read from there:
-//   codes   channels NF*r + f together, 64 bytes each, piece p at p ^ (r / 4)
-//   tokens  256 bytes a row, chunk c of row r at c ^ (r % 16)
+//   codes   channels NF*r + f together, 64 bytes each
+//   tokens  256 bytes a row
 //   scales  the 4-byte words of each channel that hold the step's
-// (both orders spread the 16 rows of an operand read over all banks).  A wave
+// (see piece_place).  A wave
 // waits for its own copies only; there is no barrier before the sums.  Every
 // step issues the same copies, those behind the wave's last from empty buffers,
 // so that one count waits for all of them, and the loop has one copy of its
@@ -220,7 +216,7 @@ w4_narrow(W4Args args)
 
     // ---- copies
     // 32-bit offsets of rows: the host checks that a tile's rows span less than 2 GiB
-    const int rowQ = lane >> 2, pieceQ = (lane & 3) ^ (lane >> 4);
+    const int rowQ = lane >> 2, pieceQ = piece_place(lane & 3, lane >> 2);
     const int rowA = lane >> 4;
     uint32_t offQ[NF];
 #pragma unroll
@@ -263,7 +259,7 @@ w4_narrow(W4Args args)
         __attribute__((always_inline)) {
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
-            const u32x4 w = deal_codes<GS>(rq[f]);
+            const u32x4 w = deal_codes(rq[f]);
             half8 b[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -296,7 +292,7 @@ w4_narrow(W4Args args)
 #pragma unroll
             for (int f = 0; f < NF; ++f) {
                 const int c = NF * r + f;
-                rq[f] = *(const lds_u32x4 *)(from + 1024 * f + 64 * r + 16 * (kg ^ (r >> 2)));
+                rq[f] = *(const lds_u32x4 *)(from + 1024 * f + 64 * r + 16 * piece_place(kg, r));
                 const int i = odd + c * (int)args.lds + (GS == kCoarse ? s >> (args.shift - 7) : 0);
 #pragma unroll
                 for (int g = 0; g < NS; ++g) {
@@ -313,7 +309,7 @@ w4_narrow(W4Args args)
                     // (operand rows without a token repeat those of the others)
                     const int row = NA < 4 ? r % (4 * NA) : 16 * m + r;
                     ra[m][j] = *(const lds_u32x4 *)(from + AT_A + 256 * row +
-                                                    16 * ((slot_value<GS>(j, kg) / 8) ^ (row & 15)));
+                                                    16 * ((4 * j + kg) ^ (row & 15)));
                 }
             if (s == full) {
                 // K ends in this step
@@ -329,7 +325,7 @@ w4_narrow(W4Args args)
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        ra[m][j] = end_shift(ra[m][j], KA - (256 * s + 2 * slot_value<GS>(j, kg)));
+                        ra[m][j] = end_shift(ra[m][j], KA - (256 * s + 2 * (32 * j + 8 * kg)));
             }
             multiply(rq, ra, scale);
         }
@@ -350,7 +346,7 @@ w4_narrow(W4Args args)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 ra[m][j] = short_row<2>(bA, 16 * m + r < rows ? (uint32_t)(2 * (16 * m + r) * (int)args.lda) : kOOB,
-                                        2 * slot_value<GS>(j, kg), KA);
+                                        2 * (32 * j + 8 * kg), KA);
         multiply(rq, ra, scale);
     }
     wait_vmcnt<0>();
@@ -463,7 +459,7 @@ w4_tile(W4Args args)
     const int steps = (K + 127) / 128, full = K / 128;
 
     // ---- copies, as in w4_narrow
-    const int pieceQ = (lane & 3) ^ (lane >> 4), rowA = lane >> 4;
+    const int pieceQ = piece_place(lane & 3, lane >> 2), rowA = lane >> 4;
     uint32_t offA[Cfg::COPY_A], offQ[NF];
 #pragma unroll
     for (int q = 0; q < Cfg::COPY_A; ++q) {
@@ -543,7 +539,7 @@ w4_tile(W4Args args)
     half8 code[2][NF][4];    // [step % 2][channel][instruction]
     u32x4 raw[NF];           // the next step's, before they are expanded
     auto read_codes = [&](int s, int slot) __attribute__((always_inline)) {
-        const lds_u8 *const from = lds + Cfg::AT_Q + (slot * NW + wave) * Cfg::BUF_Q + 64 * r + 16 * (kg ^ (r >> 2));
+        const lds_u8 *const from = lds + Cfg::AT_Q + (slot * NW + wave) * Cfg::BUF_Q + 64 * r + 16 * piece_place(kg, r);
 #pragma unroll
         for (int f = 0; f < NF; ++f)
             raw[f] = *(const lds_u32x4 *)(from + 1024 * f);
@@ -555,7 +551,7 @@ w4_tile(W4Args args)
     auto expand = [&](int set, int n) __attribute__((always_inline)) {
         if (n < 4 * NF) {
             if (n % 4 == 0)
-                raw[n / 4] = deal_codes<GS>(raw[n / 4]);
+                raw[n / 4] = deal_codes(raw[n / 4]);
             code[set][n / 4][n % 4] = codes8<IN>(raw[n / 4][n % 4]);
             // (here, and not where the next step uses them)
             asm volatile("" : "+v"(code[set][n / 4][n % 4]));
@@ -566,7 +562,7 @@ w4_tile(W4Args args)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             a[set][j] = *(const __attribute__((address_space(3))) half8 *)(
-                lds + slot * Cfg::BUF_A + 4096 * i + 256 * r + 16 * ((slot_value<GS>(j, kg) / 8) ^ r));
+                lds + slot * Cfg::BUF_A + 4096 * i + 256 * r + 16 * ((4 * j + kg) ^ r));
     };
     float scale[2][NF][NS];  // [step % 2]
     auto read_scales = [&](int set, int s, int slot) __attribute__((always_inline)) {
