@@ -174,6 +174,13 @@ __device__ __forceinline__ void store_values(int type, void *C, int64_t at, int 
 // so that one count waits for all of them, and the loop has one copy of its
 // body: the instructions of a launch come from memory once more, about 0.1 us
 // for 128 bytes of them, which a call of few microseconds notices.
+//
+// Bound: for few tokens the codes' way from memory and their expansion together
+// (8x8192x8192 FP16 11.3 us, 3.1 TB/s of codes, vector units busy 48% of the
+// time a compute unit holds waves; 64 BF16 rows over 64 experts of 2048x2048, of
+// which they reach about 41, 25.5 us, 75%); for 32 to 64 the tokens, which every
+// compute unit reads whole (64x8192x8192 24.6 us: 1 MiB of tokens and 128 KiB of
+// codes a workgroup); for one small product the launch (1x4096x4096 5.9).
 template <int IN, int GS, int NA, int NF, int WAVES, int STAGES>
 __global__ void __launch_bounds__(64 * WAVES)
 w4_narrow(W4Args args)
@@ -410,6 +417,15 @@ w4_narrow(W4Args args)
 // one issues the batch that takes the slots it freed, a few copies after each 16
 // tokens.  The sums of 16 tokens join the running ones beside the next 16 tokens'
 // instructions.
+//
+// Bound: the matrix cores at the board's power limit, with the vector work that
+// goes beside them: 8192^3 BF16 1.06 ms, 1.04e15 operations/s (a 16-bit library
+// product 0.83), matrix pipes busy 48% at 2.1 GHz, vector instructions issued in
+// 58% of the cycles.  Timed with parts left out: without the joining of sums
+// 0.99 ms, without the expansion of codes no less, copies, barriers and matrix
+// instructions alone 0.78.  Copies issued all at once instead of a few after each
+// 16 tokens cost 5%, registers spilt by sums that the compiler moves down a
+// quarter (see join).
 template <int IN_, int GS_, int BM_, int NF_, int NW_>
 struct W4Cfg {
     static constexpr int IN = IN_, GS = GS_, BM = BM_, NF = NF_, NW = NW_;
@@ -855,6 +871,8 @@ __device__ __forceinline__ uint32_t most_of_lanes(uint32_t v, int lanes)
 
 // A lane has 16 neighbouring values, a wave 1024 of a row.  Groups of up to 1024
 // values are the lanes of one wave; of larger ones a wave has one, read twice.
+// Bound: the vector units and HBM (8192x8192 BF16 in groups of 128 53 us, 3.2 TB/s;
+// 87 with 8 values a lane, whose scales and remainders cost as much as the codes).
 constexpr int kPackSpan = 1024;
 
 template <int WT, int ST>
@@ -905,6 +923,8 @@ w4_pack(W4PackArgs args)
     }
 }
 
+// A lane makes 8 values of four bytes.  Bound: the writing of the values (8192x8192
+// to FP32 50 us, 6 TB/s).
 struct W4UnpackArgs {
     const uint8_t *Q;
     const uint16_t *S;
