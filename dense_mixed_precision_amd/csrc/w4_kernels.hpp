@@ -168,12 +168,12 @@ __device__ __forceinline__ void store_values(int type, void *C, int64_t at, int 
 //   codes   channels NF*r + f together, 64 bytes each
 //   tokens  256 bytes a row
 //   scales  the 4-byte words of each channel that hold the step's
-// (see piece_place).  A wave
-// waits for its own copies only; there is no barrier before the sums.  Every
-// step issues the same copies, those behind the wave's last from empty buffers,
-// so that one count waits for all of them, and the loop has one copy of its
-// body: the instructions of a launch come from memory once more, about 0.1 us
-// for 128 bytes of them, which a call of few microseconds notices.
+// (in the places of piece_place).  A wave waits for its own copies only; there is
+// no barrier before the sums.  Every step issues the same copies, those behind the
+// wave's last from empty buffers, so that one count waits for all of them, and the
+// loop has one copy of its body: the instructions of a launch come from memory
+// once more, about 0.1 us for 128 bytes of them, which a call of few microseconds
+// notices.
 //
 // Bound: for few tokens the codes' way from memory and their expansion together
 // (8x8192x8192 FP16 11.3 us, 3.1 TB/s of codes, vector units busy 48% of the
