@@ -415,7 +415,7 @@ struct RouterBackArgs {
 // order, by the first of them, so nothing depends on the order of stores; they
 // are found by what is left of their lane numbers in that row.  One wave's LDS
 // operations happen in order; the fences keep the compiler to it.
-// Bound: vector work and memory (32768x256 BF16 with 8 slots and the loss 12.5 us,
+// Bound: vector work and memory (32768x256 BF16 with 8 slots and the loss 12.8 us,
 // 2.8 TB/s; 16384x128 FP32 normalised 5.3 us, 3.2 TB/s).
 template <int LT, int DT, int LPT, int V, int WIDE>
 __global__ void __launch_bounds__(256)
