@@ -85,7 +85,9 @@ int mpgemm_balance_loss(int l_type, int id_type, int64_t T, int64_t E, int64_t t
  * dweights NULL: the loss alone (ids is not read and may be NULL).  counts NULL:
  * the weights alone; otherwise as mpgemm_balance_loss wrote them, or their sums
  * over several devices.  dloss: one float in device memory, or NULL for 1.
- * ids may differ from those that mpgemm_select_experts chose.
+ * ids may differ from those that mpgemm_select_experts chose.  A pair without an
+ * expert, or whose expert's logit is -inf, has no part: its dweights may be
+ * anything, infinities and NaN included.
  * top_k <= MPGEMM_MAX_SELECT.
  */
 int mpgemm_router_backward(int l_type, int d_type, int id_type, int64_t T, int64_t E, int64_t top_k,
