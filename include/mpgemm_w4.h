@@ -63,7 +63,9 @@ int mpgemm_w4_dequantize(int w_type, int s_type, int64_t N, int64_t K, int64_t g
  * The codes are multiplied exactly; the sum of up to 128 of a group's products
  * (128: of larger groups too) is FP32 and joins the FP32 sum of a row by one
  * fused multiply-add with its scale; the bias is added in FP32; out_type rounds
- * once.  No weight is rounded.
+ * once.  No weight is rounded.  Those sums come before the scale: BF16 tokens of
+ * magnitude 2^122 (5.3e36) or more may overflow there although the scaled result
+ * would not; smaller ones, and FP16 ones, cannot.
  *
  * A: M x K of in_type (MPGEMM_IN_F16 or MPGEMM_IN_BF16), lda >= max(1,K).
  * Q, scale: as above, scale of the same type as A.  C: M x N of out_type
