@@ -150,7 +150,8 @@ def gemm_w4(A, Q, scale, C, group: int = 128, bias=None, offsets=None, stream=No
     With ``offsets`` (int32, groups + 1 values from :func:`route`) Q and scale
     have a matrix per group in front (bias: groups x N): rows offsets[g] ..
     offsets[g+1]-1 of A and C use group g's, other rows of C keep what they
-    hold."""
+    hold.  The gradient by A goes through :func:`dequantize_w4` to A's type (one
+    rounding a weight) and ``gemm`` or ``gemm_grouped`` with the values."""
     if _ops.torch is None:
         _ops._with_torch()
     group = _group(group)

@@ -76,6 +76,11 @@ int mpgemm_w4_dequantize(int w_type, int s_type, int64_t N, int64_t K, int64_t g
  * scale + g*stride_s and row g of bias (groups x N, contiguous); rows of C that
  * no group has keep what they hold.  See mpgemm_ops.h for offsets and groups.
  *
+ * The gradient by the tokens, dA = dC * W, has no call of its own: it is
+ * mpgemm_w4_dequantize to in_type (each weight code * scale rounded once, half a
+ * step of that type, which the product above does not do) and the 16-bit product
+ * with the values (mpgemm_gemm_ex; per expert mpgemm_grouped).
+ *
  * M below 2^31; 64 rows of A, and 32 rows of Q and of scale, within 2 GiB
  * (else MPGEMM_ELD); at most 2^22 tiles (else MPGEMM_EDIM).
  */
