@@ -220,7 +220,7 @@ constexpr int kBalanceExperts = 16;
 
 // First launch: each block adds up the probabilities of its tokens, a lane
 // always those of the same experts, and counts its pairs in LDS.  Bound: memory
-// latency and the exponentials (32768x256 BF16 with 8 slots 9 us, 2 TB/s).
+// latency and the exponentials (32768x256 BF16 with 8 slots 9-10 us, 1.8 TB/s).
 template <int LT, int LPT, int V, int WIDE>
 __global__ void __launch_bounds__(256)
 balance_tokens(BalanceArgs args)
@@ -415,8 +415,8 @@ struct RouterBackArgs {
 // order, by the first of them, so nothing depends on the order of stores; they
 // are found by what is left of their lane numbers in that row.  One wave's LDS
 // operations happen in order; the fences keep the compiler to it.
-// Bound: vector work and memory (32768x256 BF16 with 8 slots and the loss 12.8 us,
-// 2.8 TB/s; 16384x128 FP32 normalised 5.3 us, 3.2 TB/s).
+// Bound: vector work and memory (32768x256 BF16 with 8 slots and the loss 13 us,
+// 2.7 TB/s; 16384x128 FP32 normalised 5.3 us, 3.2 TB/s).
 template <int LT, int DT, int LPT, int V, int WIDE>
 __global__ void __launch_bounds__(256)
 router_backward(RouterBackArgs args)

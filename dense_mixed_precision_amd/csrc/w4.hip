@@ -103,18 +103,28 @@ const W4Entry kTable[] = {
 //     32x32 (256x1024x8192 16.1, 64x32 23.3);
 //   8 waves where each has 4 steps of K at least, else 4 (8x8192x8192 11.7
 //     against 13.3; 8x8192x1024 4.6 against 4.4);
-//   few rows a group are the reading of the weights: 4 waves, 8x32 up to 4
-//     rows a group, 16x32 up to 16 (64 rows over 64 experts of 2048x2048 25.3
-//     and 29.4; 64 over 8 of 4096x4096 25.0 and 21.8; 8 waves 33 to 55);
+//   past one round, up to 16 rows a group: 4 waves, 8x32 up to 4 rows a group,
+//     else 16x32 (64 rows over 64 experts of 2048x2048 25.3 and 29.4; 64 over 8 of
+//     4096x4096 25.0 and 21.8; 8 waves 33 to 55);
 //   128x256 tiles from 192 of them above 64 rows a group (1024x8192x8192 133,
-//     64x256 174; 512x8192x8192, 128 of them, 116 against 88; 1200 rows over 32
-//     experts of 2048x2048 39 against 53);
+//     64x256 174; 512x8192x8192, 128 of them, 116 against 88);
 //   64x256 from 160 (512x8192x8192 88, 64x128 95; 256x8192x8192, 128 of them, 85
 //     against 67);
 //   64x128, two workgroups a compute unit, from 192 (256x8192x8192 67, 64x32 89;
 //     128x8192x8192, 128 of them, 66 against 46);
 //   else 64x32.
 // The tiles take K in whole steps of 128 and K >= 128.
+//
+// Groups of 32 and 64 take the same entries, which a sweep of 1 to 1,024 rows by
+// 8192x8192 and of 8 to 1,024 by 4096x4096 bears out within 4% (64x4096x4096 in
+// groups of 32: 32x32 13.6, 64x32 20.6; 1024x8192x8192: 128x256 180, 64x256 238).
+// Where another entry is faster, in groups of 128 and alike in finer ones:
+//   a single matrix just past one round of its tile (us, taken and best):
+//     1x8224x8192 16.9 (4x16 14.4), 8x8224x8192 18.8 (8x32 17.0), 20x8224x8192
+//     44.3 (16x32 23.9, 32x32 32.6), 32x14336x8192 46.8 (16x32 32.6), 20x28672x8192
+//     68.1 (16x32 58.6);
+//   unequal groups of 17 to 64 rows on average: 1,200 rows over 32 experts of
+//     2048x2048 54.6 (128x256 39.2, 64x128 46.9).
 int select_w4(int64_t groups, int64_t M, int64_t N, int64_t K, int64_t lda)
 {
     const int64_t per = cdiv(M, groups);

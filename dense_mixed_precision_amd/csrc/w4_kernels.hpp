@@ -102,7 +102,10 @@ __device__ __forceinline__ u32x4 deal_codes(u32x4 w)
 // so on: rows 0-3 and 12-15 of one part with rows 4-11 of the next.  Chunk c of a
 // row of tokens (16 of them) stands at c ^ (r % 16), and piece p of a row of codes
 // (four of them) at p ^ -(r / 4): the 16 lanes of a turn then have 16 different
-// places of 16 bytes in the banks' 256.
+// places of 16 bytes in the banks' 256.  Kernels of 4 or 8 tokens, whose operand
+// rows repeat, miss that for tokens: the two parts of a turn meet at 4 or 8 places,
+// in other rows (conflict cycles of those that read LDS: 39% at 4x16, 34% and 25%
+// at 8x32 with 8 and 4 waves; none with 16 tokens or more).
 __device__ __forceinline__ int piece_place(int p, int r) { return p ^ (-(r >> 2) & 3); }
 
 // ---- 16 bytes of a row that may end inside them --------------------------------
@@ -175,12 +178,15 @@ __device__ __forceinline__ void store_values(int type, void *C, int64_t at, int 
 // once more, about 0.1 us for 128 bytes of them, which a call of few microseconds
 // notices.
 //
-// Bound: for few tokens the codes' way from memory and their expansion together
-// (8x8192x8192 FP16 11.3 us, 3.1 TB/s of codes, vector units busy 48% of the
-// time a compute unit holds waves; 64 BF16 rows over 64 experts of 2048x2048, of
-// which they reach about 41, 25.5 us, 75%); for 32 to 64 the tokens, which every
-// compute unit reads whole (64x8192x8192 24.6 us: 1 MiB of tokens and 128 KiB of
-// codes a workgroup); for one small product the launch (1x4096x4096 5.9).
+// Bound: for few tokens the codes' way from memory and the vector work, half of it
+// their expansion (8x8192x8192 FP16 11.3-12.1 us, 2.9 TB/s of codes, vector units
+// busy 48% of the time a compute unit holds waves; 64 BF16 rows over 64 experts of
+// 2048x2048, of which they reach about 41, 25.5-27 us, 75%); for 32 to 64 the
+// tokens, which every compute unit reads whole (64x8192x8192 24.6-25.6 us: 1 MiB of
+// tokens and 128 KiB of codes a workgroup); for one small product the launch
+// (1x4096x4096 5.2-6.0).  With 4 waves the compiler keeps the matrix instructions'
+// sums in accumulation registers: a move a value before each joining (4 waves here
+// and in w4_tile; none with 8).
 template <int IN, int GS, int NA, int NF, int WAVES, int STAGES>
 __global__ void __launch_bounds__(64 * WAVES)
 w4_narrow(W4Args args)
