@@ -147,8 +147,9 @@ def router_backward(logits, ids, dlogits, dweights=None, normalize: bool = True,
 
     logits and dlogits (T x experts): float16, bfloat16 or float32 each,
     row-major.  ids (T x top_k): int32 or int64, contiguous; None without
-    dweights.  dweights: float32, T x top_k.  counts: int32, experts + 1 values,
-    summed over devices where tokens are spread.  dloss: float32, 1 value, or
+    dweights.  dweights: float32, T x top_k; what it holds at a pair without an
+    expert, or of one whose logit is -inf, is not used.  counts: int32, experts +
+    1 values, summed over devices where tokens are spread.  dloss: float32, 1 value, or
     None for 1."""
     if _ops.torch is None:
         _ops._with_torch()
